@@ -224,7 +224,8 @@ def _handles(s):
     h["type"], h["stride"] = types[s["dtype"]], s["q"].stride(0)
     h["cache"] = E.KvCache(s["k_cache"], s["v_cache"], s["k_scales"], s["v_scales"], s["k_cache"].shape[0],
                            s["kv_heads"], s["page"], s["head_dim"])
-    h["plan"] = E.KvBatch(s["page_table"], s["kv_len"], s["row_start"], s["batch"], s["pages_of"], s["rows"])
+    h["plan"] = E.KvBatch(s["page_table"], s["kv_len"], s["row_start"], s["batch"], s["pages_of"], s["rows"],
+                          s["n_max"])
     if s["op"] == "attention":
         h["attn"] = E.Attention()
     else:
