@@ -19,6 +19,11 @@ LIB_PATH = os.path.join(_PKG, "libengram.so")
 ENGRAM_FMT_FP8 = 0
 ENGRAM_FMT_Q2K = 1
 ENGRAM_FMT_FP8_E8M0 = 2
+ENGRAM_FMT_BF16 = 3
+
+ENGRAM_T_BF16 = 0
+ENGRAM_T_F16 = 1
+ENGRAM_T_F32 = 2
 
 
 class EngramError(RuntimeError):
@@ -39,6 +44,23 @@ class engram_layer(ctypes.Structure):
                 ("rows", ctypes.c_int64), ("fmt", ctypes.c_int32),
                 ("wkv", ctypes.c_void_p), ("qk", ctypes.c_void_p), ("wkv_q2k", ctypes.c_void_p),
                 ("wkv_tiled", ctypes.c_void_p)]
+
+
+class engram_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("n_kv_heads", ctypes.c_int32), ("page_tokens", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class engram_kv_batch(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("row_start", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("rows", ctypes.c_int32), ("max_rows", ctypes.c_int32)]
+
+
+class engram_rope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_int64), ("dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
 
 
 _lib = None
@@ -88,6 +110,13 @@ def lib() -> ctypes.CDLL:
             "engram_workspace_layout": ([ctypes.POINTER(engram_geom), i64, ctypes.POINTER(sz)],
                                         ctypes.c_int),
             "engram_set_profile_events": ([P, i32], ctypes.c_int),
+            "engram_residual_norm": ([P, i32, i64, P, i32, i64, P, P, i32, i32, ctypes.c_float, i32, i32, P, P,
+                                      st], ctypes.c_int),
+            "engram_kv_append": ([P, P, i32, P, i64, P, i64, P, i64, P, i64, i32, P, st], ctypes.c_int),
+            "engram_attn_create": ([ctypes.POINTER(ctypes.c_void_p)], ctypes.c_int),
+            "engram_attn_reset": ([P, st], ctypes.c_int),
+            "engram_attn_destroy": ([P], None),
+            "engram_attention": ([P, P, P, i32, P, i64, i32, ctypes.c_float, i32, P, i64, P, st], ctypes.c_int),
             "engram_check": ([st], ctypes.c_int),
             "engram_strerror": ([ctypes.c_int], ctypes.c_char_p),
         }
@@ -313,6 +342,81 @@ def engram_workspace_layout(geom: engram_geom, tokens: int) -> list:
     off = (ctypes.c_size_t * (2 + 2 * geom.n_layers))()
     _ok(lib().engram_workspace_layout(ctypes.byref(geom), int(tokens), off), "engram_workspace_layout")
     return list(off)
+
+
+# ---- attention sub-layer ---------------------------------------------------
+
+class KvCache:
+    """An `engram_kv_cache` descriptor; keeps its tensors alive."""
+
+    def __init__(self, d_k, d_v, d_k_scales, d_v_scales, n_pages, n_kv_heads, page_tokens, head_dim, page_stride=0):
+        self._keep = (d_k, d_v, d_k_scales, d_v_scales)
+        self.desc = engram_kv_cache(*(_ptr(t).value for t in self._keep), int(n_pages), int(page_stride),
+                                    int(n_kv_heads), int(page_tokens), int(head_dim))
+        self.ref = ctypes.addressof(self.desc)
+
+
+class KvBatch:
+    """An `engram_kv_batch` descriptor; keeps its device arrays alive."""
+
+    def __init__(self, d_page_table, d_kv_len, d_row_start, batch, max_pages, rows, max_rows, table_stride=0):
+        self._keep = (d_page_table, d_kv_len, d_row_start)
+        self.desc = engram_kv_batch(*(_ptr(t).value for t in self._keep), int(table_stride), int(batch),
+                                    int(max_pages), int(rows), int(max_rows))
+        self.ref = ctypes.addressof(self.desc)
+
+
+class Rope:
+    """An `engram_rope` descriptor; keeps its table alive."""
+
+    def __init__(self, d_table, positions, dim, interleaved=False):
+        self._keep = d_table
+        self.desc = engram_rope(_ptr(d_table).value, int(positions), int(dim), int(interleaved))
+        self.ref = ctypes.addressof(self.desc)
+
+
+class Attention:
+    """The attention's workspace (`engram_attn_create`)."""
+
+    def __init__(self):
+        h = ctypes.c_void_p()
+        _ok(lib().engram_attn_create(ctypes.byref(h)), "engram_attn_create")
+        self.handle = h
+
+    def close(self):
+        if self.handle:
+            lib().engram_attn_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def engram_residual_norm(d_x, x_type, d_res, res_type, d_res_out, d_weight, rows, dim, eps, out_fmt, scale_block,
+                         d_out, d_scales, x_stride=0, res_stride=0, stream=None):
+    _ok(lib().engram_residual_norm(_ptr(d_x), x_type, x_stride, _ptr(d_res), res_type, res_stride, _ptr(d_res_out),
+                                   _ptr(d_weight), rows, dim, eps, out_fmt, scale_block, _ptr(d_out),
+                                   _ptr(d_scales), _stream(stream)), "engram_residual_norm")
+
+
+def engram_kv_append(cache: KvCache, batch: KvBatch, type, d_k, k_stride, d_v, v_stride, d_q, q_stride, d_q_out,
+                     q_out_stride, n_heads, rope: Rope = None, stream=None):
+    _ok(lib().engram_kv_append(cache.ref, batch.ref, type, _ptr(d_k), k_stride, _ptr(d_v), v_stride, _ptr(d_q),
+                               q_stride, _ptr(d_q_out), q_out_stride, n_heads, rope.ref if rope else None,
+                               _stream(stream)), "engram_kv_append")
+
+
+def engram_attn_reset(attn: Attention, stream=None):
+    _ok(lib().engram_attn_reset(attn.handle, _stream(stream)), "engram_attn_reset")
+
+
+def engram_attention(attn: Attention, cache: KvCache, batch: KvBatch, type, d_q, q_stride, n_heads, scale, window,
+                     d_out, out_stride, d_lse=None, stream=None):
+    _ok(lib().engram_attention(attn.handle, cache.ref, batch.ref, type, _ptr(d_q), q_stride, n_heads, scale, window,
+                               _ptr(d_out), out_stride, _ptr(d_lse), _stream(stream)), "engram_attention")
 
 
 def prepare_events(events) -> None:

@@ -64,6 +64,14 @@ int *err_ptr() {
     return g_err_ptr[dev];
 }
 
+}  // namespace
+
+namespace engram {
+int *error_word() { return err_ptr(); }
+}  // namespace engram
+
+namespace {
+
 inline cudaStream_t S(uintptr_t s) { return reinterpret_cast<cudaStream_t>(s); }
 inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -137,6 +145,8 @@ const char *engram_strerror(int code) {
         case ENGRAM_E_TIMEOUT: return "a bounded device wait gave up";
         case ENGRAM_E_UNSUPPORTED: return "shape outside what the kernels handle";
         case ENGRAM_E_NOALLOC_LIMIT: return "request larger than the fixed scratch of engram_forward_noalloc";
+        case ENGRAM_E_PAGE: return "a page id outside the key/value cache";
+        case ENGRAM_E_LENGTH: return "row_start or kv_len does not fit the call";
         default: return "unknown engram error";
     }
 }

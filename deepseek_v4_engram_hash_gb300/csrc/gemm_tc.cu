@@ -253,6 +253,19 @@ bool make_map(CUtensorMap *map, const void *ptr, uint64_t inner, uint64_t outer,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_map_u8_4d(CUtensorMap *map, const void *ptr, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
+                    uint32_t box1) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
+    const cuuint64_t st[3] = {strides[0], strides[1], strides[2]};
+    const cuuint32_t box[4] = {(cuuint32_t)dims[0], box1, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(ptr), d, st, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, dims[0] == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool have_tensor_maps() { return encode_fn() != nullptr; }
 
 }  // namespace tcg

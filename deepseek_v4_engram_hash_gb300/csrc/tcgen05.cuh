@@ -84,6 +84,10 @@ inline int group_rows128(int m_tiles128) {
 // 2D bf16 tensor map over [outer, inner] (inner contiguous), box {BK, box_outer},
 // 128-byte swizzle; false if the driver entry point is missing or refuses.
 bool make_map(CUtensorMap *map, const void *ptr, uint64_t inner, uint64_t outer, uint32_t box_outer);
+// 4D byte tensor map (dims and byte strides innermost first; dims[0] 64 or 128,
+// the swizzle of that width), boxes {dims[0], box1, 1, 1}.
+bool make_map_u8_4d(CUtensorMap *map, const void *ptr, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
+                    uint32_t box1);
 bool have_tensor_maps();
 
 }  // namespace tcg

@@ -61,10 +61,18 @@ extern "C" {
 #define ENGRAM_E_TIMEOUT -10    /* device: a bounded wait gave up */
 #define ENGRAM_E_UNSUPPORTED -11 /* shape outside what the kernels handle */
 #define ENGRAM_E_NOALLOC_LIMIT -12 /* request larger than engram_forward_noalloc's fixed scratch */
+#define ENGRAM_E_PAGE -13       /* device: a page id outside the cache */
+#define ENGRAM_E_LENGTH -14     /* device: row_start or kv_len does not fit the call */
 
 #define ENGRAM_FMT_FP8 0        /* e4m3 codes [rows, head_dim] + f32 scales [rows, head_dim / scale_block] */
 #define ENGRAM_FMT_Q2K 1        /* 84-byte Q2_K super-blocks [rows, 84]; head_dim must be 256 */
 #define ENGRAM_FMT_FP8_E8M0 2   /* e4m3 codes [rows, head_dim] + one-byte e8m0 scales [rows, head_dim / scale_block] */
+#define ENGRAM_FMT_BF16 3       /* plain bf16, no scales (outputs of engram_residual_norm) */
+
+/* Element types of the attention sub-layer's inputs and outputs. */
+#define ENGRAM_T_BF16 0
+#define ENGRAM_T_F16 1
+#define ENGRAM_T_F32 2
 
 /* Geometry.  C = (max_ngram - 1) * n_heads, K = C * head_dim, N = dim * (hc + 1).
  * Limits: 1 <= n_layers <= 4; 2 <= max_ngram <= 16; n_heads >= 1;
@@ -330,6 +338,131 @@ int engram_check(uintptr_t stream);
  * ENGRAM_E_TIMEOUT in the error word (read by engram_check) and returns, and
  * the device stays usable.  ENGRAM_E_INVALID for a limit out of range. */
 int engram_selftest_wait_timeout(int32_t limit_us, uintptr_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The attention sub-layer behind the engram: norm, cache append, attention.
+ * (The pages have no counterpart: these entry points belong to this library's
+ * ABI.)  The projections between them are engram_project.
+ *
+ * 8-bit blocks.  A block of values is held as e4m3 codes with one power-of-two
+ * scale: the smallest 2^e, e >= -126, with amax <= 448 * 2^e;
+ * code = e4m3_rne(value / 2^e).  A block that holds an infinity or a NaN has a
+ * NaN scale (e8m0 byte 255) and zero codes: all its values read as NaN.
+ * ------------------------------------------------------------------------- */
+
+/* Residual addition and root-mean-square norm, per row:
+ *   r = res + x (f32);  res_out = r in res_type;
+ *   y = r * rsqrt(mean(r^2) + eps) * weight.
+ *   d_x [rows, dim] x_type, rows x_stride elements apart (0 = dim), or NULL:
+ *     r = res;
+ *   d_res [rows, dim], d_res_out [rows, dim], res_type ENGRAM_T_F32 or
+ *     ENGRAM_T_BF16, rows res_stride elements apart (0 = dim); d_res_out may be
+ *     d_res itself (in place) or NULL (not written);
+ *   d_weight [dim] f32, or NULL: ones;
+ *   out_fmt ENGRAM_FMT_BF16: d_out [rows, dim] bf16, scale_block and d_scales
+ *     unused; ENGRAM_FMT_FP8 / ENGRAM_FMT_FP8_E8M0: d_out [rows, dim] codes,
+ *     d_scales [rows, dim / scale_block] f32 / e8m0 bytes -- the layout of an
+ *     engram table, so engram_rows_fp8 / engram_rows_fp8_e8m0 read it.
+ * The statistics and y are held in f32 (y is taken from the unrounded r).
+ * Limits: dim % 8 == 0, dim <= 16384; strides multiples of 8, >= dim;
+ * scale_block % 16 == 0 and divides dim; tensors 16-byte aligned (f32 scales 4,
+ * e8m0 bytes 1).  rows = 0 is a no-op.  d_out must not overlap the inputs. */
+int engram_residual_norm(const void *d_x, int32_t x_type, int64_t x_stride, const void *d_res, int32_t res_type,
+                         int64_t res_stride, void *d_res_out, const float *d_weight, int32_t rows, int32_t dim,
+                         float eps, int32_t out_fmt, int32_t scale_block, void *d_out, void *d_scales,
+                         uintptr_t stream);
+
+/* A paged key/value cache in 8 bits.  k, v: e4m3 codes [n_pages, n_kv_heads,
+ * page_tokens, head_dim], 16-byte aligned, pages page_stride bytes apart (0 =
+ * dense; else a multiple of 16); k_scales, v_scales: e8m0 bytes [n_pages,
+ * n_kv_heads], one a page and head (a block is page_tokens x head_dim values).
+ * head_dim 64 or 128; page_tokens 16, 32, 64 or 128; 1 <= n_kv_heads <= 1024;
+ * 1 <= n_pages < 2^31. */
+typedef struct {
+    uint8_t *k, *v, *k_scales, *v_scales;
+    int64_t n_pages, page_stride;
+    int32_t n_kv_heads, page_tokens, head_dim;
+} engram_kv_cache;
+
+/* The sequences of one call.  Sequence b has the rows row_start[b] ..
+ * row_start[b + 1] - 1 of the call's tensors (row_start NULL: rows / batch
+ * each) and, this call's tokens included, kv_len[b] tokens: its n rows are the
+ * positions kv_len[b] - n .. kv_len[b] - 1.  Token p of it lies in page
+ * page_table[b * table_stride + p / page_tokens] at slot p % page_tokens.
+ * Rows whose position is negative (kv_len[b] < n: the idle slots of a padded
+ * batch) are empty.  max_rows: no sequence has more rows than that.
+ * Device arrays, read when the kernels run, so a captured call sees their new
+ * contents.  A sequence whose row_start leaves 0..rows, falls, or holds more
+ * than max_rows, or whose kv_len is negative or over max_pages * page_tokens,
+ * raises ENGRAM_E_LENGTH and counts as one without rows (row_start) or without
+ * tokens (kv_len); a page id outside the cache raises ENGRAM_E_PAGE and its
+ * tokens are neither written nor seen.  table_stride 0 = max_pages.
+ * 1 <= batch <= 8192. */
+typedef struct {
+    const int32_t *page_table, *kv_len, *row_start;
+    int64_t table_stride;
+    int32_t batch, max_pages, rows, max_rows;
+} engram_kv_batch;
+
+/* Position rotation: table [positions, dim / 2] (cos, sin) f32 pairs, 16-byte
+ * aligned; element i of the first dim elements of a head is paired with i +
+ * dim / 2 (interleaved 0) or 2i with 2i + 1 (interleaved 1):
+ * (a, b) -> (a cos - b sin, b cos + a sin), in f32.  dim % 16 == 0, dim <= head_dim. */
+typedef struct {
+    const float *table;
+    int64_t positions;
+    int32_t dim, interleaved;
+} engram_rope;
+
+/* Appends the call's keys and values to the cache, rotating keys (and queries,
+ * when d_q is given) by their positions on the way:
+ *   d_k, d_v [rows, n_kv_heads * head_dim], rows k_stride / v_stride elements
+ *   apart (0 = dense); d_q, d_q_out [rows, n_heads * head_dim] likewise; all of
+ *   element type `type` (bf16, f16 or f32), rows 16-byte aligned (strides
+ *   multiples of 8).  d_q_out may be d_q itself with the same stride.  rope
+ *   NULL: no rotation.
+ * A (page, head) block keeps one scale: a page's first token sets it, later ones
+ * raise it when they need more, and the block's earlier codes are then encoded
+ * again at the new scale (e4m3_rne(code * 2^(old - new))).  What a page held
+ * before its first token does not count.
+ * A page that several sequences share must not be appended to.  Empty rows
+ * (see engram_kv_batch) store nothing and leave zeros in d_q_out.  A sequence
+ * whose kv_len exceeds the rotation table raises ENGRAM_E_LENGTH and counts as
+ * one without tokens. */
+int engram_kv_append(const engram_kv_cache *cache, const engram_kv_batch *batch, int32_t type, const void *d_k,
+                     int64_t k_stride, const void *d_v, int64_t v_stride, const void *d_q, int64_t q_stride,
+                     void *d_q_out, int64_t q_out_stride, int32_t n_heads, const engram_rope *rope,
+                     uintptr_t stream);
+
+/* The attention's workspace on the current device: partial results of the
+ * splits along the cache and their arrival counters (zero between calls).  Its size
+ * does not depend on the calls it serves.  One call at a time on a workspace:
+ * calls that may overlap on the GPU need one each. */
+typedef struct engram_attn engram_attn;
+int engram_attn_create(engram_attn **out);
+/* Zeroes the counters (enqueued on `stream`); after ENGRAM_E_TIMEOUT they may not be. */
+int engram_attn_reset(engram_attn *a, uintptr_t stream);
+void engram_attn_destroy(engram_attn *a);
+
+/* Causal attention of the call's rows over the cache (which holds their own keys
+ * and values already):
+ *   the row at position p of query head h sees the tokens j of its sequence with
+ *   max(0, p - window + 1) <= j <= p (window 0: from 0), through key/value head
+ *   h / (n_heads / n_kv_heads):
+ *     s_j = scale <q, k_j>;  out = sum_j softmax(s)_j v_j;  lse = ln sum_j exp(s_j).
+ *   d_q [rows, n_heads * head_dim], rows q_stride elements apart (0 = dense), type
+ *   bf16 or f16; d_out the same with out_stride; d_lse [rows, n_heads] f32 or NULL.
+ *   Rows that see nothing: out = 0, lse = -inf.
+ * Scores, statistics and sums are f32; q is brought to f16 by a power of two
+ * per row and head (f16 products of codes are exact); the probabilities are
+ * rounded to f16 for the product with v.  A value block whose scale is under
+ * 2^-66 counts as zeros.  Codes 127 and 255 (NaN) are not allowed at positions
+ * below kv_len; the cache may hold anything elsewhere.
+ * n_heads a multiple of n_kv_heads; scale finite; window >= 0; strides multiples of 8,
+ * tensors 16-byte aligned. */
+int engram_attention(engram_attn *a, const engram_kv_cache *cache, const engram_kv_batch *batch, int32_t type,
+                     const void *d_q, int64_t q_stride, int32_t n_heads, float scale, int32_t window, void *d_out,
+                     int64_t out_stride, float *d_lse, uintptr_t stream);
 
 const char *engram_strerror(int code);
 
