@@ -405,10 +405,18 @@ cudaError_t launch_few(const AttnArgs &a, cudaStream_t s) {
 
 }  // namespace
 
-size_t attn_part_floats(int sms) { return (size_t)sms * kCtasPerSm * 2 * Few<128>::kPart; }
-size_t attn_counters(int sms) { return (size_t)sms * kCtasPerSm; }
+size_t attn_part_floats(int sms) {
+    const size_t few = (size_t)sms * kCtasPerSm * 2 * Few<128>::kPart, tile = attn_tile_part_floats(sms);
+    return few > tile ? few : tile;
+}
+size_t attn_counters(int sms) {
+    const size_t few = (size_t)sms * kCtasPerSm, tile = attn_tile_counters(sms);
+    return few > tile ? few : tile;
+}
 
 cudaError_t launch_attention(const AttnArgs &a, cudaStream_t s) {
+    // rows of one key/value head and sequence: up to one 16-row mma tile, or the tensor cores' 128-row tiles
+    if ((int64_t)a.c.max_rows * a.group > kRows) return launch_attn_tile(a, s);
     const bool bf = a.type == ENGRAM_T_BF16;
     if (a.c.D == 128) return bf ? launch_few<ENGRAM_T_BF16, 128>(a, s) : launch_few<ENGRAM_T_F16, 128>(a, s);
     return bf ? launch_few<ENGRAM_T_BF16, 64>(a, s) : launch_few<ENGRAM_T_F16, 64>(a, s);

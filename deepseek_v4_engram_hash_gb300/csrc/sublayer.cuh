@@ -180,5 +180,9 @@ struct AttnArgs {
     int32_t sms;
 };
 cudaError_t launch_attention(const AttnArgs &a, cudaStream_t s);
+// The same on tensor-core tiles (attn_tile.cu), and what it takes of the workspace.
+cudaError_t launch_attn_tile(const AttnArgs &a, cudaStream_t s);
+size_t attn_tile_part_floats(int sms);
+size_t attn_tile_counters(int sms);
 
 }  // namespace engram
