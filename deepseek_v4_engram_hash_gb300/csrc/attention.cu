@@ -1,6 +1,6 @@
 // attention.cu -- causal attention over the paged 8-bit cache (engram_attention)
-// for up to 16 query rows a key/value head and tile (rows = new tokens x query
-// heads that share the head): single tokens and short chunks.
+// for up to 16 query rows a key/value head (rows = new tokens x query heads that
+// share the head): single tokens and a few tokens at once.
 //
 // Mathematics.  With a power-of-two scale 2^ek, 2^ev a (page, head) block and
 // codes kc, vc, the scores in log2 units are s_j = <q, kc_j> 2^ek scale log2(e),
@@ -11,14 +11,17 @@
 // the scales.  M moves (and the sums are rescaled) only when a t exceeds it by more
 // than 8: until then p <= 2^8, which f16 and the f32 sums hold.
 //
-// Bound by the cache's bytes.  A CTA takes a contiguous range of the call's
-// (sequence, head, row tile, 64-token tile) list, cut evenly over the grid, so any
-// mix of lengths keeps every SM busy; ranges that cut a list entry leave partial results,
-// which the last CTA to arrive joins in a fixed order.  Inside a CTA each warp
-// streams its own 16-token units through a private ring of TMA copies (one
-// thread issues, the warp itself consumes: no barrier between warps), turns codes
-// into f16 mma operands in registers (e4m3 to f16 is exact) and keeps its own
-// softmax state; four warps join through shared memory at the end of an entry.
+// Bound by the cache's bytes, so what counts is instructions a byte.  The tokens are
+// the M side of both products (m16n8k16 with f16 operands: S^T = K Q^T and
+// O^T = V^T P^T), 8 query rows the N side: one mma covers 16 tokens x 8 rows, and
+// codes become operands in registers (e4m3 to f16 is exact) once for all rows.
+// A CTA takes a contiguous range of the call's (sequence, head, 64-token tile) list,
+// cut evenly over the grid, so any mix of lengths keeps every SM busy; ranges that
+// cut an entry leave partial results, which the last CTA to arrive joins in
+// CTA order.  Inside a CTA each warp streams its own 16-token units through a
+// private ring of TMA copies (one thread issues, the warp itself consumes: no
+// barrier between warps) and keeps its own softmax state; four warps join through
+// shared memory at the end of an entry.
 #include "attn.cuh"
 
 namespace engram {
@@ -30,8 +33,9 @@ using namespace attn;
 constexpr int kWarps = 4;
 constexpr int kUnit = 16;                            // tokens a copy
 constexpr int kTile = kUnit * kWarps;                // tokens a CTA step
-constexpr int kRows = 16;
-constexpr int kCtasPerSm = 3;
+constexpr int kMaxRows = 16;
+constexpr int kMinTiles = 2;                         // tiles a CTA takes at least
+constexpr int kCtasPerSm = 4;                        // 3 with 16 rows (registers)
 constexpr uint32_t kNever = 0x7FFFFFFF;
 
 struct FewParams {
@@ -41,12 +45,12 @@ struct FewParams {
 
 template <int D>
 struct Few {
-    static constexpr int kStages = 512 / D;          // 16 KB a warp
+    static constexpr int kStages = 384 / D;          // 12 KB a warp
     static constexpr int kHalf = kUnit * D;          // bytes of a unit's keys (or values)
     static constexpr int kRing = kStages * 2 * kHalf;
     static constexpr int kRegion = kWarps * kRing;
     static constexpr size_t kSmem = 1024 + kRegion + 1024;
-    static constexpr int kPart = kRows * (D + 2);    // floats of a partial result
+    static constexpr int kPart = kMaxRows * (D + 2); // floats of a partial result
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -57,35 +61,38 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// List entries of a sequence: row tiles x heads, each of `tiles` 64-token tiles from token lo.
+// The transpose of an 8 x 8 matrix of f16 held two a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// A sequence's entries, one a head, each of `tiles` 64-token tiles from token lo.
 struct Plan {
     Seq s;
-    int lo, tiles, row_tiles;
+    int lo, tiles;
 };
 __device__ __forceinline__ Plan plan_of(const AttnArgs &a, int b) {
     Plan p;
     p.s = sequence(a.c, b);
-    p.row_tiles = (p.s.n * a.group + kRows - 1) / kRows;
     p.lo = a.window ? max(0, p.s.kv - p.s.n - a.window + 1) / kTile * kTile : 0;
-    p.tiles = max(1, (p.s.kv - p.lo + kTile - 1) / kTile);
+    p.tiles = p.s.n == 0 ? 0 : max(1, (p.s.kv - p.lo + kTile - 1) / kTile);
     return p;
 }
-__device__ __forceinline__ int64_t tiles_of(const AttnArgs &a, int b) {
-    const Plan p = plan_of(a, b);
-    return (int64_t)p.row_tiles * a.c.KH * p.tiles;
-}
 
-template <int TYPE, int D>
-__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_few_kernel(const __grid_constant__ FewParams p) {
+// NT: groups of 8 query rows.
+template <int TYPE, int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm + 1 - NT) attn_few_kernel(const __grid_constant__ FewParams p) {
     using F = Few<D>;
-    constexpr int KS = D / 16;                       // mma k steps of q k, and n tiles of p v over 2
+    constexpr int KS = D / 16;                       // k steps of K Q^T, and 16-dim tiles of V^T P^T
     extern __shared__ uint8_t smem_raw[];
     const AttnArgs &a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q4 = lane & 3;
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (base - raw);
     const uint32_t ring = base + warp * F::kRing;
-    float *stat = reinterpret_cast<float *>(smem + F::kRegion);          // [2][kWarps][kRows]
+    float *stat = reinterpret_cast<float *>(smem + F::kRegion);          // [2][kWarps][kMaxRows]
     const uint32_t bars = smem_u32(smem + F::kRegion + 512) + warp * F::kStages * 8;
     int *flags = reinterpret_cast<int *>(smem + F::kRegion + 512 + kWarps * F::kStages * 8);
     volatile int *abort_flag = flags;
@@ -102,7 +109,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_few_kernel(const
     int64_t mine = 0;
     for (int j = 0; j < lanes_per; ++j) {
         const int b = lane * lanes_per + j;
-        if (b < a.c.batch) mine += tiles_of(a, b);
+        if (b < a.c.batch) mine += (int64_t)plan_of(a, b).tiles * a.c.KH;
     }
     int64_t upto = mine;
 #pragma unroll
@@ -111,7 +118,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_few_kernel(const
         if (lane >= o) upto += x;
     }
     const int64_t total = __shfl_sync(0xFFFFFFFFu, upto, 31);
-    const int64_t per = max((int64_t)1, (total + gridDim.x - 1) / gridDim.x);
+    const int64_t per = max((int64_t)kMinTiles, (total + gridDim.x - 1) / gridDim.x);
     int64_t t = blockIdx.x * per;
     const int64_t end = min(total, t + per);
     if (t >= end) return;
@@ -119,26 +126,23 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_few_kernel(const
     int b = owner * lanes_per;
     int64_t before = __shfl_sync(0xFFFFFFFFu, upto - mine, owner);
     Plan pl = plan_of(a, b);
-    int64_t mine_b = (int64_t)pl.row_tiles * a.c.KH * pl.tiles;
 
     uint32_t phase = 0;                              // parity of each stage's next wait
     int stage = 0;
     while (t < end) {
-        while (t >= before + mine_b && b + 1 < a.c.batch) {
-            before += mine_b;
+        while (t >= before + (int64_t)pl.tiles * a.c.KH && b + 1 < a.c.batch) {
+            before += (int64_t)pl.tiles * a.c.KH;
             pl = plan_of(a, ++b);
-            mine_b = (int64_t)pl.row_tiles * a.c.KH * pl.tiles;
         }
         const int64_t rel = t - before;
-        const int entry = (int)(rel / pl.tiles), tile0 = (int)(rel % pl.tiles);
+        const int head = (int)(rel / pl.tiles), tile0 = (int)(rel % pl.tiles);
         const int count = (int)min((int64_t)(pl.tiles - tile0), end - t);
-        const int head = entry / pl.row_tiles, r0 = entry % pl.row_tiles * kRows;
         const int64_t entry_t0 = t - tile0;
         t += count;
 
         const int tok0 = pl.lo + tile0 * kTile + warp * kUnit, tok1 = min(pl.s.kv, pl.lo + (tile0 + count) * kTile);
         const int units = tok0 < tok1 ? (tok1 - tok0 + kTile - 1) / kTile : 0;
-        const int n_rows = min(kRows, pl.s.n * a.group - r0);
+        const int n_rows = min(8 * NT, pl.s.n * a.group);
 
         // pages and scales of 32 units at a time, one a lane: id, key byte | value byte << 8
         auto load_id = [&](int k) {
@@ -166,18 +170,15 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_few_kernel(const
         for (int u = 0; u < min(units, F::kStages); ++u) issue(u, 0);
         uint32_t sc_cur = load_scales(id_cur), sc_next = 0;
 
-        // queries of rows g and g + 8, the thread's D / 4 dims, as f16 of about 1
-        uint32_t qa[KS][4];
-        float kf[2];
-        int lim[2], low[2];
+        // query row 8 nt + g, the lane's D / 4 dims, as f16 of about 1; bounds and factors of rows 8 nt + 2 q4 + e
+        uint32_t qb[NT][KS][2];
+        float kf[NT][2];
+        int lim[NT][2], low[NT][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = r0 + g + 8 * h;
-            const bool live = g + 8 * h < n_rows;
-            const int i = r / a.group, pos = pl.s.kv - pl.s.n + i;
-            lim[h] = live ? pos + 1 : (int)kNever;
-            low[h] = live && a.window ? pos - a.window + 1 : 0;
-            const int64_t at = (int64_t)(pl.s.row0 + i) * a.q_stride + (int64_t)(head * a.group + r % a.group) * D + q4 * (D / 4);
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = 8 * nt + g;
+            const bool live = r < n_rows;
+            const int64_t at = (int64_t)(pl.s.row0 + r / a.group) * a.q_stride + (int64_t)(head * a.group + r % a.group) * D + q4 * (D / 4);
             float x[D / 4];
             uint32_t m = 0;
 #pragma unroll
@@ -192,20 +193,29 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_few_kernel(const
             }
             m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
             m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-            float down;
-            q_scale(m, a.scale_log2, down, kf[h]);
+            float down, f;
+            q_scale(m, a.scale_log2, down, f);
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-                qa[k][h] = pack_f16x2(x[4 * k] * down, x[4 * k + 1] * down);
-                qa[k][2 + h] = pack_f16x2(x[4 * k + 2] * down, x[4 * k + 3] * down);
+                qb[nt][k][0] = pack_f16x2(x[4 * k] * down, x[4 * k + 1] * down);
+                qb[nt][k][1] = pack_f16x2(x[4 * k + 2] * down, x[4 * k + 3] * down);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                kf[nt][e] = __shfl_sync(0xFFFFFFFFu, f, 4 * (2 * q4 + e));
+                const int row = 8 * nt + 2 * q4 + e, pos = pl.s.kv - pl.s.n + row / a.group;
+                lim[nt][e] = row < n_rows ? pos + 1 : (int)kNever;
+                low[nt][e] = row < n_rows && a.window ? pos - a.window + 1 : 0;
             }
         }
-        // tokens that every row of the tile sees
-        const int first_pos = pl.s.kv - pl.s.n + r0 / a.group, last_pos = pl.s.kv - pl.s.n + (r0 + n_rows - 1) / a.group;
+        // tokens that every row sees
+        const int first_pos = pl.s.kv - pl.s.n, last_pos = first_pos + (n_rows - 1) / a.group;
         const int all_lo = a.window ? last_pos - a.window + 1 : 0, all_hi = first_pos + 1;
 
-        float o[2 * KS][4] = {};
-        float M[2] = {-INFINITY, -INFINITY}, L[2] = {};
+        float o[NT][KS][4] = {};
+        float M[NT][2], L[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) M[nt][0] = M[nt][1] = -INFINITY, L[nt][0] = L[nt][1] = 0.f;
 #pragma unroll 1
         for (int u = 0; u < units; ++u) {
             const int tb = tok0 + u * kTile;
@@ -215,7 +225,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_few_kernel(const
                 id_next = load_id((u >> 5) + 1);
             }
             if ((u & 31) == 16) sc_next = load_scales(id_next);
-            const int st = (stage + u) % F::kStages;
+            const int st = stage;
+            stage = stage + 1 == F::kStages ? 0 : stage + 1;
             const bool here = wait_bar(bars + 8 * st, (phase >> st) & 1, abort_flag, a.c.err);
             phase ^= 1u << st;
             if (!__all_sync(0xFFFFFFFFu, here)) break;
@@ -223,105 +234,125 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_few_kernel(const
             const uint32_t sc = __shfl_sync(0xFFFFFFFFu, sc_cur, u & 31);
             const int id = __shfl_sync(0xFFFFFFFFu, id_cur, u & 31);
 
-            // scores: token n of the mma is row g of the unit's half; its dims go to the k slots in the order of qa
-            float s[2][4] = {};
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t w[KS];
-                load_k_row<D>(ks, 8 * j + g, q4, w);
-#pragma unroll
-                for (int k = 0; k < KS; ++k)
-                    mma16816(s[j], qa[k][0], qa[k][1], qa[k][2], qa[k][3], e4m3_lo(w[k]), e4m3_hi(w[k]));
-            }
-            const float ek = e8m0_to_f32(sc & 255u), ev = value_exp(sc >> 8);
-            const float c0 = kf[0] * ek, c1 = kf[1] * ek;
-            float tmax0 = -INFINITY, tmax1 = -INFINITY;
-            const bool whole = tb >= all_lo && tb + kUnit <= all_hi && id >= 0;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float t0 = fmaf(s[j][e], c0, ev), t1 = fmaf(s[j][2 + e], c1, ev);
-                    if (!whole) {
-                        const int tok = tb + 8 * j + 2 * q4 + e;
-                        if (tok >= lim[0] || tok < low[0] || id < 0) t0 = -INFINITY;
-                        if (tok >= lim[1] || tok < low[1] || id < 0) t1 = -INFINITY;
-                    }
-                    s[j][e] = t0, s[j][2 + e] = t1;
-                    tmax0 = fmaxf(tmax0, t0), tmax1 = fmaxf(tmax1, t1);
-                }
-            if (__any_sync(0xFFFFFFFFu, tmax0 > M[0] + kLazy || tmax1 > M[1] + kLazy)) {
-                tmax0 = fmaxf(tmax0, __shfl_xor_sync(0xFFFFFFFFu, tmax0, 1));
-                tmax1 = fmaxf(tmax1, __shfl_xor_sync(0xFFFFFFFFu, tmax1, 1));
-                tmax0 = fmaxf(tmax0, __shfl_xor_sync(0xFFFFFFFFu, tmax0, 2));
-                tmax1 = fmaxf(tmax1, __shfl_xor_sync(0xFFFFFFFFu, tmax1, 2));
-                const float n0 = fmaxf(M[0], tmax0), n1 = fmaxf(M[1], tmax1);
-                const float f0 = M[0] == n0 ? 1.f : exp2_approx(M[0] - n0), f1 = M[1] == n1 ? 1.f : exp2_approx(M[1] - n1);
-                M[0] = n0, M[1] = n1;
-                L[0] *= f0, L[1] *= f1;
-#pragma unroll
-                for (int k = 0; k < 2 * KS; ++k) {
-                    o[k][0] *= f0, o[k][1] *= f0;
-                    o[k][2] *= f1, o[k][3] *= f1;
-                }
-            }
-            const float m0 = M[0] == -INFINITY ? 0.f : M[0], m1 = M[1] == -INFINITY ? 0.f : M[1];
-            const float back = value_unscale(sc >> 8);
-            uint32_t pa[4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float x0 = exp2_approx(s[j][0] - m0), x1 = exp2_approx(s[j][1] - m0);
-                const float y0 = exp2_approx(s[j][2] - m1), y1 = exp2_approx(s[j][3] - m1);
-                L[0] = fmaf(x0 + x1, back, L[0]);
-                L[1] = fmaf(y0 + y1, back, L[1]);
-                pa[2 * j] = pack_f16x2(x0, x1);
-                pa[2 * j + 1] = pack_f16x2(y0, y1);
-            }
-            // out: k slots are the unit's tokens 2q, 2q + 1 (and + 8), n = g the dims D / 8 g + j of n tile j
+            // scores of tokens g and g + 8 (mma rows) and rows 2 q4, 2 q4 + 1; dims go to the k slots in the order of qb
+            float s[NT][4] = {};
             {
-                constexpr int VW = D / 32;                             // 32-bit words of a thread's dims
+                uint32_t w0[KS], w1[KS];
+                load_k_row<D>(ks, g, q4, w0);
+                load_k_row<D>(ks, g + 8, q4, w1);
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    const uint32_t a0 = e4m3_lo(w0[k]), a1 = e4m3_lo(w1[k]), a2 = e4m3_hi(w0[k]), a3 = e4m3_hi(w1[k]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], a0, a1, a2, a3, qb[nt][k][0], qb[nt][k][1]);
+                }
+            }
+            const float ek = e8m0_to_f32(sc & 255u), ev = value_exp(sc >> 8), back = value_unscale(sc >> 8);
+            const bool whole = tb >= all_lo && tb + kUnit <= all_hi && id >= 0;
+            bool over = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[nt][e] = fmaf(s[nt][e], kf[nt][e & 1] * ek, ev);
+            if (!whole) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int tok = tb + g + 8 * (e >> 1);
+                        if (tok >= lim[nt][e & 1] || tok < low[nt][e & 1] || id < 0) s[nt][e] = -INFINITY;
+                    }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) over |= fmaxf(s[nt][e], s[nt][2 + e]) > M[nt][e] + kLazy;
+            if (__any_sync(0xFFFFFFFFu, over)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float m = fmaxf(s[nt][e], s[nt][2 + e]);
+                        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+                        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+                        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+                        m = fmaxf(m, M[nt][e]);
+                        const float f = M[nt][e] == m ? 1.f : exp2_approx(M[nt][e] - m);
+                        M[nt][e] = m;
+                        L[nt][e] *= f;
+#pragma unroll
+                        for (int k = 0; k < KS; ++k) o[nt][k][e] *= f, o[nt][k][2 + e] *= f;
+                    }
+            }
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float m0 = M[nt][0] == -INFINITY ? 0.f : M[nt][0], m1 = M[nt][1] == -INFINITY ? 0.f : M[nt][1];
+                const float x0 = exp2_approx(s[nt][0] - m0), x1 = exp2_approx(s[nt][1] - m1);
+                const float y0 = exp2_approx(s[nt][2] - m0), y1 = exp2_approx(s[nt][3] - m1);
+                L[nt][0] = fmaf(x0 + y0, back, L[nt][0]);
+                L[nt][1] = fmaf(x1 + y1, back, L[nt][1]);
+                pb[nt][0] = transpose8(pack_f16x2(x0, x1));             // row g, tokens 2 q4, 2 q4 + 1
+                pb[nt][1] = transpose8(pack_f16x2(y0, y1));             // and those + 8
+            }
+            // out: mma rows g and g + 8 of tile i are the dims D / 8 g + 2 i and + 1, k slots the tokens 2 q4, 2 q4 + 1 (+ 8)
+            {
+                constexpr int VW = D / 32;                              // 32-bit words of a lane's dims
                 uint32_t v[4][VW];
-                const bool zero = (int)((sc >> 8) & 255u) < kLeastValueByte;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int tok = 2 * q4 + (r & 1) + 8 * (r >> 1);
-                    load_v_row<D>(vs, tok, g, v[r]);
-                    if (zero || tb + tok >= pl.s.kv)                   // nothing is written there, or it does not count
+                for (int r = 0; r < 4; ++r) load_v_row<D>(vs, 2 * q4 + (r & 1) + 8 * (r >> 1), g, v[r]);
+                if (tb + kUnit > pl.s.kv || (int)(sc >> 8) < kLeastValueByte) {
 #pragma unroll
-                        for (int i = 0; i < VW; ++i) v[r][i] = 0u;
+                    for (int r = 0; r < 4; ++r)
+                        if (tb + 2 * q4 + (r & 1) + 8 * (r >> 1) >= pl.s.kv || (int)(sc >> 8) < kLeastValueByte)
+#pragma unroll
+                            for (int i = 0; i < VW; ++i) v[r][i] = 0u;  // nothing is written there, or it does not count
                 }
 #pragma unroll
                 for (int i = 0; i < VW; ++i) {
                     const uint32_t a01 = __byte_perm(v[0][i], v[1][i], 0x5140), a23 = __byte_perm(v[0][i], v[1][i], 0x7362);
                     const uint32_t b01 = __byte_perm(v[2][i], v[3][i], 0x5140), b23 = __byte_perm(v[2][i], v[3][i], 0x7362);
-                    mma16816(o[4 * i + 0], pa[0], pa[1], pa[2], pa[3], e4m3_lo(a01), e4m3_lo(b01));
-                    mma16816(o[4 * i + 1], pa[0], pa[1], pa[2], pa[3], e4m3_hi(a01), e4m3_hi(b01));
-                    mma16816(o[4 * i + 2], pa[0], pa[1], pa[2], pa[3], e4m3_lo(a23), e4m3_lo(b23));
-                    mma16816(o[4 * i + 3], pa[0], pa[1], pa[2], pa[3], e4m3_hi(a23), e4m3_hi(b23));
+                    const uint32_t a0 = e4m3_lo(a01), a1 = e4m3_hi(a01), a2 = e4m3_lo(b01), a3 = e4m3_hi(b01);
+                    const uint32_t c0 = e4m3_lo(a23), c1 = e4m3_hi(a23), c2 = e4m3_lo(b23), c3 = e4m3_hi(b23);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma16816(o[nt][2 * i], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                        mma16816(o[nt][2 * i + 1], c0, c1, c2, c3, pb[nt][0], pb[nt][1]);
+                    }
                 }
             }
-            __syncwarp();                                              // the stage is read
-            if (u + F::kStages < units) issue(u + F::kStages, u >> 5);
+            __syncwarp();                                               // the stage is read
+            if (u + F::kStages < units) {
+                const int mine_id = ((u + F::kStages) >> 5) == (u >> 5) ? id_cur : id_next;
+                const int nid = __shfl_sync(0xFFFFFFFFu, mine_id, (u + F::kStages) & 31);
+                if (lane == 0) {
+                    const int tok = tb + F::kStages * kTile, at = tok & (a.c.pt - 1), page = nid < 0 ? a.c.n_pages : nid;
+                    mbar_expect_tx(bars + 8 * st, 2 * F::kHalf);
+                    tma_load_4d(ks, &p.mk, 0, at, head, page, bars + 8 * st);
+                    tma_load_4d(vs, &p.mv, 0, at, head, page, bars + 8 * st);
+                }
+            }
         }
-        stage = (stage + units) % F::kStages;
-        if (__syncthreads_or(*abort_flag)) break;                      // copies in flight are waited for below
+        if (__syncthreads_or(*abort_flag)) break;                       // copies in flight are waited for below
 
         // join the four warps: each leaves its sums in its own ring
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            L[h] += __shfl_xor_sync(0xFFFFFFFFu, L[h], 1);
-            L[h] += __shfl_xor_sync(0xFFFFFFFFu, L[h], 2);
-            const int r = g + 8 * h;
-            if (r >= n_rows) continue;
-            if (q4 == 0) stat[warp * kRows + r] = M[h], stat[(kWarps + warp) * kRows + r] = L[h];
-            float4 *dst = reinterpret_cast<float4 *>(smem + warp * F::kRing) + r * (D / 4);
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 2; ++c)                               // dims D/4 q + D/8 c + 0 .. D/8 - 1
+            for (int e = 0; e < 2; ++e) {
+                float l = L[nt][e];
+                l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
+                l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
+                l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+                const int r = 8 * nt + 2 * q4 + e;
+                if (r >= n_rows) continue;
+                if (g == 0) stat[warp * kMaxRows + r] = M[nt][e], stat[(kWarps + warp) * kMaxRows + r] = l;
+                float4 *dst = reinterpret_cast<float4 *>(smem + warp * F::kRing) + r * (D / 4);
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i)
-                    dst[swz(r, 2 * q4 * (D / 32) + c * (D / 32) + i)] =
-                        make_float4(o[4 * i][2 * h + c], o[4 * i + 1][2 * h + c], o[4 * i + 2][2 * h + c], o[4 * i + 3][2 * h + c]);
-        }
+                for (int i = 0; i < D / 32; ++i)                        // dims D / 8 g + 4 i ..
+                    dst[swz(r, g * (D / 32) + i)] =
+                        make_float4(o[nt][2 * i][e], o[nt][2 * i][2 + e], o[nt][2 * i + 1][e], o[nt][2 * i + 1][2 + e]);
+            }
         __syncthreads();
         const int64_t first_cta = entry_t0 / per, last_cta = (entry_t0 + pl.tiles - 1) / per;
         const bool alone = first_cta == last_cta;
@@ -330,21 +361,21 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_few_kernel(const
             const int r = i / (D / 4), d4 = i % (D / 4);
             float m = stat[r], l = 0.f;
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) m = fmaxf(m, stat[w * kRows + r]);
+            for (int w = 1; w < kWarps; ++w) m = fmaxf(m, stat[w * kMaxRows + r]);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float mw = stat[w * kRows + r], f = mw == -INFINITY ? 0.f : exp2_approx(mw - m);
-                if (mw == -INFINITY && stat[(kWarps + w) * kRows + r] == 0.f) continue;
+                const float mw = stat[w * kMaxRows + r], lw = stat[(kWarps + w) * kMaxRows + r];
+                const float f = mw == -INFINITY ? (lw == 0.f ? 0.f : 1.f) : exp2_approx(mw - m);
                 const float4 x = reinterpret_cast<const float4 *>(smem + w * F::kRing)[r * (D / 4) + swz(r, d4)];
-                l = fmaf(stat[(kWarps + w) * kRows + r], f, l);
+                l = fmaf(lw, f, l);
                 acc.x = fmaf(x.x, f, acc.x), acc.y = fmaf(x.y, f, acc.y), acc.z = fmaf(x.z, f, acc.z), acc.w = fmaf(x.w, f, acc.w);
             }
             if (alone) {
-                store_row4<TYPE, D>(a, pl.s.row0, head, r0 + r, d4, acc, m, l);
+                store_row4<TYPE, D>(a, pl.s.row0, head, r, d4, acc, m, l);
             } else {
                 reinterpret_cast<float4 *>(part)[i] = acc;
-                if (d4 == 0) part[kRows * D + r] = m, part[kRows * D + kRows + r] = l;
+                if (d4 == 0) part[kMaxRows * D + r] = m, part[kMaxRows * D + kMaxRows + r] = l;
             }
         }
         if (!alone) {
@@ -359,24 +390,12 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_few_kernel(const
                 __threadfence();
             }
             __syncthreads();
-            if (flags[1]) {
-                for (int i = tid; i < n_rows * (D / 4); i += kWarps * 32) {
-                    const int r = i / (D / 4);
-                    float m = -INFINITY, l = 0.f;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int64_t c = first_cta; c <= last_cta; ++c) {
-                        const float *pc = a.ws.part + (c * 2 + (c == first_cta ? 1 : 0)) * F::kPart;
-                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(pc) + i);
-                        join(m, l, acc, __ldcg(pc + kRows * D + r), __ldcg(pc + kRows * D + kRows + r), x);
-                    }
-                    store_row4<TYPE, D>(a, pl.s.row0, head, r0 + r, i % (D / 4), acc, m, l);
-                }
-            }
+            if (flags[1]) join_parts<TYPE, D>(a, pl.s.row0, head, n_rows, first_cta, (int)(last_cta - first_cta) + 1, F::kPart);
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the rings go back to the copies
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");    // the rings go back to the copies
         __syncthreads();
     }
-    if (*abort_flag) {                                                 // leave no copy in flight behind
+    if (*abort_flag) {                                                  // leave no copy in flight behind
         const uint64_t t0 = now_ns();
         for (int i = 0; i < F::kStages; ++i)
             while (!mbar_try(bars + 8 * i, (phase >> i) & 1) && now_ns() - t0 < 10000000ull) {
@@ -384,7 +403,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) attn_few_kernel(const
     }
 }
 
-template <int TYPE, int D>
+template <int TYPE, int D, int NT>
 cudaError_t launch_few(const AttnArgs &a, cudaStream_t s) {
     FewParams p;
     p.a = a;
@@ -394,13 +413,18 @@ cudaError_t launch_few(const AttnArgs &a, cudaStream_t s) {
     static bool attr[64] = {};
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!attr[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(attn_few_kernel<TYPE, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t e = cudaFuncSetAttribute(attn_few_kernel<TYPE, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    (int)Few<D>::kSmem);
         if (e != cudaSuccess) return e;
         attr[dev] = true;
     }
-    attn_few_kernel<TYPE, D><<<a.sms * kCtasPerSm, kWarps * 32, Few<D>::kSmem, s>>>(p);
+    attn_few_kernel<TYPE, D, NT><<<a.sms * (kCtasPerSm + 1 - NT), kWarps * 32, Few<D>::kSmem, s>>>(p);
     return cudaGetLastError();
+}
+
+template <int TYPE, int D>
+cudaError_t launch_rows(const AttnArgs &a, cudaStream_t s) {
+    return a.c.max_rows * a.group <= 8 ? launch_few<TYPE, D, 1>(a, s) : launch_few<TYPE, D, 2>(a, s);
 }
 
 }  // namespace
@@ -416,10 +440,10 @@ size_t attn_counters(int sms) {
 
 cudaError_t launch_attention(const AttnArgs &a, cudaStream_t s) {
     // rows of one key/value head and sequence: up to one 16-row mma tile, or the tensor cores' 128-row tiles
-    if ((int64_t)a.c.max_rows * a.group > kRows) return launch_attn_tile(a, s);
+    if ((int64_t)a.c.max_rows * a.group > kMaxRows) return launch_attn_tile(a, s);
     const bool bf = a.type == ENGRAM_T_BF16;
-    if (a.c.D == 128) return bf ? launch_few<ENGRAM_T_BF16, 128>(a, s) : launch_few<ENGRAM_T_F16, 128>(a, s);
-    return bf ? launch_few<ENGRAM_T_BF16, 64>(a, s) : launch_few<ENGRAM_T_F16, 64>(a, s);
+    if (a.c.D == 128) return bf ? launch_rows<ENGRAM_T_BF16, 128>(a, s) : launch_rows<ENGRAM_T_F16, 128>(a, s);
+    return bf ? launch_rows<ENGRAM_T_BF16, 64>(a, s) : launch_rows<ENGRAM_T_F16, 64>(a, s);
 }
 
 }  // namespace engram

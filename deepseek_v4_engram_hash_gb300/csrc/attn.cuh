@@ -43,12 +43,14 @@ __device__ __forceinline__ void q_scale(uint32_t m, float scale_log2, float &dow
 
 // The low / high two codes of a word as f16x2 (exact).
 __device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3);
-    return (uint32_t)h.x | (uint32_t)h.y << 16;
+    uint32_t h;
+    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(h) : "r"(w));
+    return h;
 }
 __device__ __forceinline__ uint32_t e4m3_hi(uint32_t w) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-    return (uint32_t)h.x | (uint32_t)h.y << 16;
+    uint32_t h;
+    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, u;\n\t}" : "=r"(h) : "r"(w));
+    return h;
 }
 
 // Shared-memory rows as the tensor maps place them: rows of 128 bytes with the
@@ -102,7 +104,7 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
 }
 
 // Where float4 i of row r lies in a warp's sums (spreads the rows over the banks).
-__device__ __forceinline__ int swz(int r, int i) { return i ^ (r & 7); }
+__device__ __forceinline__ int swz(int r, int i) { return i ^ (r >> 1 & 3); }
 
 // Joins a partial result (bound m2, sum l2, values x) to (m, l, acc).
 __device__ __forceinline__ void join(float &m, float &l, float4 &acc, float m2, float l2, const float4 &x) {
@@ -128,6 +130,34 @@ __device__ __forceinline__ void store_row4(const AttnArgs &a, int row0, int head
         w = make_uint2(pack_f16x2(acc.x * inv, acc.y * inv), pack_f16x2(acc.z * inv, acc.w * inv));
     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * a.out_stride + (int64_t)h * D + 4 * d4) = w;
     if (d4 == 0 && a.lse) a.lse[row * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// Joins `n` partial results of n_rows rows ([row][D] values, then bounds and sums of
+// kMaxRows = 16 rows each; the first in slot 1 of CTA first, the others in slot 0 of theirs)
+// and stores them: a thread a float4, eight loads at a time.
+template <int TYPE, int D>
+__device__ __forceinline__ void join_parts(const AttnArgs &a, int row0, int head, int n_rows, int64_t first, int n, int part_floats) {
+    for (int i = threadIdx.x; i < n_rows * (D / 4); i += blockDim.x) {
+        const int r = i / (D / 4);
+        auto at = [&](int c) { return a.ws.part + ((first + c) * 2 + (c == 0 ? 1 : 0)) * part_floats; };
+        float m = -INFINITY, l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c0 = 0; c0 < n; c0 += 8) {
+            float mm[8], ll[8];
+            float4 x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float *pc = at(min(c0 + j, n - 1));
+                x[j] = __ldcg(reinterpret_cast<const float4 *>(pc) + i);
+                mm[j] = __ldcg(pc + 16 * D + r);
+                ll[j] = __ldcg(pc + 16 * D + 16 + r);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c0 + j < n) join(m, l, acc, mm[j], ll[j], x[j]);
+        }
+        store_row4<TYPE, D>(a, row0, head, r, i % (D / 4), acc, m, l);
+    }
 }
 
 // The cache's codes as a 4D map {head_dim, page_tokens, heads, pages}, boxes of `tokens` rows of one head.
