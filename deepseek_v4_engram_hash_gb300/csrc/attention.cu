@@ -15,12 +15,12 @@
 // the M side of both products (m16n8k16 with f16 operands: S^T = K Q^T and
 // O^T = V^T P^T), 8 query rows the N side: one mma covers 16 tokens x 8 rows, and
 // codes become operands in registers (e4m3 to f16 is exact) once for all rows.
-// A CTA takes a contiguous range of the call's (sequence, head, 64-token tile) list,
+// A CTA takes a contiguous range of the call's (sequence, head, 128-token tile) list,
 // cut evenly over the grid, so any mix of lengths keeps every SM busy; ranges that
 // cut an entry leave partial results, which the last CTA to arrive joins in
-// CTA order.  Inside a CTA each warp streams its own 16-token units through a
+// CTA order.  Inside a CTA each warp streams its own 32-token units through a
 // private ring of TMA copies (one thread issues, the warp itself consumes: no
-// barrier between warps) and keeps its own softmax state; four warps join through
+// barrier between warps) and keeps its own softmax state; the warps join through
 // shared memory at the end of an entry.
 #include "attn.cuh"
 
@@ -30,12 +30,11 @@ namespace {
 
 using namespace attn;
 
-constexpr int kWarps = 4;
-constexpr int kUnit = 16;                            // tokens a copy
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kUnit = 32, kSub = 16;                 // tokens a warp step, in two parts of one page each
 constexpr int kTile = kUnit * kWarps;                // tokens a CTA step
 constexpr int kMaxRows = 16;
-constexpr int kMinTiles = 2;                         // tiles a CTA takes at least
-constexpr int kCtasPerSm = 4;                        // 3 with 16 rows (registers)
+constexpr int kCtasPerSm = 3;
 constexpr uint32_t kNever = 0x7FFFFFFF;
 
 struct FewParams {
@@ -45,11 +44,15 @@ struct FewParams {
 
 template <int D>
 struct Few {
-    static constexpr int kStages = 384 / D;          // 12 KB a warp
+    static constexpr int kStages = 256 / D;          // 16 KB a warp
     static constexpr int kHalf = kUnit * D;          // bytes of a unit's keys (or values)
     static constexpr int kRing = kStages * 2 * kHalf;
     static constexpr int kRegion = kWarps * kRing;
-    static constexpr size_t kSmem = 1024 + kRegion + 1024;
+    // behind the rings: bounds and sums of the warps, the copies' barriers, two flags
+    static constexpr int oBars = kRegion + 2 * kWarps * kMaxRows * 4, oFlags = oBars + kWarps * kStages * 8;
+    static constexpr size_t kSmem = 1024 + oFlags + 16;
+    static_assert(kMaxRows * D * 4 <= kRing && kCtasPerSm * (kSmem + 1024) <= 227 * 1024, "shared memory");
+    static_assert(kThreads * 16 + (kMaxRows * kCtasPerSm * 160 + 2 * kMaxRows) * 4 <= kRegion, "factors of a join");
     static constexpr int kPart = kMaxRows * (D + 2); // floats of a partial result
 };
 
@@ -68,7 +71,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-// A sequence's entries, one a head, each of `tiles` 64-token tiles from token lo.
+// A sequence's entries, one a head, each of `tiles` 128-token tiles from token lo.
 struct Plan {
     Seq s;
     int lo, tiles;
@@ -76,14 +79,74 @@ struct Plan {
 __device__ __forceinline__ Plan plan_of(const AttnArgs &a, int b) {
     Plan p;
     p.s = sequence(a.c, b);
-    p.lo = a.window ? max(0, p.s.kv - p.s.n - a.window + 1) / kTile * kTile : 0;
+    p.lo = a.window ? max(0, p.s.kv - p.s.n - a.window + 1) / kUnit * kUnit : 0;
     p.tiles = p.s.n == 0 ? 0 : max(1, (p.s.kv - p.lo + kTile - 1) / kTile);
     return p;
 }
 
+// Joins the n partial results of an entry ([row][D] values, then the bounds and the
+// sums of kMaxRows rows; the first in slot 1 of CTA `first`, the others in slot 0 of
+// theirs) and stores them.  The factors 2^(M_c - M) go through shared memory, then
+// a thread adds up one float4 over every groups-th part, sixteen loads at a time,
+// and the groups are added in order.
+template <int TYPE, int D>
+__device__ __forceinline__ void join_parts(const AttnArgs &a, int row0, int head, int n_rows, int64_t first, int n, uint8_t *smem) {
+    constexpr int kPart = Few<D>::kPart;
+    float *fac = reinterpret_cast<float *>(smem) + 4 * kThreads;         // [n_rows][n]
+    float4 *sums = reinterpret_cast<float4 *>(smem);                     // [groups][items]
+    float *row_m = fac + n_rows * n, *row_l = row_m + kMaxRows;
+    const int tid = threadIdx.x, lane = tid & 31;
+    auto at = [&](int c) { return a.ws.part + ((first + c) * 2 + (c == 0 ? 1 : 0)) * kPart; };
+    for (int r = tid >> 5; r < n_rows; r += kWarps) {
+        float m = -INFINITY, l = 0.f;
+        for (int c = lane; c < n; c += 32) m = fmaxf(m, __ldcg(at(c) + kMaxRows * D + r));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        for (int c = lane; c < n; c += 32) {
+            const float mc = __ldcg(at(c) + kMaxRows * D + r), lc = __ldcg(at(c) + kMaxRows * D + kMaxRows + r);
+            const float f = mc == -INFINITY ? (lc == 0.f ? 0.f : 1.f) : exp2_approx(mc - m);
+            fac[r * n + c] = f;
+            l = fmaf(lc, f, l);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        if (lane == 0) row_m[r] = m, row_l[r] = l;
+    }
+    __syncthreads();
+    const int items = n_rows * (D / 4), groups = items >= kThreads ? 1 : kThreads / items;
+    for (int i0 = 0; i0 < items; i0 += kThreads) {
+        const int i = i0 + (groups > 1 ? tid % items : tid), grp = groups > 1 ? tid / items : 0, r = i / (D / 4);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < items && grp < groups) {
+            for (int c0 = grp; c0 < n; c0 += 16 * groups) {
+                float4 x[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    x[j] = __ldcg(reinterpret_cast<const float4 *>(at(min(c0 + j * groups, n - 1))) + i);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int c = c0 + j * groups;
+                    const float f = c < n ? fac[r * n + c] : 0.f;
+                    if (c < n) acc.x = fmaf(x[j].x, f, acc.x), acc.y = fmaf(x[j].y, f, acc.y), acc.z = fmaf(x[j].z, f, acc.z), acc.w = fmaf(x[j].w, f, acc.w);
+                }
+            }
+        }
+        if (groups > 1) {
+            sums[tid] = acc;
+            __syncthreads();
+            if (grp == 0)
+                for (int k = 1; k < groups; ++k) {
+                    const float4 x = sums[k * items + i];
+                    acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
+                }
+        }
+        if (i < items && grp == 0) store_row4<TYPE, D>(a, row0, head, r, i % (D / 4), acc, row_m[r], row_l[r]);
+    }
+}
+
 // NT: groups of 8 query rows.
 template <int TYPE, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm + 1 - NT) attn_few_kernel(const __grid_constant__ FewParams p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_few_kernel(const __grid_constant__ FewParams p) {
     using F = Few<D>;
     constexpr int KS = D / 16;                       // k steps of K Q^T, and 16-dim tiles of V^T P^T
     extern __shared__ uint8_t smem_raw[];
@@ -93,8 +156,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm + 1 - NT) attn_few_ker
     uint8_t *smem = smem_raw + (base - raw);
     const uint32_t ring = base + warp * F::kRing;
     float *stat = reinterpret_cast<float *>(smem + F::kRegion);          // [2][kWarps][kMaxRows]
-    const uint32_t bars = smem_u32(smem + F::kRegion + 512) + warp * F::kStages * 8;
-    int *flags = reinterpret_cast<int *>(smem + F::kRegion + 512 + kWarps * F::kStages * 8);
+    const uint32_t bars = smem_u32(smem + F::oBars) + warp * F::kStages * 8;
+    int *flags = reinterpret_cast<int *>(smem + F::oFlags);
     volatile int *abort_flag = flags;
     if (tid == 0) flags[0] = 0;
     if (lane == 0) {
@@ -118,7 +181,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm + 1 - NT) attn_few_ker
         if (lane >= o) upto += x;
     }
     const int64_t total = __shfl_sync(0xFFFFFFFFu, upto, 31);
-    const int64_t per = max((int64_t)kMinTiles, (total + gridDim.x - 1) / gridDim.x);
+    const int64_t per = max((int64_t)1, (total + gridDim.x - 1) / gridDim.x);
     int64_t t = blockIdx.x * per;
     const int64_t end = min(total, t + per);
     if (t >= end) return;
@@ -144,10 +207,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm + 1 - NT) attn_few_ker
         const int units = tok0 < tok1 ? (tok1 - tok0 + kTile - 1) / kTile : 0;
         const int n_rows = min(8 * NT, pl.s.n * a.group);
 
-        // pages and scales of 32 units at a time, one a lane: id, key byte | value byte << 8
+        // pages and scales of 16 units at a time, one part a lane: id, key byte | value byte << 8
         auto load_id = [&](int k) {
-            const int u = 32 * k + lane, tok = tok0 + u * kTile;
-            return u < units ? page_of(a.c, b, tok >> a.c.pt_log2) : -1;
+            const int tok = tok0 + (16 * k + (lane >> 1)) * kTile + (lane & 1) * kSub;
+            return tok < tok1 ? page_of(a.c, b, tok >> a.c.pt_log2) : -1;
         };
         auto load_scales = [&](int id) {
             if (id < 0) return 0u;
@@ -155,19 +218,23 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm + 1 - NT) attn_few_ker
             return (uint32_t)a.c.k_scales[i] | (uint32_t)a.c.v_scales[i] << 8;
         };
         int id_cur = load_id(0), id_next = load_id(1);
-        auto issue = [&](int u, int cur_block) {
-            const int mine_id = (u >> 5) == cur_block ? id_cur : id_next;
-            const int id = __shfl_sync(0xFFFFFFFFu, mine_id, u & 31);
+        auto issue = [&](int u, int st, int cur_block) {
+            const int ids = (u >> 4) == cur_block ? id_cur : id_next;
+            const int id0 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (u & 15)), id1 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (u & 15) + 1);
             if (lane == 0) {
-                const int st = (stage + u) % F::kStages;
-                const int tok = tok0 + u * kTile, at = tok & (a.c.pt - 1), page = id < 0 ? a.c.n_pages : id;
+                const int at = (tok0 + u * kTile) & (a.c.pt - 1);
+                const int p0 = id0 < 0 ? a.c.n_pages : id0, p1 = id1 < 0 ? a.c.n_pages : id1;   // outside the cache: zeros
                 const uint32_t dst = ring + st * 2 * F::kHalf, bar = bars + 8 * st;
                 mbar_expect_tx(bar, 2 * F::kHalf);
-                tma_load_4d(dst, &p.mk, 0, at, head, page, bar);       // a page outside the cache reads as zeros
-                tma_load_4d(dst + F::kHalf, &p.mv, 0, at, head, page, bar);
+                tma_load_4d(dst, &p.mk, 0, at, head, p0, bar);
+                tma_load_4d(dst + F::kHalf, &p.mv, 0, at, head, p0, bar);
+                if (a.c.pt == kSub) {
+                    tma_load_4d(dst + F::kHalf / 2, &p.mk, 0, 0, head, p1, bar);
+                    tma_load_4d(dst + F::kHalf + F::kHalf / 2, &p.mv, 0, 0, head, p1, bar);
+                }
             }
         };
-        for (int u = 0; u < min(units, F::kStages); ++u) issue(u, 0);
+        for (int u = 0; u < min(units, F::kStages); ++u) issue(u, (stage + u) % F::kStages, 0);
         uint32_t sc_cur = load_scales(id_cur), sc_next = 0;
 
         // query row 8 nt + g, the lane's D / 4 dims, as f16 of about 1; bounds and factors of rows 8 nt + 2 q4 + e
@@ -219,60 +286,71 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm + 1 - NT) attn_few_ker
 #pragma unroll 1
         for (int u = 0; u < units; ++u) {
             const int tb = tok0 + u * kTile;
-            if ((u & 31) == 0 && u) {
+            if ((u & 15) == 0 && u) {
                 id_cur = id_next;
                 sc_cur = sc_next;
-                id_next = load_id((u >> 5) + 1);
+                id_next = load_id((u >> 4) + 1);
             }
-            if ((u & 31) == 16) sc_next = load_scales(id_next);
+            if ((u & 15) == 8) sc_next = load_scales(id_next);
             const int st = stage;
             stage = stage + 1 == F::kStages ? 0 : stage + 1;
             const bool here = wait_bar(bars + 8 * st, (phase >> st) & 1, abort_flag, a.c.err);
             phase ^= 1u << st;
             if (!__all_sync(0xFFFFFFFFu, here)) break;
             const uint32_t ks = ring + st * 2 * F::kHalf, vs = ks + F::kHalf;
-            const uint32_t sc = __shfl_sync(0xFFFFFFFFu, sc_cur, u & 31);
-            const int id = __shfl_sync(0xFFFFFFFFu, id_cur, u & 31);
+            uint32_t sc[2];
+            bool known[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                sc[h] = __shfl_sync(0xFFFFFFFFu, sc_cur, 2 * (u & 15) + h);
+                known[h] = __shfl_sync(0xFFFFFFFFu, id_cur, 2 * (u & 15) + h) >= 0;
+            }
 
-            // scores of tokens g and g + 8 (mma rows) and rows 2 q4, 2 q4 + 1; dims go to the k slots in the order of qb
-            float s[NT][4] = {};
-            {
+            // scores of tokens g and g + 8 of a part (mma rows) and rows 2 q4, 2 q4 + 1; dims go to the k slots in the order of qb
+            float s[2][NT][4] = {};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
                 uint32_t w0[KS], w1[KS];
-                load_k_row<D>(ks, g, q4, w0);
-                load_k_row<D>(ks, g + 8, q4, w1);
+                load_k_row<D>(ks, kSub * h + g, q4, w0);
+                load_k_row<D>(ks, kSub * h + g + 8, q4, w1);
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
                     const uint32_t a0 = e4m3_lo(w0[k]), a1 = e4m3_lo(w1[k]), a2 = e4m3_hi(w0[k]), a3 = e4m3_hi(w1[k]);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], a0, a1, a2, a3, qb[nt][k][0], qb[nt][k][1]);
+                    for (int nt = 0; nt < NT; ++nt) mma16816(s[h][nt], a0, a1, a2, a3, qb[nt][k][0], qb[nt][k][1]);
                 }
             }
-            const float ek = e8m0_to_f32(sc & 255u), ev = value_exp(sc >> 8), back = value_unscale(sc >> 8);
-            const bool whole = tb >= all_lo && tb + kUnit <= all_hi && id >= 0;
             bool over = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[nt][e] = fmaf(s[nt][e], kf[nt][e & 1] * ek, ev);
-            if (!whole) {
+            for (int h = 0; h < 2; ++h) {
+                const float ek = e8m0_to_f32(sc[h] & 255u), ev = value_exp(sc[h] >> 8);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int tok = tb + g + 8 * (e >> 1);
-                        if (tok >= lim[nt][e & 1] || tok < low[nt][e & 1] || id < 0) s[nt][e] = -INFINITY;
-                    }
+                    for (int e = 0; e < 4; ++e) s[h][nt][e] = fmaf(s[h][nt][e], kf[nt][e & 1] * ek, ev);
+            }
+            if (!(tb >= all_lo && tb + kUnit <= all_hi && known[0] && known[1])) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int tok = tb + kSub * h + g + 8 * (e >> 1);
+                            if (tok >= lim[nt][e & 1] || tok < low[nt][e & 1] || !known[h]) s[h][nt][e] = -INFINITY;
+                        }
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) over |= fmaxf(s[nt][e], s[nt][2 + e]) > M[nt][e] + kLazy;
+                for (int e = 0; e < 2; ++e)
+                    over |= fmaxf(fmaxf(s[0][nt][e], s[0][nt][2 + e]), fmaxf(s[1][nt][e], s[1][nt][2 + e])) > M[nt][e] + kLazy;
             if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float m = fmaxf(s[nt][e], s[nt][2 + e]);
+                        float m = fmaxf(fmaxf(s[0][nt][e], s[0][nt][2 + e]), fmaxf(s[1][nt][e], s[1][nt][2 + e]));
                         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
                         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
@@ -284,27 +362,33 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm + 1 - NT) attn_few_ker
                         for (int k = 0; k < KS; ++k) o[nt][k][e] *= f, o[nt][k][2 + e] *= f;
                     }
             }
-            uint32_t pb[NT][2];
+            uint32_t pb[2][NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const float m0 = M[nt][0] == -INFINITY ? 0.f : M[nt][0], m1 = M[nt][1] == -INFINITY ? 0.f : M[nt][1];
-                const float x0 = exp2_approx(s[nt][0] - m0), x1 = exp2_approx(s[nt][1] - m1);
-                const float y0 = exp2_approx(s[nt][2] - m0), y1 = exp2_approx(s[nt][3] - m1);
-                L[nt][0] = fmaf(x0 + y0, back, L[nt][0]);
-                L[nt][1] = fmaf(x1 + y1, back, L[nt][1]);
-                pb[nt][0] = transpose8(pack_f16x2(x0, x1));             // row g, tokens 2 q4, 2 q4 + 1
-                pb[nt][1] = transpose8(pack_f16x2(y0, y1));             // and those + 8
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float back = value_unscale(sc[h] >> 8);
+                    const float x0 = exp2_approx(s[h][nt][0] - m0), x1 = exp2_approx(s[h][nt][1] - m1);
+                    const float y0 = exp2_approx(s[h][nt][2] - m0), y1 = exp2_approx(s[h][nt][3] - m1);
+                    L[nt][0] = fmaf(x0 + y0, back, L[nt][0]);
+                    L[nt][1] = fmaf(x1 + y1, back, L[nt][1]);
+                    pb[h][nt][0] = transpose8(pack_f16x2(x0, x1));      // row g, tokens 2 q4, 2 q4 + 1
+                    pb[h][nt][1] = transpose8(pack_f16x2(y0, y1));      // and those + 8
+                }
             }
             // out: mma rows g and g + 8 of tile i are the dims D / 8 g + 2 i and + 1, k slots the tokens 2 q4, 2 q4 + 1 (+ 8)
-            {
+            const bool cut = tb + kUnit > pl.s.kv || (int)min(sc[0], sc[1]) >> 8 < kLeastValueByte;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
                 constexpr int VW = D / 32;                              // 32-bit words of a lane's dims
                 uint32_t v[4][VW];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) load_v_row<D>(vs, 2 * q4 + (r & 1) + 8 * (r >> 1), g, v[r]);
-                if (tb + kUnit > pl.s.kv || (int)(sc >> 8) < kLeastValueByte) {
+                for (int r = 0; r < 4; ++r) load_v_row<D>(vs, kSub * h + 2 * q4 + (r & 1) + 8 * (r >> 1), g, v[r]);
+                if (cut) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        if (tb + 2 * q4 + (r & 1) + 8 * (r >> 1) >= pl.s.kv || (int)(sc >> 8) < kLeastValueByte)
+                        if (tb + kSub * h + 2 * q4 + (r & 1) + 8 * (r >> 1) >= pl.s.kv || (int)(sc[h] >> 8) < kLeastValueByte)
 #pragma unroll
                             for (int i = 0; i < VW; ++i) v[r][i] = 0u;  // nothing is written there, or it does not count
                 }
@@ -316,26 +400,17 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm + 1 - NT) attn_few_ker
                     const uint32_t c0 = e4m3_lo(a23), c1 = e4m3_hi(a23), c2 = e4m3_lo(b23), c3 = e4m3_hi(b23);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        mma16816(o[nt][2 * i], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-                        mma16816(o[nt][2 * i + 1], c0, c1, c2, c3, pb[nt][0], pb[nt][1]);
+                        mma16816(o[nt][2 * i], a0, a1, a2, a3, pb[h][nt][0], pb[h][nt][1]);
+                        mma16816(o[nt][2 * i + 1], c0, c1, c2, c3, pb[h][nt][0], pb[h][nt][1]);
                     }
                 }
             }
             __syncwarp();                                               // the stage is read
-            if (u + F::kStages < units) {
-                const int mine_id = ((u + F::kStages) >> 5) == (u >> 5) ? id_cur : id_next;
-                const int nid = __shfl_sync(0xFFFFFFFFu, mine_id, (u + F::kStages) & 31);
-                if (lane == 0) {
-                    const int tok = tb + F::kStages * kTile, at = tok & (a.c.pt - 1), page = nid < 0 ? a.c.n_pages : nid;
-                    mbar_expect_tx(bars + 8 * st, 2 * F::kHalf);
-                    tma_load_4d(ks, &p.mk, 0, at, head, page, bars + 8 * st);
-                    tma_load_4d(vs, &p.mv, 0, at, head, page, bars + 8 * st);
-                }
-            }
+            if (u + F::kStages < units) issue(u + F::kStages, st, u >> 4);
         }
         if (__syncthreads_or(*abort_flag)) break;                       // copies in flight are waited for below
 
-        // join the four warps: each leaves its sums in its own ring
+        // join the warps: each leaves its sums in its own ring
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -357,7 +432,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm + 1 - NT) attn_few_ker
         const int64_t first_cta = entry_t0 / per, last_cta = (entry_t0 + pl.tiles - 1) / per;
         const bool alone = first_cta == last_cta;
         float *part = a.ws.part + ((int64_t)blockIdx.x * 2 + (blockIdx.x == first_cta ? 1 : 0)) * F::kPart;
-        for (int i = tid; i < n_rows * (D / 4); i += kWarps * 32) {
+        for (int i = tid; i < n_rows * (D / 4); i += kThreads) {
             const int r = i / (D / 4), d4 = i % (D / 4);
             float m = stat[r], l = 0.f;
 #pragma unroll
@@ -390,7 +465,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm + 1 - NT) attn_few_ker
                 __threadfence();
             }
             __syncthreads();
-            if (flags[1]) join_parts<TYPE, D>(a, pl.s.row0, head, n_rows, first_cta, (int)(last_cta - first_cta) + 1, F::kPart);
+            if (flags[1]) join_parts<TYPE, D>(a, pl.s.row0, head, n_rows, first_cta, (int)(last_cta - first_cta) + 1, smem);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");    // the rings go back to the copies
         __syncthreads();
@@ -407,7 +482,8 @@ template <int TYPE, int D, int NT>
 cudaError_t launch_few(const AttnArgs &a, cudaStream_t s) {
     FewParams p;
     p.a = a;
-    if (!make_cache_map(&p.mk, a.c, a.c.k, kUnit) || !make_cache_map(&p.mv, a.c, a.c.v, kUnit)) return cudaErrorInvalidValue;
+    const int box = a.c.pt < kUnit ? a.c.pt : kUnit;
+    if (!make_cache_map(&p.mk, a.c, a.c.k, box) || !make_cache_map(&p.mv, a.c, a.c.v, box)) return cudaErrorInvalidValue;
     int dev = 0;
     cudaGetDevice(&dev);
     static bool attr[64] = {};
@@ -418,7 +494,7 @@ cudaError_t launch_few(const AttnArgs &a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         attr[dev] = true;
     }
-    attn_few_kernel<TYPE, D, NT><<<a.sms * (kCtasPerSm + 1 - NT), kWarps * 32, Few<D>::kSmem, s>>>(p);
+    attn_few_kernel<TYPE, D, NT><<<a.sms * kCtasPerSm, kThreads, Few<D>::kSmem, s>>>(p);
     return cudaGetLastError();
 }
 

@@ -132,34 +132,6 @@ __device__ __forceinline__ void store_row4(const AttnArgs &a, int row0, int head
     if (d4 == 0 && a.lse) a.lse[row * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-// Joins `n` partial results of n_rows rows ([row][D] values, then bounds and sums of
-// kMaxRows = 16 rows each; the first in slot 1 of CTA first, the others in slot 0 of theirs)
-// and stores them: a thread a float4, eight loads at a time.
-template <int TYPE, int D>
-__device__ __forceinline__ void join_parts(const AttnArgs &a, int row0, int head, int n_rows, int64_t first, int n, int part_floats) {
-    for (int i = threadIdx.x; i < n_rows * (D / 4); i += blockDim.x) {
-        const int r = i / (D / 4);
-        auto at = [&](int c) { return a.ws.part + ((first + c) * 2 + (c == 0 ? 1 : 0)) * part_floats; };
-        float m = -INFINITY, l = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c0 = 0; c0 < n; c0 += 8) {
-            float mm[8], ll[8];
-            float4 x[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float *pc = at(min(c0 + j, n - 1));
-                x[j] = __ldcg(reinterpret_cast<const float4 *>(pc) + i);
-                mm[j] = __ldcg(pc + 16 * D + r);
-                ll[j] = __ldcg(pc + 16 * D + 16 + r);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c0 + j < n) join(m, l, acc, mm[j], ll[j], x[j]);
-        }
-        store_row4<TYPE, D>(a, row0, head, r, i % (D / 4), acc, m, l);
-    }
-}
-
 // The cache's codes as a 4D map {head_dim, page_tokens, heads, pages}, boxes of `tokens` rows of one head.
 inline bool make_cache_map(CUtensorMap *map, const KvView &c, const uint8_t *codes, int tokens) {
     const uint64_t dims[4] = {(uint64_t)c.D, (uint64_t)c.pt, (uint64_t)c.KH, (uint64_t)c.n_pages};
