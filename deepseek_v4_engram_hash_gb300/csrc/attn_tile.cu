@@ -15,7 +15,7 @@
 //   warps 8..11        codes to f16 operand tiles in shared memory (e4m3 to f16 is exact);
 //                      keys and values alike stay [token][dim]: values are the
 //                      MN-major operand of the second product;
-//   warp 12            issues the MMAs (M 128, N 128 / D, K 16): S_h = Q_h K^T,
+//   warps 12, 14       issue the MMAs of half 0 / 1 (M 128, N 128 / D, K 16): S_h = Q_h K^T,
 //                      O_h += P_h V with P_h from tensor memory;
 //   warp 13            pages, scales and TMA copies of the codes.
 // While one half is in its softmax the tensor cores work for the other.  Tensor
@@ -44,19 +44,6 @@ constexpr int kGroups = kTok / 16;                   // scale groups a step (a p
 constexpr int kMetaRing = 4;
 constexpr uint32_t kNever = 0x7FFFFFFF;
 
-template <int D>
-struct Tile {
-    static constexpr int kQ = kHalf * D * 2;         // bytes of a half's queries
-    static constexpr int kF16 = kTok * D * 2;        // bytes of a converted tile
-    static constexpr int kFp8 = kTok * D;            // bytes of a staged tile
-    static constexpr int oQ = 0, oK = oQ + 2 * kQ, oV = oK + 2 * kF16, oS = oV + 2 * kF16, oAux = oS + 2 * kFp8;
-    static constexpr size_t kSmem = 1024 + oAux + 1024;
-    static constexpr int kSub = kTok * 128;          // bytes of a 64-dim sub-tile (128 rows of 128 bytes)
-    static constexpr int kPart = kRows * (D + 2);    // floats of a partial result
-    static constexpr uint32_t cS = 0, cO = 256;      // tensor-memory columns
-    static constexpr uint32_t cP = D == 128 ? 0 : 384, sP = D == 128 ? 128 : 64;
-};
-
 struct TileParams {
     AttnArgs a;
     CUtensorMap mk, mv;
@@ -81,16 +68,16 @@ __device__ __forceinline__ int64_t head_tiles(const AttnArgs &a, const Seq &s) {
     return n;
 }
 
-// This CTA's range of the list, entry by entry; every warp walks it by itself.
+// This CTA's range of the list, entry by entry.  Every warp walks it by itself; the
+// walk lies in shared memory (one a warp, stepped by its lane 0), so the roles'
+// inner loops keep their registers.
 struct Walk {
-    int64_t t, end, per, before, per_head;
-    int b;
+    int64_t t, end, per, entry_t0;
     Seq s;
-    // the current entry
     RowTile rt;
-    int head, tile0, count;
-    int64_t entry_t0;
+    int b, head, row_tile_no, tile0, count;
 
+    // A whole warp calls this.
     __device__ __forceinline__ bool start(const AttnArgs &a) {
         const int lane = threadIdx.x & 31;
         const int lanes_per = (a.c.batch + 31) / 32;
@@ -106,67 +93,118 @@ struct Walk {
             if (lane >= o) upto += x;
         }
         const int64_t total = __shfl_sync(0xFFFFFFFFu, upto, 31);
-        per = max((int64_t)1, (total + gridDim.x - 1) / gridDim.x);
-        t = blockIdx.x * per;
-        end = min(total, t + per);
-        if (t >= end) return false;
-        const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, t < upto)) - 1;
-        b = owner * lanes_per;
-        before = __shfl_sync(0xFFFFFFFFu, upto - mine, owner);
-        s = sequence(a.c, b);
-        per_head = head_tiles(a, s);
+        const int64_t p = max((int64_t)1, (total + gridDim.x - 1) / gridDim.x), from = blockIdx.x * p;
+        if (from >= total) return false;
+        const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, from < upto)) - 1;
+        int64_t rel = from - __shfl_sync(0xFFFFFFFFu, upto - mine, owner);
+        if (lane == 0) {
+            b = owner * lanes_per;
+            s = sequence(a.c, b);
+            int64_t per_head = head_tiles(a, s);
+            while (rel >= per_head * a.c.KH && b + 1 < a.c.batch) {
+                rel -= per_head * a.c.KH;
+                s = sequence(a.c, ++b);
+                per_head = head_tiles(a, s);
+            }
+            head = (int)(rel / per_head);
+            rel -= head * per_head;
+            rt = row_tile(a, s, row_tile_no = 0);
+            while (rel >= rt.tiles && rt.r0 + rt.n_rows < s.n * a.group) {
+                rel -= rt.tiles;
+                rt = row_tile(a, s, ++row_tile_no);
+            }
+            tile0 = (int)rel;
+            t = from;
+            end = min(total, from + p);
+            per = p;
+            count = 0;
+        }
         return true;
     }
-    __device__ __forceinline__ bool next(const AttnArgs &a) {
-        if (t >= end) return false;
-        while (t >= before + per_head * a.c.KH && b + 1 < a.c.batch) {
-            before += per_head * a.c.KH;
-            s = sequence(a.c, ++b);
-            per_head = head_tiles(a, s);
+    // The next entry; `first` on the first call.  A whole warp calls this.
+    __device__ __forceinline__ bool next(const AttnArgs &a, bool first) {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) {
+            if (!first && t < end) {                  // the entry before ended with its row tile
+                tile0 = 0;
+                if (rt.r0 + rt.n_rows < s.n * a.group) {
+                    rt = row_tile(a, s, ++row_tile_no);
+                } else {
+                    if (++head == a.c.KH) {
+                        head = 0;
+                        do {
+                            if (b + 1 >= a.c.batch) {             // the arrays changed under the call
+                                t = end;
+                                break;
+                            }
+                            s = sequence(a.c, ++b);
+                        } while (s.n == 0);
+                    }
+                    rt = row_tile(a, s, row_tile_no = 0);
+                }
+            }
+            count = (int)min((int64_t)(rt.tiles - tile0), end - t);
+            entry_t0 = t - tile0;
+            t += count;
         }
-        int64_t rel = t - before;
-        head = (int)(rel / per_head);
-        rel -= head * per_head;
-        for (int i = 0;; ++i) {
-            rt = row_tile(a, s, i);
-            if (rel < rt.tiles || rt.r0 + rt.n_rows >= s.n * a.group) break;
-            rel -= rt.tiles;
-        }
-        tile0 = (int)rel;
-        count = (int)min((int64_t)(rt.tiles - tile0), end - t);
-        entry_t0 = t - tile0;
-        t += count;
-        return true;
+        __syncwarp();
+        return count > 0;
     }
+};
+
+template <int D>
+struct Tile {
+    static constexpr int kQ = kHalf * D * 2;         // bytes of a half's queries
+    static constexpr int kF16 = kTok * D * 2;        // bytes of a converted tile
+    static constexpr int kFp8 = kTok * D;            // bytes of a staged tile
+    static constexpr int oQ = 0, oK = oQ + 2 * kQ, oV = oK + 2 * kF16, oS = oV + 2 * kF16, oAux = oS + 2 * kFp8;
+    static constexpr int oWalk = 768;                // in aux, behind the scales, barriers and flags
+    static constexpr size_t kSmem = 1024 + oAux + oWalk + 16 * sizeof(Walk);
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+    static constexpr int kSub = kTok * 128;          // bytes of a 64-dim sub-tile (128 rows of 128 bytes)
+    static constexpr int kPart = kRows * (D + 2);    // floats of a partial result
+    static constexpr uint32_t cS = 0, cO = 256;      // tensor-memory columns
+    static constexpr uint32_t cP = D == 128 ? 0 : 384, sP = D == 128 ? 128 : 64;
 };
 
 // Instruction descriptor, kind::f16 with f16 operands and an f32 accumulator;
 // mn_b: the B operand is MN-major (bit 16).
-constexpr uint32_t idesc_f16(int M, int N, bool mn_b) {
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool mn_b) {
     return (1u << 4) | (mn_b ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// MN-major operand with the 128-byte swizzle: 64 elements of the outer
-// dimension a 128-byte row, 8-row groups along K 1024 bytes apart (stride byte offset),
-// the next 64 elements a sub-tile further (leading byte offset).
-__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t sub_bytes) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)(sub_bytes >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
-           (uint64_t)1u << 46 | (uint64_t)2u << 61;
+// Shared-memory descriptors as two words: the upper one (8-row groups 1024 bytes
+// apart, version 1, 128-byte swizzle) is the same for both operand layouts.  K-major:
+// a row is 64 elements of K; MN-major: a row is 64 elements of the outer dimension,
+// 8-row groups along K, the next 64 elements a sub-tile further (leading byte offset).
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lead_bytes) {
+    return ((saddr >> 4) & 0x3FFFu) | (lead_bytes >> 4) << 16;
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t accumulate) {
+template <uint32_t IDESC>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(da), "l"(db), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}"
+        ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(IDESC), "r"((uint32_t)accumulate)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t ta, uint64_t db, uint32_t idesc, uint32_t accumulate) {
+template <uint32_t IDESC>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t ta, uint32_t b_lo, bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d), "r"(ta), "l"(db), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}"
+        ::"r"(d), "r"(ta), "r"(b_lo), "r"(kDescHi), "r"(IDESC), "r"((uint32_t)accumulate)
         : "memory");
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
 }
 __device__ __forceinline__ void commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -191,6 +229,30 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&u)[16]) {
           "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
         : "r"(taddr));
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// Two f32 at a time (the packed FMA and ADD of sm_100 and up), and the three-way maximum.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float &x, float &y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -234,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
     float4 *meta = reinterpret_cast<float4 *>(aux);                       // [kMetaRing][kGroups]: 2^ek, ev, 2^-ev, counts
     const uint32_t bar0 = smem_u32(aux + kMetaRing * kGroups * 16);
     enum { Q_FULL = 0, ST_FULL = 2, ST_EMPTY = 4, K_FULL = 6, K_EMPTY = 8, V_FULL = 10, V_EMPTY = 12, S_FULL = 14, P_FULL = 16,
-           PV_DONE = 18, DRAIN = 20, BARS = 21 };
+           PV_DONE = 18, DRAIN = 20, BARS = 22 };
     auto bar = [&](int i) { return bar0 + 8u * i; };
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(aux + kMetaRing * kGroups * 16 + BARS * 8);
     int *flags = reinterpret_cast<int *>(aux + kMetaRing * kGroups * 16 + BARS * 8 + 8);
@@ -246,14 +308,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
             mbar_init(bar(ST_FULL + i), 1);
             mbar_init(bar(ST_EMPTY + i), 128);
             mbar_init(bar(K_FULL + i), 128);
-            mbar_init(bar(K_EMPTY + i), 1);
+            mbar_init(bar(K_EMPTY + i), 2);               // both halves' products
             mbar_init(bar(V_FULL + i), 128);
-            mbar_init(bar(V_EMPTY + i), 1);
+            mbar_init(bar(V_EMPTY + i), 2);
             mbar_init(bar(S_FULL + i), 1);
             mbar_init(bar(P_FULL + i), kHalf);
             mbar_init(bar(PV_DONE + i), 1);
+            mbar_init(bar(DRAIN + i), 1);
         }
-        mbar_init(bar(DRAIN), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_smem();
@@ -268,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     int *err = a.c.err;
-    Walk e;
+    Walk &e = reinterpret_cast<Walk *>(aux + T::oWalk)[warp];
 
     // 512 threads launch with 128 registers each: 2 x 128 x 176 + 128 x 88 + 128 x 72 are as many
     if (warp >= 12) {
@@ -277,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
             // ---- pages, scales, copies ----
             bool ok = e.start(a);
             int it = 0;
-            while (ok && e.next(a)) {
+            for (bool first = true; ok && e.next(a, first); first = false) {
                 const int tok0 = e.rt.lo + e.tile0 * kTok;
                 const int at = 16 * (lane & 7);
                 const bool leader = lane < 8 && (at & (a.c.pt - 1)) == 0;
@@ -322,61 +384,65 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
             for (int i = 0; i < 2; ++i)
                 while (it > 0 && !mbar_try(bar(ST_FULL + i), (it - 1) & 1) && now_ns() - t0 < 10000000ull) {
                 }
-        } else if (warp == 12) {
-            // ---- the tensor cores ----
+        } else if (warp != 15) {
+            // ---- the tensor cores: warp 12 for half 0, warp 14 for half 1 ----
+            const int h = (warp - 12) >> 1;
             bool ok = e.start(a);
-            uint32_t n = 0, nh[2] = {0, 0}, ent[2] = {0, 0};              // steps, steps a half, entries a half
-            while (ok && e.next(a)) {
-                const int halves = e.rt.n_rows > kHalf ? 2 : 1;
-                if (lane == 0) {
-                    auto qk = [&](int h, uint32_t step) {
-                        const uint32_t q = base + T::oQ + h * T::kQ, k = base + T::oK + (step & 1) * T::kF16;
+            uint32_t n = 0, nh = 0, ent = 0;                              // steps, steps with rows in this half, such entries
+            const uint32_t q_lo = desc_lo(base + T::oQ + h * T::kQ, 16);
+            const uint32_t tS = tmem + T::cS + h * 128, tO = tmem + T::cO + h * D, tP = tmem + T::cP + h * T::sP;
+            for (bool first = true; ok && e.next(a, first); first = false) {
+                const int count = e.count;
+                const bool both = e.rt.n_rows > kHalf;
+                if (h && !both) {
+                    // no rows in this half: keep step with the converted tiles (their barriers count both halves)
+                    for (int j = 0; j < count && ok; ++j, ++n) {
+                        ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(K_FULL + (n & 1)), (n >> 1) & 1, abort_flag, err));
+                        if (ok && lane == 0) mbar_arrive(bar(K_EMPTY + (n & 1)));
+                        ok = ok && __all_sync(0xFFFFFFFFu, wait_bar(bar(V_FULL + (n & 1)), (n >> 1) & 1, abort_flag, err));
+                        if (ok && lane == 0) mbar_arrive(bar(V_EMPTY + (n & 1)));
+                    }
+                    continue;
+                }
+                ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(Q_FULL + h), ent++ & 1, abort_flag, err));
+                for (int j = 0; j < count && ok; ++j, ++n, ++nh) {
+                    // scores: over this half's last probabilities (D = 128), so their product has to be done
+                    ok = wait_bar(bar(K_FULL + (n & 1)), (n >> 1) & 1, abort_flag, err) &&
+                         (D == 64 || j == 0 || wait_bar(bar(PV_DONE + h), (nh - 1) & 1, abort_flag, err));
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect()) {
+                        const uint32_t k_lo = desc_lo(base + T::oK + (n & 1) * T::kF16, 16);
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t off = (kk >> 2) * T::kSub + (kk & 3) * 32;
-                            mma_ss(tmem + T::cS + h * 128, sdesc(q + off), sdesc(k + off), idesc_f16(kHalf, kTok, false), kk != 0);
+                            const uint32_t off = ((kk >> 2) * T::kSub + (kk & 3) * 32) >> 4;
+                            mma_ss<idesc_f16(kHalf, kTok, false)>(tS, q_lo + off, k_lo + off, kk != 0);
                         }
                         commit(bar(S_FULL + h));
-                    };
-                    for (int h = 0; h < halves && ok; ++h) ok = wait_bar(bar(Q_FULL + h), ent[h]++ & 1, abort_flag, err);
-                    ok = ok && wait_bar(bar(K_FULL + (n & 1)), (n >> 1) & 1, abort_flag, err);
-                    if (ok) {
-                        tc_fence_after();
-                        for (int h = 0; h < halves; ++h) qk(h, n);
                         commit(bar(K_EMPTY + (n & 1)));
                     }
-                    for (int j = 0; j < e.count && ok; ++j, ++n) {
-                        ok = wait_bar(bar(V_FULL + (n & 1)), (n >> 1) & 1, abort_flag, err);
-                        if (ok && j + 1 < e.count) ok = wait_bar(bar(K_FULL + ((n + 1) & 1)), ((n + 1) >> 1) & 1, abort_flag, err);
-                        for (int h = 0; h < halves && ok; ++h) {
-                            ok = wait_bar(bar(P_FULL + h), nh[h] & 1, abort_flag, err);
-                            if (!ok) break;
-                            tc_fence_after();
-                            const uint32_t v = base + T::oV + (n & 1) * T::kF16;
+                    __syncwarp();
+                    ok = wait_bar(bar(V_FULL + (n & 1)), (n >> 1) & 1, abort_flag, err) &&
+                         wait_bar(bar(P_FULL + h), nh & 1, abort_flag, err);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect()) {
+                        const uint32_t v_lo = desc_lo(base + T::oV + (n & 1) * T::kF16, T::kSub);
+                        mma_ts<idesc_f16(kHalf, D, true)>(tO, tP, v_lo, j != 0);
 #pragma unroll
-                            for (int kk = 0; kk < kTok / 16; ++kk)
-                                mma_ts(tmem + T::cO + h * D, tmem + T::cP + h * T::sP + kk * 8, sdesc_mn(v + kk * 2048, T::kSub),
-                                       idesc_f16(kHalf, D, true), (j | kk) != 0);
-                            commit(bar(PV_DONE + h));
-                            if (h + 1 == halves) commit(bar(V_EMPTY + (n & 1)));
-                            if (j + 1 < e.count) {
-                                // the next scores go over this half's probabilities: their product has to be done
-                                if (D == 128) ok = wait_bar(bar(PV_DONE + h), nh[h] & 1, abort_flag, err);
-                                if (!ok) break;
-                                qk(h, n + 1);
-                                if (h + 1 == halves) commit(bar(K_EMPTY + ((n + 1) & 1)));
-                            }
-                            ++nh[h];
-                        }
+                        for (int kk = 1; kk < kTok / 16; ++kk)
+                            mma_ts<idesc_f16(kHalf, D, true)>(tO, tP + kk * 8, v_lo + kk * (2048 >> 4), true);
+                        commit(bar(PV_DONE + h));
+                        commit(bar(V_EMPTY + (n & 1)));
                     }
+                    __syncwarp();
                 }
-                ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
             }
-            if (lane == 0) {
-                commit(bar(DRAIN));
-                const uint64_t t0 = now_ns();
-                while (!mbar_try(bar(DRAIN), 0) && now_ns() - t0 < 100000000ull) {
-                }
+            if (elect()) commit(bar(DRAIN + h));                          // from the lane that issued the MMAs
+            const uint64_t t0 = now_ns();
+            while (!mbar_try(bar(DRAIN + h), 0) && now_ns() - t0 < 100000000ull) {
             }
             __syncwarp();
         }
@@ -386,10 +452,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
         const int wt = threadIdx.x - 256;
         bool ok = e.start(a);
         uint32_t n = 0;
-        while (ok && e.next(a)) {
-            const int tok0 = e.rt.lo + e.tile0 * kTok;
-            for (int j = 0; j < e.count; ++j, ++n) {
-                const int valid = e.s.kv - (tok0 + j * kTok);             // tokens of the tile that exist
+        for (bool first = true; ok && e.next(a, first); first = false) {
+            const int left = e.s.kv - (e.rt.lo + e.tile0 * kTok), count = e.count;
+            for (int j = 0; j < count; ++j, ++n) {
+                const int valid = left - j * kTok;                        // tokens of the tile that exist
                 for (int x = 0; x < 2 && ok; ++x) {
                     ok = wait_bar(bar(ST_FULL + x), n & 1, abort_flag, err) &&
                          wait_bar(bar((x ? V_EMPTY : K_EMPTY) + (n & 1)), ((n >> 1) & 1) ^ 1, abort_flag, err);
@@ -411,10 +477,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
         const uint32_t tS = lanes + T::cS + h * 128, tO = lanes + T::cO + h * D, tP = lanes + T::cP + h * T::sP;
         bool ok = true;
         uint32_t n = 0, nh = 0;
-        bool more = e.start(a);
-        for (; more && e.next(a);) {
+        const bool some = e.start(a);
+        for (bool first = true; some && e.next(a, first); first = false) {
+            const int count = e.count, tok0 = e.rt.lo + e.tile0 * kTok;
             if (h * kHalf >= e.rt.n_rows) {                               // no rows in this half
-                n += e.count;
+                n += count;
                 continue;
             }
             const int rr = e.rt.r0 + h * kHalf + row;
@@ -457,8 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
             mbar_arrive(bar(Q_FULL + h));
 
             float M = -INFINITY, L = 0.f;
-            for (int j = 0; j < e.count; ++j, ++n, ++nh) {
-                const int tb = e.rt.lo + (e.tile0 + j) * kTok;
+            for (int j = 0; j < count; ++j, ++n, ++nh) {
+                const int tb = tok0 + j * kTok;
                 const bool got = ok && wait_bar(bar(S_FULL + h), nh & 1, abort_flag, err);
                 ok = __all_sync(0xFFFFFFFFu, got);
                 if (!ok) continue;
@@ -468,33 +535,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                 for (int c = 0; c < 4; ++c) tmem_ld32_nowait(tS + 32 * c, t + 32 * c);
                 const float4 *mt = meta + (n % kMetaRing) * kGroups;
                 tmem_wait_ld();
-                float tmax = -INFINITY;
-                const bool mask = __any_sync(0xFFFFFFFFu, tb + kTok > lim || tb < low);
-                if (mask) {
+                // u_j = t_j - M with the bound so far; what passes it by more than 8 raises the bound
+                const float m0 = M == -INFINITY ? 0.f : M;
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int g = 0; g < kGroups; ++g) {
-                        const float c = kf * mt[g].x, ev = mt[g].y;
+                for (int g = 0; g < kGroups; ++g) {
+                    const float4 f = mt[g];
+                    const uint64_t c2 = pack2(kf * f.x, kf * f.x), e2 = pack2(f.y - m0, f.y - m0);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int tok = tb + 16 * g + i;
-                            const float x = fmaf(t[16 * g + i], c, ev);
-                            t[16 * g + i] = tok < lim && tok >= low ? x : -INFINITY;
-                            tmax = fmaxf(tmax, t[16 * g + i]);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int g = 0; g < kGroups; ++g) {
-                        const float c = kf * mt[g].x, ev = mt[g].y;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            t[16 * g + i] = fmaf(t[16 * g + i], c, ev);
-                            tmax = fmaxf(tmax, t[16 * g + i]);
-                        }
+                    for (int i = 0; i < 8; ++i) {
+                        float &x = t[16 * g + 2 * i], &y = t[16 * g + 2 * i + 1];
+                        unpack2(fma2(pack2(x, y), c2, e2), x, y);
                     }
                 }
-                if (__any_sync(0xFFFFFFFFu, tmax > M + kLazy)) {
-                    const float m2 = fmaxf(M, tmax), f = M == m2 ? 1.f : exp2_approx(M - m2);
+                if (__any_sync(0xFFFFFFFFu, tb + kTok > lim || tb < low)) {
+#pragma unroll
+                    for (int i = 0; i < 128; ++i)
+                        if (tb + i >= lim || tb + i < low) t[i] = -INFINITY;
+                }
+#pragma unroll
+                for (int i = 0; i < 64; ++i) mx[i & 3] = max3(mx[i & 3], t[2 * i], t[2 * i + 1]);
+                const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if (__any_sync(0xFFFFFFFFu, tmax > (M == -INFINITY ? -INFINITY : kLazy))) {
+                    const float m2 = fmaxf(M, m0 + tmax), f = M == m2 ? 1.f : exp2_approx(M - m2);
+                    if (m2 != -INFINITY) {
+                        const float d = m0 - m2;
+#pragma unroll
+                        for (int i = 0; i < 128; ++i) t[i] += d;
+                    }
                     M = m2;
                     L *= f;
                     if (j > 0) {
@@ -512,22 +580,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                         }
                     }
                 }
-                const float m0 = M == -INFINITY ? 0.f : M;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t u[16];
+                    uint64_t sum[2][2] = {};
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        float sum = 0.f;
+                    for (int i = 0; i < 8; ++i)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float x = exp2_approx(t[32 * c + 16 * g + 2 * i] - m0), y = exp2_approx(t[32 * c + 16 * g + 2 * i + 1] - m0);
-                            sum += x + y;
+                        for (int g = 0; g < 2; ++g) {
+                            const float x = exp2_approx(t[32 * c + 16 * g + 2 * i]), y = exp2_approx(t[32 * c + 16 * g + 2 * i + 1]);
+                            sum[g][i & 1] = add2(sum[g][i & 1], pack2(x, y));
                             u[8 * g + i] = pack_f16x2(x, y);
                         }
-                        L = fmaf(sum, mt[2 * c + g].z, L);
-                    }
                     tmem_st16(tP + 16 * c, u);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        float x, y;
+                        unpack2(add2(sum[g][0], sum[g][1]), x, y);
+                        L = fmaf(x + y, mt[2 * c + g].z, L);
+                    }
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -594,30 +665,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                 }
                 asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");
                 if (flags[1 + h]) {
-                    auto at = [&](int64_t c) { return a.ws.part + (c * 2 + (c == first_cta ? 1 : 0)) * T::kPart; };
+                    const float *st = a.ws.part + kRows * D + h * kHalf + row;
+                    const int parts = (int)(last_cta - first_cta) + 1;
+                    auto at = [&](int c) { return ((first_cta + c) * 2 + (c == 0 ? 1 : 0)) * T::kPart; };
                     float m = -INFINITY, l = 0.f;
-                    for (int64_t c = first_cta; c <= last_cta; ++c) {
-                        const float *st = at(c) + kRows * D + h * kHalf + row;
-                        float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-                        join(m, l, none, __ldcg(st), __ldcg(st + kRows), none);
-                    }
+                    for (int c = 0; c < parts; ++c) m = fmaxf(m, __ldcg(st + at(c)));
+                    auto factor = [&](int c) {
+                        const float mc = __ldcg(st + at(c));
+                        return mc == -INFINITY ? (__ldcg(st + at(c) + kRows) == 0.f ? 0.f : 1.f) : exp2_approx(mc - m);
+                    };
+                    for (int c = 0; c < parts; ++c) l = fmaf(__ldcg(st + at(c) + kRows), factor(c), l);
                     const float il = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
-                    for (int c4 = 0; c4 < D; c4 += 16) {
-                        float x[16] = {};
-                        for (int64_t c = first_cta; c <= last_cta; ++c) {
-                            const float *st = at(c) + kRows * D + h * kHalf + row;
-                            const float mc = __ldcg(st), f = mc == -INFINITY ? 1.f : exp2_approx(mc - m);
-                            if (mc == -INFINITY && __ldcg(st + kRows) == 0.f) continue;
-                            const float4 *src = reinterpret_cast<const float4 *>(at(c)) + h * kHalf + row;
+                    for (int d = 0; d < D; d += 64) {                     // 16 float4 in flight
+                        float x[64] = {};
+#pragma unroll 1
+                        for (int c = 0; c < parts; ++c) {
+                            const float f = factor(c);
+                            const float4 *src = reinterpret_cast<const float4 *>(a.ws.part + at(c)) + (d / 4) * kRows + h * kHalf + row;
+                            float4 v[16];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float4 v = __ldcg(src + (c4 / 4 + i) * kRows);
-                                x[4 * i] = fmaf(v.x, f, x[4 * i]), x[4 * i + 1] = fmaf(v.y, f, x[4 * i + 1]);
-                                x[4 * i + 2] = fmaf(v.z, f, x[4 * i + 2]), x[4 * i + 3] = fmaf(v.w, f, x[4 * i + 3]);
+                            for (int i = 0; i < 16; ++i) v[i] = __ldcg(src + i * kRows);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                x[4 * i] = fmaf(v[i].x, f, x[4 * i]), x[4 * i + 1] = fmaf(v[i].y, f, x[4 * i + 1]);
+                                x[4 * i + 2] = fmaf(v[i].z, f, x[4 * i + 2]), x[4 * i + 3] = fmaf(v[i].w, f, x[4 * i + 3]);
                             }
                         }
-                        put(c4, x, il);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) put(d + 16 * i, x + 16 * i, il);
                     }
                     put_lse(m, l);
                 }
@@ -629,7 +705,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    if (warp == 12)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
 template <int TYPE, int D>
