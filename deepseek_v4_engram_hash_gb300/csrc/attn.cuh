@@ -91,9 +91,10 @@ __device__ __forceinline__ void load_v_row(uint32_t vs, int r, int g, uint32_t (
     }
 }
 
-// Bounded wait, without reading the clock when the phase is there already.
+// Bounded wait whose tests sleep until the phase completes or 20 us pass: many
+// warps wait here at a time, and those that test in a loop slow the others down.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err) {
-    return mbar_try(bar, parity) || mbar_wait(bar, parity, abort_flag, err);
+    return mbar_try(bar, parity) || mbar_wait(bar, parity, abort_flag, err, kWaitNs, 20000u);
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint32_t bar) {

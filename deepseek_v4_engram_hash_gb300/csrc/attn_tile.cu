@@ -10,23 +10,26 @@
 // heads of one key/value head) and 128 tokens a step, so a converted key or
 // value tile serves both halves:
 //   warps 0..3, 4..7   softmax of half 0 / 1, one thread a row: scores from tensor
-//                      memory, probabilities back to tensor memory as f16, rescaling
-//                      and the output;
+//                      memory, probabilities back to tensor memory as f16, rescaling and
+//                      the output;
 //   warps 8..11        codes to f16 operand tiles in shared memory (e4m3 to f16 is exact);
 //                      keys and values alike stay [token][dim]: values are the
 //                      MN-major operand of the second product;
-//   warps 12, 14       issue the MMAs of half 0 / 1 (M 128, N 128 / D, K 16): S_h = Q_h K^T,
-//                      O_h += P_h V with P_h from tensor memory;
-//   warp 13            pages, scales and TMA copies of the codes.
-// While one half is in its softmax the tensor cores work for the other.  Tensor
-// memory: S 2 x 128 columns, O 2 x D; P lies over its S for D = 128 (all 512 columns
-// are taken), beside it for D = 64.
+//   warps 12, 14       issue the MMAs of half 0 / 1 (M 128, N 64 / D, K 16): S_h = Q_h K^T
+//                      for 64 tokens at a time, O_h += P_h V with P_h from tensor memory;
+//   warp 13            pages, scales and TMA copies of the codes;
+//   warp 15            the schedule: entries of the list for all others.
+// A half's scores have two buffers of 64 tokens: while one is in its softmax, the tensor
+// cores fill the other and take the probabilities before (a chain of one score buffer a half left
+// them idle for the latencies between product, softmax and product: 432 against 379 us for 4096 tokens behind 4096, 32 query and 8 key/value heads of 128).
+// Tensor memory: S 2 x 2 x 64 columns, O 2 x D; P lies over its S.
 //
 // The call's (sequence, head, row tile, 128-token tile) list is cut evenly
 // over one CTA an SM; ranges that cut a row tile's tokens leave partial
 // results that the last to arrive joins in CTA order.
-// Every wait is bounded (2 s); on expiry ENGRAM_E_TIMEOUT is raised, the roles run
-// out their loops without waiting, and tensor memory is freed.
+// Every wait is bounded (2 s); on expiry ENGRAM_E_TIMEOUT is raised, every role leaves
+// its loops (all waits are on mbarriers, and a warp votes before it branches on one)
+// and tensor memory is freed.
 #include "attn.cuh"
 
 namespace engram {
@@ -38,11 +41,10 @@ using namespace tcg;
 
 constexpr int kHalf = 128;                           // rows of a half
 constexpr int kRows = 2 * kHalf;
-constexpr int kTok = 128;                            // tokens a step
-constexpr int kThreads = 512;
+constexpr int kTok = 128, kPartTok = 64;             // tokens a step, and a score buffer
+constexpr int kThreads = 512, kSoftWarps = 8;
 constexpr int kGroups = kTok / 16;                   // scale groups a step (a page is at least 16 tokens)
 constexpr int kMetaRing = 4;
-constexpr uint32_t kNever = 0x7FFFFFFF;
 
 struct TileParams {
     AttnArgs a;
@@ -62,93 +64,127 @@ __device__ __forceinline__ RowTile row_tile(const AttnArgs &a, const Seq &s, int
     t.tiles = max(1, (min(s.kv, last + 1) - t.lo + kTok - 1) / kTok);
     return t;
 }
+__device__ __forceinline__ int row_tiles(const AttnArgs &a, const Seq &s) { return (s.n * a.group + kRows - 1) / kRows; }
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+// Sum of v over lanes up to this one.
+__device__ __forceinline__ int64_t warp_scan(int64_t v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if ((threadIdx.x & 31) >= o) v += x;
+    }
+    return v;
+}
+// Token tiles of one head of sequence s: by one lane, or by a whole warp.
 __device__ __forceinline__ int64_t head_tiles(const AttnArgs &a, const Seq &s) {
     int64_t n = 0;
-    for (int rt = 0; rt < (s.n * a.group + kRows - 1) / kRows; ++rt) n += row_tile(a, s, rt).tiles;
+    for (int rt = 0; rt < row_tiles(a, s); ++rt) n += row_tile(a, s, rt).tiles;
     return n;
 }
+__device__ __forceinline__ int64_t head_tiles_warp(const AttnArgs &a, const Seq &s) {
+    int64_t n = 0;
+    for (int rt = threadIdx.x & 31; rt < row_tiles(a, s); rt += 32) n += row_tile(a, s, rt).tiles;
+    return warp_sum(n);
+}
 
-// This CTA's range of the list, entry by entry.  Every warp walks it by itself; the
-// walk lies in shared memory (one a warp, stepped by its lane 0), so the roles'
-// inner loops keep their registers.
-struct Walk {
-    int64_t t, end, per, entry_t0;
+// An entry of this CTA's range of the list.
+struct Entry {
     Seq s;
     RowTile rt;
-    int b, head, row_tile_no, tile0, count;
+    int b, head, tile0, count;                       // count 0: no more
+    int first_cta, last_cta;                         // those that share the row tile
+};
+constexpr int kEntries = 4, kEntryUsers = kSoftWarps + 4 + 3;
 
-    // A whole warp calls this.
+// This CTA's range, walked by one warp (start) and its lane 0 (next).
+struct Walk {
+    int64_t t, end, per;
+    Entry e;
+    int row_tile_no;
+
     __device__ __forceinline__ bool start(const AttnArgs &a) {
         const int lane = threadIdx.x & 31;
+        // the sequence that holds this CTA's first tile: up to 32 sequences one by one with the warp on
+        // each one's row tiles, more of them with a lane on each
+        const bool few = a.c.batch <= 32;
         const int lanes_per = (a.c.batch + 31) / 32;
         int64_t mine = 0;
-        for (int j = 0; j < lanes_per; ++j) {
-            const int i = lane * lanes_per + j;
-            if (i < a.c.batch) mine += head_tiles(a, sequence(a.c, i)) * a.c.KH;
-        }
-        int64_t upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-            if (lane >= o) upto += x;
-        }
-        const int64_t total = __shfl_sync(0xFFFFFFFFu, upto, 31);
-        const int64_t p = max((int64_t)1, (total + gridDim.x - 1) / gridDim.x), from = blockIdx.x * p;
-        if (from >= total) return false;
-        const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, from < upto)) - 1;
-        int64_t rel = from - __shfl_sync(0xFFFFFFFFu, upto - mine, owner);
-        if (lane == 0) {
-            b = owner * lanes_per;
-            s = sequence(a.c, b);
-            int64_t per_head = head_tiles(a, s);
-            while (rel >= per_head * a.c.KH && b + 1 < a.c.batch) {
-                rel -= per_head * a.c.KH;
-                s = sequence(a.c, ++b);
-                per_head = head_tiles(a, s);
+        if (few) {
+            for (int i = 0; i < a.c.batch; ++i) {
+                const int64_t n = head_tiles_warp(a, sequence(a.c, i)) * a.c.KH;
+                if (lane == i) mine = n;
             }
-            head = (int)(rel / per_head);
-            rel -= head * per_head;
-            rt = row_tile(a, s, row_tile_no = 0);
-            while (rel >= rt.tiles && rt.r0 + rt.n_rows < s.n * a.group) {
-                rel -= rt.tiles;
-                rt = row_tile(a, s, ++row_tile_no);
+        } else {
+            for (int j = 0; j < lanes_per; ++j) {
+                const int i = lane * lanes_per + j;
+                if (i < a.c.batch) mine += head_tiles(a, sequence(a.c, i)) * a.c.KH;
             }
-            tile0 = (int)rel;
-            t = from;
-            end = min(total, from + p);
-            per = p;
-            count = 0;
         }
+        const int64_t upto = warp_scan(mine), total = __shfl_sync(0xFFFFFFFFu, upto, 31);
+        per = max((int64_t)1, (total + gridDim.x - 1) / gridDim.x);
+        t = blockIdx.x * per;
+        end = min(total, t + per);
+        if (t >= total) return false;
+        const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, t < upto)) - 1;
+        int64_t rel = t - __shfl_sync(0xFFFFFFFFu, upto - mine, owner);
+        e.b = owner * lanes_per;
+        e.s = sequence(a.c, e.b);
+        int64_t per_head = head_tiles_warp(a, e.s);
+        while (rel >= per_head * a.c.KH && e.b + 1 < a.c.batch) {
+            rel -= per_head * a.c.KH;
+            e.s = sequence(a.c, ++e.b);
+            per_head = head_tiles_warp(a, e.s);
+        }
+        e.head = (int)(rel / per_head);
+        rel -= e.head * per_head;
+        // its row tile, 32 at a time
+        row_tile_no = 0;
+        const int n_tiles = row_tiles(a, e.s);
+        for (int r0 = 0; r0 < n_tiles; r0 += 32) {
+            const int64_t n = r0 + lane < n_tiles ? row_tile(a, e.s, r0 + lane).tiles : 0, sum = warp_scan(n);
+            const uint32_t has = __ballot_sync(0xFFFFFFFFu, rel < sum);
+            if (has) {
+                const int l = __ffs(has) - 1;
+                row_tile_no = r0 + l;
+                rel -= __shfl_sync(0xFFFFFFFFu, sum - n, l);
+                break;
+            }
+            rel -= __shfl_sync(0xFFFFFFFFu, sum, 31);
+        }
+        e.rt = row_tile(a, e.s, row_tile_no);
+        e.tile0 = (int)rel;
         return true;
     }
-    // The next entry; `first` on the first call.  A whole warp calls this.
-    __device__ __forceinline__ bool next(const AttnArgs &a, bool first) {
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) {
-            if (!first && t < end) {                  // the entry before ended with its row tile
-                tile0 = 0;
-                if (rt.r0 + rt.n_rows < s.n * a.group) {
-                    rt = row_tile(a, s, ++row_tile_no);
-                } else {
-                    if (++head == a.c.KH) {
-                        head = 0;
-                        do {
-                            if (b + 1 >= a.c.batch) {             // the arrays changed under the call
-                                t = end;
-                                break;
-                            }
-                            s = sequence(a.c, ++b);
-                        } while (s.n == 0);
-                    }
-                    rt = row_tile(a, s, row_tile_no = 0);
-                }
-            }
-            count = (int)min((int64_t)(rt.tiles - tile0), end - t);
-            entry_t0 = t - tile0;
-            t += count;
+    // Completes the entry at t.
+    __device__ __forceinline__ void take() {
+        e.count = (int)min((int64_t)(e.rt.tiles - e.tile0), end - t);
+        const int64_t t0 = t - e.tile0;
+        e.first_cta = (int)(t0 / per);
+        e.last_cta = (int)((t0 + e.rt.tiles - 1) / per);
+        t += e.count;
+    }
+    // Goes to the entry after it, which begins a row tile.
+    __device__ __forceinline__ void next(const AttnArgs &a) {
+        e.tile0 = 0;
+        if (e.rt.r0 + e.rt.n_rows < e.s.n * a.group) {
+            e.rt = row_tile(a, e.s, ++row_tile_no);
+            return;
         }
-        __syncwarp();
-        return count > 0;
+        if (++e.head == a.c.KH) {
+            e.head = 0;
+            do {
+                if (e.b + 1 >= a.c.batch) {                        // the arrays changed under the call
+                    t = end;
+                    return;
+                }
+                e.s = sequence(a.c, ++e.b);
+            } while (e.s.n == 0);
+        }
+        e.rt = row_tile(a, e.s, row_tile_no = 0);
     }
 };
 
@@ -158,13 +194,14 @@ struct Tile {
     static constexpr int kF16 = kTok * D * 2;        // bytes of a converted tile
     static constexpr int kFp8 = kTok * D;            // bytes of a staged tile
     static constexpr int oQ = 0, oK = oQ + 2 * kQ, oV = oK + 2 * kF16, oS = oV + 2 * kF16, oAux = oS + 2 * kFp8;
-    static constexpr int oWalk = 768;                // in aux, behind the scales, barriers and flags
-    static constexpr size_t kSmem = 1024 + oAux + oWalk + 16 * sizeof(Walk);
-    static_assert(kSmem <= 227 * 1024, "shared memory");
+    // behind the tiles (base 1024-aligned): scales, schedule, barriers, flags
+    static constexpr int oMeta = oAux, oEntry = oMeta + kMetaRing * kGroups * 16, oBar = oEntry + kEntries * 64,
+                         oFlag = oBar + 48 * 8;
+    static constexpr size_t kSmem = oFlag + 64;
+    static_assert(kSmem <= 227 * 1024 && sizeof(Entry) <= 64, "shared memory");
     static constexpr int kSub = kTok * 128;          // bytes of a 64-dim sub-tile (128 rows of 128 bytes)
     static constexpr int kPart = kRows * (D + 2);    // floats of a partial result
     static constexpr uint32_t cS = 0, cO = 256;      // tensor-memory columns
-    static constexpr uint32_t cP = D == 128 ? 0 : 384, sP = D == 128 ? 128 : 64;
 };
 
 // Instruction descriptor, kind::f16 with f16 operands and an f32 accumulator;
@@ -255,6 +292,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Uses of these registers stay behind the wait before it.
+__device__ __forceinline__ void pin32(float *r) {
+    asm volatile("" : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31]));
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&u)[16]) {
     asm volatile(
@@ -289,32 +330,41 @@ __device__ __forceinline__ void convert_tile(uint32_t src, uint32_t dst, int wt,
 template <int TYPE, int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_constant__ TileParams p) {
     using T = Tile<D>;
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     const AttnArgs &a = p.a;
-    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-    uint8_t *aux = smem_raw + (base - raw) + T::oAux;
-    float4 *meta = reinterpret_cast<float4 *>(aux);                       // [kMetaRing][kGroups]: 2^ek, ev, 2^-ev, counts
-    const uint32_t bar0 = smem_u32(aux + kMetaRing * kGroups * 16);
-    enum { Q_FULL = 0, ST_FULL = 2, ST_EMPTY = 4, K_FULL = 6, K_EMPTY = 8, V_FULL = 10, V_EMPTY = 12, S_FULL = 14, P_FULL = 16,
-           PV_DONE = 18, DRAIN = 20, BARS = 22 };
-    auto bar = [&](int i) { return bar0 + 8u * i; };
-    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(aux + kMetaRing * kGroups * 16 + BARS * 8);
-    int *flags = reinterpret_cast<int *>(aux + kMetaRing * kGroups * 16 + BARS * 8 + 8);
-    volatile int *abort_flag = flags;
+    const uint32_t base = smem_u32(smem);
+    float4 *meta = reinterpret_cast<float4 *>(smem + T::oMeta);           // [kMetaRing][kGroups]: 2^ek, ev, 2^-ev, counts
+    enum { Q_FULL = 0, ST_FULL = 2, ST_EMPTY = 4, K_FULL = 6, K_EMPTY = 8, V_FULL = 10, V_EMPTY = 12, DRAIN = 14, HALF = 16,
+           S_FULL = 18, P_FULL = 22, PV_DONE = 26, E_FULL = 30, E_EMPTY = 34 };      // [2 halves][2 buffers] from S_FULL to PV_DONE
+    auto bar = [&](int i) { return base + T::oBar + 8u * i; };
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + T::oFlag);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + T::oFlag + 4);
+    volatile int *last_flag = reinterpret_cast<volatile int *>(smem + T::oFlag + 8);           // [2]
+    if (base & 1023u) {                                                   // the swizzles count on it
+        set_err(a.c.err, ENGRAM_E_UNSUPPORTED);
+        return;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(Q_FULL + i), kHalf);
+            mbar_init(bar(Q_FULL + i), 4);
             mbar_init(bar(ST_FULL + i), 1);
-            mbar_init(bar(ST_EMPTY + i), 128);
-            mbar_init(bar(K_FULL + i), 128);
+            mbar_init(bar(ST_EMPTY + i), 4);
+            mbar_init(bar(K_FULL + i), 4);
             mbar_init(bar(K_EMPTY + i), 2);               // both halves' products
-            mbar_init(bar(V_FULL + i), 128);
+            mbar_init(bar(V_FULL + i), 4);
             mbar_init(bar(V_EMPTY + i), 2);
-            mbar_init(bar(S_FULL + i), 1);
-            mbar_init(bar(P_FULL + i), kHalf);
-            mbar_init(bar(PV_DONE + i), 1);
             mbar_init(bar(DRAIN + i), 1);
+            mbar_init(bar(HALF + i), 4);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bar(S_FULL + i), 1);
+            mbar_init(bar(P_FULL + i), 4);
+            mbar_init(bar(PV_DONE + i), 1);
+        }
+        for (int i = 0; i < kEntries; ++i) {
+            mbar_init(bar(E_FULL + i), 1);
+            mbar_init(bar(E_EMPTY + i), kEntryUsers);
         }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -330,36 +380,57 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     int *err = a.c.err;
-    Walk &e = reinterpret_cast<Walk *>(aux + T::oWalk)[warp];
+    // A whole warp waits, and agrees on the outcome.
+    auto wait = [&](int i, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait_bar(bar(i), parity & 1, abort_flag, err)) != 0; };
+    // Entry number i of the CTA, and its release.
+    auto entry = [&](uint32_t i) -> const Entry & { return *reinterpret_cast<const Entry *>(smem + T::oEntry + (i % kEntries) * 64); };
+    auto open = [&](uint32_t i) { return wait(E_FULL + i % kEntries, i / kEntries) && entry(i).count > 0; };
+    auto close = [&](uint32_t i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(E_EMPTY + i % kEntries));
+    };
 
-    // 512 threads launch with 128 registers each: 2 x 128 x 176 + 128 x 88 + 128 x 72 are as many
     if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp == 13) {
+        if (warp == 15) {
+            // ---- the schedule ----
+            Walk w;
+            bool more = w.start(a);
+            for (uint32_t i = 0;; ++i) {
+                if (!wait(E_EMPTY + i % kEntries, i / kEntries + 1)) break;
+                if (more) w.take();
+                else w.e.count = 0;
+                if (lane == 0) *reinterpret_cast<Entry *>(smem + T::oEntry + (i % kEntries) * 64) = w.e;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(E_FULL + i % kEntries));
+                if (!more) break;
+                if (w.t < w.end) w.next(a);
+                more = w.t < w.end;
+            }
+        } else if (warp == 13) {
             // ---- pages, scales, copies ----
-            bool ok = e.start(a);
-            int it = 0;
-            for (bool first = true; ok && e.next(a, first); first = false) {
-                const int tok0 = e.rt.lo + e.tile0 * kTok;
+            bool ok = true;
+            uint32_t it = 0;
+            for (uint32_t i = 0; ok && (ok = open(i)); close(i++)) {
+                const Entry &e = entry(i);
+                const int tok0 = e.rt.lo + e.tile0 * kTok, kv = e.s.kv, b = e.b, head = e.head, count = e.count;
                 const int at = 16 * (lane & 7);
                 const bool leader = lane < 8 && (at & (a.c.pt - 1)) == 0;
                 auto page_at = [&](int j) {
                     const int tok = tok0 + j * kTok + at;
-                    return lane < 8 && j < e.count && tok < e.s.kv ? page_of(a.c, e.b, tok >> a.c.pt_log2) : -1;
+                    return lane < 8 && j < count && tok < kv ? page_of(a.c, b, tok >> a.c.pt_log2) : -1;
                 };
                 auto scales_of = [&](int id) {
                     if (id < 0) return 0u;
-                    const int64_t i = (int64_t)id * a.c.KH + e.head;
-                    return (uint32_t)a.c.k_scales[i] | (uint32_t)a.c.v_scales[i] << 8;
+                    const int64_t k = (int64_t)id * a.c.KH + head;
+                    return (uint32_t)a.c.k_scales[k] | (uint32_t)a.c.v_scales[k] << 8;
                 };
                 int id = page_at(0), id1 = page_at(1);
                 uint32_t sc = scales_of(id);
-                for (int j = 0; j < e.count && ok; ++j, ++it) {
+                for (int j = 0; j < count; ++j, ++it) {
                     const int id2 = page_at(j + 2);
                     const uint32_t sc1 = scales_of(id1);
                     const int page = id < 0 ? a.c.n_pages : id;           // outside the cache: zeros
-                    ok = wait_bar(bar(ST_EMPTY + 0), (it & 1) ^ 1, abort_flag, err);
-                    if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+                    if (!(ok = wait(ST_EMPTY + 0, it + 1))) break;
                     if (lane < 8)
                         meta[(it % kMetaRing) * kGroups + lane] =
                             id < 0 ? make_float4(1.f, -INFINITY, 0.f, 0.f)
@@ -368,12 +439,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                     __syncwarp();
                     if (lane == 0) mbar_expect_tx(bar(ST_FULL + 0), T::kFp8);
                     __syncwarp();
-                    if (leader) tma_load_4d(base + T::oS + at * D, &p.mk, 0, (tok0 + at) & (a.c.pt - 1), e.head, page, bar(ST_FULL + 0));
-                    ok = wait_bar(bar(ST_EMPTY + 1), (it & 1) ^ 1, abort_flag, err);
-                    if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+                    if (leader) tma_load_4d(base + T::oS + at * D, &p.mk, 0, (tok0 + at) & (a.c.pt - 1), head, page, bar(ST_FULL + 0));
+                    if (!(ok = wait(ST_EMPTY + 1, it + 1))) {
+                        ++it;
+                        break;
+                    }
                     if (lane == 0) mbar_expect_tx(bar(ST_FULL + 1), T::kFp8);
                     __syncwarp();
-                    if (leader) tma_load_4d(base + T::oS + T::kFp8 + at * D, &p.mv, 0, (tok0 + at) & (a.c.pt - 1), e.head, page, bar(ST_FULL + 1));
+                    if (leader) tma_load_4d(base + T::oS + T::kFp8 + at * D, &p.mv, 0, (tok0 + at) & (a.c.pt - 1), head, page, bar(ST_FULL + 1));
                     id = id1;
                     sc = sc1;
                     id1 = id2;
@@ -381,323 +454,338 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
             }
             // every copy issued has landed before the CTA can leave (only an abort leaves one behind)
             const uint64_t t0 = now_ns();
-            for (int i = 0; i < 2; ++i)
-                while (it > 0 && !mbar_try(bar(ST_FULL + i), (it - 1) & 1) && now_ns() - t0 < 10000000ull) {
+            for (int x = 0; x < 2; ++x)
+                while (it > 0 && !mbar_try(bar(ST_FULL + x), (it - 1) & 1) && now_ns() - t0 < 10000000ull) {
                 }
-        } else if (warp != 15) {
-            // ---- the tensor cores: warp 12 for half 0, warp 14 for half 1 ----
+        } else {
+            // ---- the tensor cores ----
             const int h = (warp - 12) >> 1;
-            bool ok = e.start(a);
-            uint32_t n = 0, nh = 0, ent = 0;                              // steps, steps with rows in this half, such entries
+            bool ok = true;
+            uint32_t n = 0, ns = 0, ent = 0;                              // tiles, score buffers of this half, its entries
             const uint32_t q_lo = desc_lo(base + T::oQ + h * T::kQ, 16);
-            const uint32_t tS = tmem + T::cS + h * 128, tO = tmem + T::cO + h * D, tP = tmem + T::cP + h * T::sP;
-            for (bool first = true; ok && e.next(a, first); first = false) {
-                const int count = e.count;
-                const bool both = e.rt.n_rows > kHalf;
-                if (h && !both) {
+            const uint32_t tS = tmem + T::cS + h * 128, tO = tmem + T::cO + h * D;
+            // the scores of 64 tokens, part s & 1 of tile n, into buffer s & 1
+            auto qk = [&](uint32_t s, uint32_t tile) {
+                tc_fence_after();
+                if (elect()) {
+                    const uint32_t k_lo = desc_lo(base + T::oK + (tile & 1) * T::kF16 + (s & 1) * (kPartTok * 128), 16);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk >> 2) * T::kSub + (kk & 3) * 32) >> 4;
+                        mma_ss<idesc_f16(kHalf, kPartTok, false)>(tS + (s & 1) * kPartTok, q_lo + off, k_lo + off, kk != 0);
+                    }
+                    commit(bar(S_FULL + 2 * h + (s & 1)));
+                    if (s & 1) commit(bar(K_EMPTY + (tile & 1)));
+                }
+                __syncwarp();
+            };
+            for (uint32_t i = 0; ok && (ok = open(i)); close(i++)) {
+                const int count = entry(i).count;
+                if (h && entry(i).rt.n_rows <= kHalf) {
                     // no rows in this half: keep step with the converted tiles (their barriers count both halves)
-                    for (int j = 0; j < count && ok; ++j, ++n) {
-                        ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(K_FULL + (n & 1)), (n >> 1) & 1, abort_flag, err));
-                        if (ok && lane == 0) mbar_arrive(bar(K_EMPTY + (n & 1)));
-                        ok = ok && __all_sync(0xFFFFFFFFu, wait_bar(bar(V_FULL + (n & 1)), (n >> 1) & 1, abort_flag, err));
-                        if (ok && lane == 0) mbar_arrive(bar(V_EMPTY + (n & 1)));
+                    for (int j = 0; j < count; ++j, ++n) {
+                        if (!(ok = wait(K_FULL + (n & 1), n >> 1))) break;
+                        if (lane == 0) mbar_arrive(bar(K_EMPTY + (n & 1)));
+                        if (!(ok = wait(V_FULL + (n & 1), n >> 1))) break;
+                        if (lane == 0) mbar_arrive(bar(V_EMPTY + (n & 1)));
                     }
                     continue;
                 }
-                ok = __all_sync(0xFFFFFFFFu, wait_bar(bar(Q_FULL + h), ent++ & 1, abort_flag, err));
-                for (int j = 0; j < count && ok; ++j, ++n, ++nh) {
-                    // scores: over this half's last probabilities (D = 128), so their product has to be done
-                    ok = wait_bar(bar(K_FULL + (n & 1)), (n >> 1) & 1, abort_flag, err) &&
-                         (D == 64 || j == 0 || wait_bar(bar(PV_DONE + h), (nh - 1) & 1, abort_flag, err));
-                    ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!(ok = wait(Q_FULL + h, ent++) && wait(K_FULL + (n & 1), n >> 1))) continue;
+                qk(0, n);
+                qk(1, n);
+                for (int s = 0; s < 2 * count; ++s, ++ns) {
+                    ok = ((s & 1) || wait(V_FULL + (n & 1), n >> 1)) && wait(P_FULL + 2 * h + (s & 1), ns >> 1);
                     if (!ok) break;
                     tc_fence_after();
                     if (elect()) {
-                        const uint32_t k_lo = desc_lo(base + T::oK + (n & 1) * T::kF16, 16);
+                        const uint32_t v_lo = desc_lo(base + T::oV + (n & 1) * T::kF16 + (s & 1) * (kPartTok * 128), T::kSub);
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t off = ((kk >> 2) * T::kSub + (kk & 3) * 32) >> 4;
-                            mma_ss<idesc_f16(kHalf, kTok, false)>(tS, q_lo + off, k_lo + off, kk != 0);
-                        }
-                        commit(bar(S_FULL + h));
-                        commit(bar(K_EMPTY + (n & 1)));
+                        for (int kk = 0; kk < kPartTok / 16; ++kk)
+                            mma_ts<idesc_f16(kHalf, D, true)>(tO, tS + (s & 1) * kPartTok + kk * 8, v_lo + kk * (2048 >> 4), (s | kk) != 0);
+                        commit(bar(PV_DONE + 2 * h + (s & 1)));
+                        if (s & 1) commit(bar(V_EMPTY + (n & 1)));
                     }
                     __syncwarp();
-                    ok = wait_bar(bar(V_FULL + (n & 1)), (n >> 1) & 1, abort_flag, err) &&
-                         wait_bar(bar(P_FULL + h), nh & 1, abort_flag, err);
-                    ok = __all_sync(0xFFFFFFFFu, ok);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (elect()) {
-                        const uint32_t v_lo = desc_lo(base + T::oV + (n & 1) * T::kF16, T::kSub);
-                        mma_ts<idesc_f16(kHalf, D, true)>(tO, tP, v_lo, j != 0);
-#pragma unroll
-                        for (int kk = 1; kk < kTok / 16; ++kk)
-                            mma_ts<idesc_f16(kHalf, D, true)>(tO, tP + kk * 8, v_lo + kk * (2048 >> 4), true);
-                        commit(bar(PV_DONE + h));
-                        commit(bar(V_EMPTY + (n & 1)));
+                    if (s + 2 < 2 * count) {
+                        // the buffer's next scores go over these probabilities: their product has to be done
+                        ok = ((s & 1) || wait(K_FULL + ((n + 1) & 1), (n + 1) >> 1)) && wait(PV_DONE + 2 * h + (s & 1), ns >> 1);
+                        if (!ok) break;
+                        qk(s, n + 1);
                     }
-                    __syncwarp();
+                    n += s & 1;
                 }
             }
+            __syncwarp();
             if (elect()) commit(bar(DRAIN + h));                          // from the lane that issued the MMAs
             const uint64_t t0 = now_ns();
             while (!mbar_try(bar(DRAIN + h), 0) && now_ns() - t0 < 100000000ull) {
             }
             __syncwarp();
         }
-    } else if (warp >= 8) {
+    } else if (warp >= kSoftWarps) {
         // ---- codes to f16 ----
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        const int wt = threadIdx.x - 256;
-        bool ok = e.start(a);
+        const int wt = threadIdx.x - 32 * kSoftWarps;
+        bool ok = true;
         uint32_t n = 0;
-        for (bool first = true; ok && e.next(a, first); first = false) {
-            const int left = e.s.kv - (e.rt.lo + e.tile0 * kTok), count = e.count;
-            for (int j = 0; j < count; ++j, ++n) {
+        for (uint32_t i = 0; ok && (ok = open(i)); close(i++)) {
+            const int left = entry(i).s.kv - (entry(i).rt.lo + entry(i).tile0 * kTok), count = entry(i).count;
+            for (int j = 0; j < count && ok; ++j, ++n) {
                 const int valid = left - j * kTok;                        // tokens of the tile that exist
-                for (int x = 0; x < 2 && ok; ++x) {
-                    ok = wait_bar(bar(ST_FULL + x), n & 1, abort_flag, err) &&
-                         wait_bar(bar((x ? V_EMPTY : K_EMPTY) + (n & 1)), ((n >> 1) & 1) ^ 1, abort_flag, err);
-                    if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+                for (int x = 0; x < 2; ++x) {
+                    ok = wait(ST_FULL + x, n) && wait((x ? V_EMPTY : K_EMPTY) + (n & 1), (n >> 1) + 1);
+                    if (!ok) break;
                     convert_tile<D>(base + T::oS + x * T::kFp8, base + (x ? T::oV : T::oK) + (n & 1) * T::kF16, wt, x != 0, valid,
                                     meta + (n % kMetaRing) * kGroups);
                     fence_async_smem();
-                    mbar_arrive(bar(ST_EMPTY + x));
-                    mbar_arrive(bar((x ? V_FULL : K_FULL) + (n & 1)));
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(ST_EMPTY + x));
+                        mbar_arrive(bar((x ? V_FULL : K_FULL) + (n & 1)));
+                    }
                 }
-                if (!ok) break;
             }
         }
     } else {
         // ---- softmax, one thread a row ----
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         const int h = warp >> 2, row = (warp & 3) * 32 + lane;            // row of the half = tensor-memory lane
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t tS = lanes + T::cS + h * 128, tO = lanes + T::cO + h * D, tP = lanes + T::cP + h * T::sP;
+        const uint32_t tO = lanes + T::cO + h * D;
+        uint32_t n = 0, ns = 0, half_syncs = 0;                          // tiles, score buffers of this half
+        auto half_sync = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(HALF + h));
+            return wait(HALF + h, half_syncs++);
+        };
         bool ok = true;
-        uint32_t n = 0, nh = 0;
-        const bool some = e.start(a);
-        for (bool first = true; some && e.next(a, first); first = false) {
-            const int count = e.count, tok0 = e.rt.lo + e.tile0 * kTok;
+        for (uint32_t i = 0; ok && (ok = open(i)); close(i++)) {
+            const Entry &e = entry(i);
+            const int count = e.count;
             if (h * kHalf >= e.rt.n_rows) {                               // no rows in this half
                 n += count;
                 continue;
             }
-            const int rr = e.rt.r0 + h * kHalf + row;
-            const bool live = h * kHalf + row < e.rt.n_rows;
-            const int tok_i = rr / a.group, pos = e.s.kv - e.s.n + tok_i;
-            const int lim = live ? pos + 1 : (int)kNever, low = live && a.window ? pos - a.window + 1 : 0;
+            // the columns of the buffer that the row sees: lo_col <= column < hi_col, moving with the step
+            int hi_col, lo_col, moving;
             float kf;
             {
-                const int64_t at = (int64_t)(e.s.row0 + tok_i) * a.q_stride + (int64_t)(e.head * a.group + rr % a.group) * D;
-                uint32_t m = 0, w[D / 2];
-                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + at);
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 x = live ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-                    w[4 * c] = x.x, w[4 * c + 1] = x.y, w[4 * c + 2] = x.z, w[4 * c + 3] = x.w;
-                }
-                auto pair = [&](uint32_t u) {
+                const int rr = e.rt.r0 + h * kHalf + row, tok_i = rr / a.group;
+                const bool live = h * kHalf + row < e.rt.n_rows;
+                const int64_t q_row = e.s.row0 + tok_i;
+                const int q_head = e.head * a.group + rr - tok_i * a.group;
+                const int pos = e.s.kv - e.s.n + tok_i, tb0 = e.rt.lo + e.tile0 * kTok;
+                moving = live ? kPartTok : 0;
+                hi_col = live ? pos + 1 - tb0 : kPartTok;
+                lo_col = live && a.window ? pos - a.window + 1 - tb0 : 0;
+                // the row's largest element, then the row as f16
+                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + q_row * a.q_stride + (int64_t)q_head * D);
+                auto pair_of = [&](uint32_t u) {
                     return TYPE == ENGRAM_T_BF16 ? make_float2(bf16_lo(u), bf16_hi(u)) : __half22float2(*reinterpret_cast<__half2 *>(&u));
                 };
+                uint32_t m = 0;
+#pragma unroll 2
+                for (int k = 0; k < D / 8; ++k) {
+                    const uint4 x = live ? src[k] : make_uint4(0u, 0u, 0u, 0u);
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int i = 0; i < D / 2; ++i) {
-                    const float2 f = pair(w[i]);
-                    m = max(m, max(__float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu));
+                    for (int q = 0; q < 4; ++q) {
+                        const float2 f = pair_of(w[q]);
+                        m = max(m, max(__float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu));
+                    }
                 }
                 float down;
                 q_scale(m, a.scale_log2, down, kf);
                 const uint32_t dst = base + T::oQ + h * T::kQ + row * 128;
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
+#pragma unroll 2
+                for (int k = 0; k < D / 8; ++k) {
+                    const uint4 x = live ? src[k] : make_uint4(0u, 0u, 0u, 0u);
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
                     uint32_t o[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 f = pair(w[4 * c + i]);
-                        o[i] = pack_f16x2(f.x * down, f.y * down);
+                    for (int q = 0; q < 4; ++q) {
+                        const float2 f = pair_of(w[q]);
+                        o[q] = pack_f16x2(f.x * down, f.y * down);
                     }
-                    sts128(dst + (c >> 3) * T::kSub + (((c & 7) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
+                    sts128(dst + (k >> 3) * T::kSub + (((k & 7) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
                 }
             }
             fence_async_smem();
-            mbar_arrive(bar(Q_FULL + h));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(Q_FULL + h));
 
             float M = -INFINITY, L = 0.f;
-            for (int j = 0; j < count; ++j, ++n, ++nh) {
-                const int tb = tok0 + j * kTok;
-                const bool got = ok && wait_bar(bar(S_FULL + h), nh & 1, abort_flag, err);
-                ok = __all_sync(0xFFFFFFFFu, got);
-                if (!ok) continue;
+            for (int j = 0; j < 2 * count; ++j, ++ns, hi_col -= moving, lo_col -= moving) {
+                const uint32_t tS = lanes + T::cS + h * 128 + (j & 1) * kPartTok;
+                if (!(ok = wait(S_FULL + 2 * h + (j & 1), ns >> 1))) break;
                 tc_fence_after();
-                float t[128];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32_nowait(tS + 32 * c, t + 32 * c);
-                const float4 *mt = meta + (n % kMetaRing) * kGroups;
-                tmem_wait_ld();
                 // u_j = t_j - M with the bound so far; what passes it by more than 8 raises the bound
-                const float m0 = M == -INFINITY ? 0.f : M;
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                const float4 *mt = meta + (n % kMetaRing) * kGroups + (j & 1) * (kGroups / 2);
+                float t[64];
 #pragma unroll
-                for (int g = 0; g < kGroups; ++g) {
+                for (int b = 0; b < 2; ++b) tmem_ld32_nowait(tS + 32 * b, t + 32 * b);
+                tmem_wait_ld();
+#pragma unroll
+                for (int b = 0; b < 2; ++b) pin32(t + 32 * b);
+                const float m0 = M == -INFINITY ? 0.f : M;
+#pragma unroll
+                for (int g = 0; g < kGroups / 2; ++g) {
                     const float4 f = mt[g];
                     const uint64_t c2 = pack2(kf * f.x, kf * f.x), e2 = pack2(f.y - m0, f.y - m0);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float &x = t[16 * g + 2 * i], &y = t[16 * g + 2 * i + 1];
+                    for (int k = 0; k < 8; ++k) {
+                        float &x = t[16 * g + 2 * k], &y = t[16 * g + 2 * k + 1];
                         unpack2(fma2(pack2(x, y), c2, e2), x, y);
                     }
                 }
-                if (__any_sync(0xFFFFFFFFu, tb + kTok > lim || tb < low)) {
+                if (__any_sync(0xFFFFFFFFu, hi_col < kPartTok || lo_col > 0)) {
 #pragma unroll
-                    for (int i = 0; i < 128; ++i)
-                        if (tb + i >= lim || tb + i < low) t[i] = -INFINITY;
+                    for (int k = 0; k < kPartTok; ++k)
+                        if (k >= hi_col || k < lo_col) t[k] = -INFINITY;
                 }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int i = 0; i < 64; ++i) mx[i & 3] = max3(mx[i & 3], t[2 * i], t[2 * i + 1]);
+                for (int k = 0; k < kPartTok / 2; ++k) mx[k & 3] = max3(mx[k & 3], t[2 * k], t[2 * k + 1]);
                 const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 if (__any_sync(0xFFFFFFFFu, tmax > (M == -INFINITY ? -INFINITY : kLazy))) {
                     const float m2 = fmaxf(M, m0 + tmax), f = M == m2 ? 1.f : exp2_approx(M - m2);
                     if (m2 != -INFINITY) {
                         const float d = m0 - m2;
 #pragma unroll
-                        for (int i = 0; i < 128; ++i) t[i] += d;
+                        for (int k = 0; k < kPartTok; ++k) t[k] += d;
                     }
                     M = m2;
                     L *= f;
                     if (j > 0) {
-                        const bool done = wait_bar(bar(PV_DONE + h), (nh - 1) & 1, abort_flag, err);
-                        ok = __all_sync(0xFFFFFFFFu, done);
-                        if (!ok) continue;
+                        if (!(ok = wait(PV_DONE + 2 * h + (j + 1 & 1), (ns - 1) >> 1))) break;
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 16) {
+                        for (int d = 0; d < D; d += 16) {
                             uint32_t o[16];
-                            tmem_ld16(tO + c, o);
+                            tmem_ld16(tO + d, o);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                            tmem_st16(tO + c, o);
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_st16(tO + d, o);
                         }
                     }
                 }
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int b = 0; b < 2; ++b) {
                     uint32_t u[16];
                     uint64_t sum[2][2] = {};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
+                    for (int k = 0; k < 8; ++k)
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
-                            const float x = exp2_approx(t[32 * c + 16 * g + 2 * i]), y = exp2_approx(t[32 * c + 16 * g + 2 * i + 1]);
-                            sum[g][i & 1] = add2(sum[g][i & 1], pack2(x, y));
-                            u[8 * g + i] = pack_f16x2(x, y);
+                            const float x = exp2_approx(t[32 * b + 16 * g + 2 * k]), y = exp2_approx(t[32 * b + 16 * g + 2 * k + 1]);
+                            sum[g][k & 1] = add2(sum[g][k & 1], pack2(x, y));
+                            u[8 * g + k] = pack_f16x2(x, y);
                         }
-                    tmem_st16(tP + 16 * c, u);
+                    tmem_st16(tS + 16 * b, u);
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         float x, y;
                         unpack2(add2(sum[g][0], sum[g][1]), x, y);
-                        L = fmaf(x + y, mt[2 * c + g].z, L);
+                        L = fmaf(x + y, mt[2 * b + g].z, L);
                     }
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(bar(P_FULL + h));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(P_FULL + 2 * h + (j & 1)));
+                n += j & 1;
             }
+            if (!ok) continue;
 
             // the entry's result, or a part of it
-            if (ok) {
-                const bool done = wait_bar(bar(PV_DONE + h), (nh - 1) & 1, abort_flag, err);
-                ok = __all_sync(0xFFFFFFFFu, done);
-                tc_fence_after();
-            }
-            const int64_t first_cta = e.entry_t0 / e.per, last_cta = (e.entry_t0 + e.rt.tiles - 1) / e.per;
-            const bool alone = first_cta == last_cta;
-            const int64_t out_at = (int64_t)(e.s.row0 + tok_i) * a.out_stride + (int64_t)(e.head * a.group + rr % a.group) * D;
-            const float inv = L == 0.f ? 0.f : 1.f / L;
-            auto put = [&](int c, const float *x, float f) {              // 16 values from dim c
+            if (!(ok = wait(PV_DONE + 2 * h + 1, (ns - 1) >> 1))) continue;   // the last product, and all before it
+            tc_fence_after();
+            const bool alone = e.first_cta == e.last_cta;
+            const int rr = e.rt.r0 + h * kHalf + row, tok_i = rr / a.group;
+            const bool live = h * kHalf + row < e.rt.n_rows;
+            const int64_t q_row = e.s.row0 + tok_i;
+            const int q_head = e.head * a.group + rr - tok_i * a.group;
+            uint16_t *out = static_cast<uint16_t *>(a.out) + q_row * a.out_stride + (int64_t)q_head * D;
+            auto put = [&](int d, const float *x, float f) {              // 16 values from dim d
                 if (!live) return;
                 uint32_t w[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    w[i] = TYPE == ENGRAM_T_BF16 ? pack_bf16x2(x[2 * i] * f, x[2 * i + 1] * f) : pack_f16x2(x[2 * i] * f, x[2 * i + 1] * f);
-                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + out_at + c);
+                for (int k = 0; k < 8; ++k)
+                    w[k] = TYPE == ENGRAM_T_BF16 ? pack_bf16x2(x[2 * k] * f, x[2 * k + 1] * f) : pack_f16x2(x[2 * k] * f, x[2 * k + 1] * f);
+                uint4 *dst = reinterpret_cast<uint4 *>(out + d);
                 dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
                 dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
             };
             auto put_lse = [&](float m, float l) {
-                if (live && a.lse)
-                    a.lse[(int64_t)(e.s.row0 + tok_i) * a.H + e.head * a.group + rr % a.group] =
-                        l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                if (live && a.lse) a.lse[q_row * a.H + q_head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
             };
-            const int64_t slot = (int64_t)blockIdx.x * 2 + (blockIdx.x == first_cta ? 1 : 0);
+            const float inv = L == 0.f ? 0.f : 1.f / L;
             // partial results are column-major: float4 d4 of row r at [d4][r]
-            float4 *part = reinterpret_cast<float4 *>(a.ws.part + slot * T::kPart) + h * kHalf + row;
-            float *stat = a.ws.part + slot * T::kPart + kRows * D + h * kHalf + row;
-            if (ok) {
+            const int64_t slot = (int64_t)blockIdx.x * 2 + ((int)blockIdx.x == e.first_cta ? 1 : 0);
+            const int of = 4 * (h * kHalf + row);
 #pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                    uint32_t o[16];
-                    tmem_ld16(tO + c, o);
-                    float x[16];
+            for (int d = 0; d < D; d += 16) {
+                uint32_t o[16];
+                tmem_ld16(tO + d, o);
+                float x[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(o[i]);
-                    if (alone) {
-                        put(c, x, inv);
-                    } else {
+                for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(o[k]);
+                if (alone) {
+                    put(d, x, inv);
+                } else {
+                    float4 *part = reinterpret_cast<float4 *>(a.ws.part + slot * T::kPart + of) + d / 4 * kRows;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) part[(c / 4 + i) * kRows] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-                    }
+                    for (int k = 0; k < 4; ++k) part[k * kRows] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
                 }
-                if (alone) put_lse(M, L);
-                else stat[0] = M, stat[kRows] = L;
             }
             tc_fence_before();                                            // the sums are read: the next entry may overwrite them
-            if (!alone) {
+            if (alone) {
+                put_lse(M, L);
+                continue;
+            }
+            float *stat = a.ws.part + slot * T::kPart + kRows * D + h * kHalf + row;
+            stat[0] = L == 0.f ? -INFINITY : M;
+            stat[kRows] = L;
+            __threadfence();
+            if (!(ok = half_sync())) continue;
+            if ((warp & 3) == 0 && lane == 0) {
+                int *arrived = a.ws.arrived + e.first_cta * 2 + h;
+                const bool last = atomicAdd(arrived, 1) == e.last_cta - e.first_cta;
+                if (last) *arrived = 0;
+                last_flag[h] = last;
                 __threadfence();
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");
-                if ((threadIdx.x & 127) == 0) {
-                    int *arrived = a.ws.arrived + first_cta * 2 + h;
-                    const bool last = atomicAdd(arrived, 1) == (int)(last_cta - first_cta);
-                    if (last) *arrived = 0;
-                    flags[1 + h] = last;
-                    __threadfence();
-                }
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");
-                if (flags[1 + h]) {
-                    const float *st = a.ws.part + kRows * D + h * kHalf + row;
-                    const int parts = (int)(last_cta - first_cta) + 1;
-                    auto at = [&](int c) { return ((first_cta + c) * 2 + (c == 0 ? 1 : 0)) * T::kPart; };
-                    float m = -INFINITY, l = 0.f;
-                    for (int c = 0; c < parts; ++c) m = fmaxf(m, __ldcg(st + at(c)));
-                    auto factor = [&](int c) {
-                        const float mc = __ldcg(st + at(c));
-                        return mc == -INFINITY ? (__ldcg(st + at(c) + kRows) == 0.f ? 0.f : 1.f) : exp2_approx(mc - m);
-                    };
-                    for (int c = 0; c < parts; ++c) l = fmaf(__ldcg(st + at(c) + kRows), factor(c), l);
-                    const float il = l == 0.f ? 0.f : 1.f / l;
+            }
+            if (!(ok = half_sync())) continue;
+            if (last_flag[h]) {
+                const float *st = a.ws.part + kRows * D + h * kHalf + row;
+                const int parts = e.last_cta - e.first_cta + 1;
+                auto at = [&](int k) { return ((int64_t)(e.first_cta + k) * 2 + (k == 0 ? 1 : 0)) * T::kPart; };
+                float m = -INFINITY, l = 0.f;
+                for (int k = 0; k < parts; ++k) m = fmaxf(m, __ldcg(st + at(k)));
+                auto factor = [&](int k) {
+                    const float mk = __ldcg(st + at(k));
+                    return mk == -INFINITY ? (__ldcg(st + at(k) + kRows) == 0.f ? 0.f : 1.f) : exp2_approx(mk - m);
+                };
+                for (int k = 0; k < parts; ++k) l = fmaf(__ldcg(st + at(k) + kRows), factor(k), l);
+                const float il = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
-                    for (int d = 0; d < D; d += 64) {                     // 16 float4 in flight
-                        float x[64] = {};
+                for (int d = 0; d < D; d += 16) {
+                    float x[16] = {};
 #pragma unroll 1
-                        for (int c = 0; c < parts; ++c) {
-                            const float f = factor(c);
-                            const float4 *src = reinterpret_cast<const float4 *>(a.ws.part + at(c)) + (d / 4) * kRows + h * kHalf + row;
-                            float4 v[16];
+                    for (int k = 0; k < parts; ++k) {
+                        const float f = factor(k);
+                        const float4 *src = reinterpret_cast<const float4 *>(a.ws.part + at(k) + of) + d / 4 * kRows;
+                        float4 v[4];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) v[i] = __ldcg(src + i * kRows);
+                        for (int q = 0; q < 4; ++q) v[q] = __ldcg(src + q * kRows);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                x[4 * i] = fmaf(v[i].x, f, x[4 * i]), x[4 * i + 1] = fmaf(v[i].y, f, x[4 * i + 1]);
-                                x[4 * i + 2] = fmaf(v[i].z, f, x[4 * i + 2]), x[4 * i + 3] = fmaf(v[i].w, f, x[4 * i + 3]);
-                            }
+                        for (int q = 0; q < 4; ++q) {
+                            x[4 * q] = fmaf(v[q].x, f, x[4 * q]), x[4 * q + 1] = fmaf(v[q].y, f, x[4 * q + 1]);
+                            x[4 * q + 2] = fmaf(v[q].z, f, x[4 * q + 2]), x[4 * q + 3] = fmaf(v[q].w, f, x[4 * q + 3]);
                         }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) put(d + 16 * i, x + 16 * i, il);
                     }
-                    put_lse(m, l);
+                    put(d, x, il);
                 }
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");   // flags[1 + h] is read
+                put_lse(m, l);
             }
         }
     }
