@@ -6,8 +6,10 @@
 // the block's earlier scale give the block's scale, and the codes go out; the
 // page's earlier codes are read and encoded again only when the scale grew.
 // One group of threads owns a unit, so nothing is shared between units and no
-// order matters.  Further blocks rotate the queries, one row each.
-// Bound by memory for prompts and by launch and load latency for single tokens.
+// order matters.  Further blocks rotate the queries.
+// Bound by memory for prompts and by launch and load latency for single tokens.  64 registers a thread
+// keep 1024 threads on an SM: a 4096-token prompt of 32 query and 8 key/value heads of
+// 128 (94 MB, 13.9 us at the copy rate) takes 22.3 us; without the bound 26.6 us.
 #include "sublayer.cuh"
 
 namespace engram {
@@ -74,42 +76,67 @@ __device__ __forceinline__ bool find_slot(const AppendArgs &a, int slot, int &b,
     return true;
 }
 
-// Eight elements from dim0 of the head at `base`, rotated to position pos.
+// Sixteen elements of a head, as two chunks of eight: item j of a head that rotates
+// by halves has the elements 8j.. and their partners rot / 2 + 8j.., past rot and
+// in every other case 16 consecutive ones.
+enum { kPlain = 0, kHalves = 1, kAdjacent = 2 };
+struct Item {
+    int c0, c1, turn;
+};
+__device__ __forceinline__ Item item_of(const AppendArgs &a, int j, bool turn) {
+    if (turn && !a.interleaved && 16 * j < a.rot) return {8 * j, (a.rot >> 1) + 8 * j, kHalves};
+    return {16 * j, 16 * j + 8, turn && 16 * j < a.rot ? kAdjacent : kPlain};
+}
+// The (cos, sin) pairs of an item at a position: eight of them (kHalves: elements c0 .. c0 + 7; kAdjacent: 16 elements from c0).
+__device__ __forceinline__ void load_angles(const AppendArgs &a, const Item &it, int64_t pos, float (&t)[16]) {
+    if (it.turn == kPlain) return;
+    const float *cs = a.rope + pos * a.rot + (it.turn == kHalves ? 2 * it.c0 : it.c0);
+    float u[8], w[8];
+    load8<ENGRAM_T_F32>(cs, 0, u);
+    load8<ENGRAM_T_F32>(cs, 8, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = u[e], t[8 + e] = w[e];
+}
 template <int TYPE>
-__device__ __forceinline__ void load_rotated(const AppendArgs &a, const void *p, int64_t base, int dim0, int64_t pos,
-                                             bool turn, float (&x)[8]) {
-    load8<TYPE>(p, base + dim0, x);
-    if (!turn || dim0 >= a.rot) return;
-    const float *cs = a.rope + pos * a.rot;                        // rot / 2 pairs
-    if (a.interleaved) {
-        float t[8];
-        load8<ENGRAM_T_F32>(cs, dim0, t);
+__device__ __forceinline__ void load_item(const void *p, int64_t base, const Item &it, float (&x)[8], float (&y)[8]) {
+    load8<TYPE>(p, base + it.c0, x);
+    load8<TYPE>(p, base + it.c1, y);
+}
+__device__ __forceinline__ void rotate(const Item &it, const float (&t)[16], float (&x)[8], float (&y)[8]) {
+    if (it.turn == kHalves) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float c = t[2 * e], s = t[2 * e + 1], u = x[e], w = y[e];
+            x[e] = __fsub_rn(__fmul_rn(u, c), __fmul_rn(w, s));
+            y[e] = __fadd_rn(__fmul_rn(w, c), __fmul_rn(u, s));
+        }
+    } else if (it.turn == kAdjacent) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float c = t[2 * e], s = t[2 * e + 1], u = x[2 * e], w = x[2 * e + 1];
             x[2 * e] = __fsub_rn(__fmul_rn(u, c), __fmul_rn(w, s));
             x[2 * e + 1] = __fadd_rn(__fmul_rn(w, c), __fmul_rn(u, s));
-        }
-    } else {
-        const int half = a.rot >> 1;
-        const bool upper = dim0 >= half;
-        const int d = upper ? dim0 - half : dim0;
-        float y[8], t[8], t2[8];
-        load8<TYPE>(p, base + (upper ? d : d + half), y);
-        load8<ENGRAM_T_F32>(cs, 2 * d, t);
-        load8<ENGRAM_T_F32>(cs, 2 * d + 8, t2);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float c = e < 4 ? t[2 * e] : t2[2 * e - 8], s = e < 4 ? t[2 * e + 1] : t2[2 * e - 7];
-            x[e] = upper ? __fadd_rn(__fmul_rn(x[e], c), __fmul_rn(y[e], s))
-                         : __fsub_rn(__fmul_rn(x[e], c), __fmul_rn(y[e], s));
+            const float c2 = t[8 + 2 * e], s2 = t[9 + 2 * e], u2 = y[2 * e], w2 = y[2 * e + 1];
+            y[2 * e] = __fsub_rn(__fmul_rn(u2, c2), __fmul_rn(w2, s2));
+            y[2 * e + 1] = __fadd_rn(__fmul_rn(w2, c2), __fmul_rn(u2, s2));
         }
     }
 }
 
-// One row of queries.  A thread writes what it read (both halves of its pairs), so q_out may be q.
+// Query rows, `per` of a block at a time: a thread keeps its place in a head (and its angles) and goes
+// through the heads, the first loaded beside the row's sequence and angles.  It writes what it read alone, so q_out may be q.
 template <int TYPE>
-__device__ __forceinline__ void query_row(const AppendArgs &a, int r) {
+__device__ __forceinline__ void query_rows(const AppendArgs &a, int block) {
+    const int per = a.rows_per_block, threads = blockDim.x / per, t = threadIdx.x % threads;
+    const int r = block * per + threadIdx.x / threads;                // a warp lies within one row
+    if (r >= a.c.rows) return;
+    const int items = a.c.D >> 4;                                     // 4 or 8: divides the threads of a row
+    const int step = threads / items;
+    const Item it = item_of(a, t % items, a.rot > 0);
+    const int64_t in = (int64_t)r * a.q_stride, to = (int64_t)r * a.q_out_stride;
+    float x[8], y[8];
+    int h = t / items;
+    if (h < a.H) load_item<TYPE>(a.q, in + (int64_t)h * a.c.D, it, x, y);
     const int b = sequence_of_row(a.c, r);
     if (b >= a.c.batch) return;
     const Seq s = sequence(a.c, b);
@@ -117,39 +144,31 @@ __device__ __forceinline__ void query_row(const AppendArgs &a, int r) {
     int fp, f;
     const bool known = pages_touched(a, s, fp, f) > 0;
     const int64_t pos = (int64_t)s.kv - s.n + (r - s.row0);
-    const int D = a.c.D;
-    const int half = a.rot >> 1, pairs = a.interleaved ? 0 : half >> 3, plain = (D - (a.interleaved ? 0 : a.rot)) >> 3;
-    const int items = a.H * (pairs + plain);
-    for (int i = threadIdx.x; i < items; i += blockDim.x) {
-        const int h = i / (pairs + plain), j = i % (pairs + plain);
-        const int64_t in = (int64_t)r * a.q_stride + (int64_t)h * D, to = (int64_t)r * a.q_out_stride + (int64_t)h * D;
-        float x[8], y[8];
-        if (pos < 0 || !known) {
+    const bool empty = pos < 0 || !known;
+    float cs[16];
+    if (!empty) load_angles(a, it, pos, cs);
+    while (h < a.H) {
+        if (empty) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = 0.f;
-            store8<TYPE>(a.q_out, to + (j < pairs ? 8 * j : (a.interleaved ? 0 : a.rot) + 8 * (j - pairs)), x);
-            if (j < pairs) store8<TYPE>(a.q_out, to + half + 8 * j, x);
-        } else if (j < pairs) {
-            load_rotated<TYPE>(a, a.q, in, 8 * j, pos, true, x);
-            load_rotated<TYPE>(a, a.q, in, half + 8 * j, pos, true, y);
-            store8<TYPE>(a.q_out, to + 8 * j, x);
-            store8<TYPE>(a.q_out, to + half + 8 * j, y);
+            for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
         } else {
-            const int d = (a.interleaved ? 0 : a.rot) + 8 * (j - pairs);
-            load_rotated<TYPE>(a, a.q, in, d, pos, a.rot > 0, x);
-            store8<TYPE>(a.q_out, to + d, x);
+            rotate(it, cs, x, y);
         }
+        store8<TYPE>(a.q_out, to + (int64_t)h * a.c.D + it.c0, x);
+        store8<TYPE>(a.q_out, to + (int64_t)h * a.c.D + it.c1, y);
+        h += step;
+        if (h < a.H) load_item<TYPE>(a.q, in + (int64_t)h * a.c.D, it, x, y);
     }
 }
 
-// W threads a unit (32: a warp, four units a block; 256: a block); NP passes of
-// W / (D / 8) tokens stay in registers, longer units are read a second time (from L1 or L2).
+// W threads a unit (32: a warp, four units a block; else a block).  A unit has at most NP x W items
+// of 16 elements, so its values stay in registers between their maximum and their codes.
 template <int TYPE, int W, int NP>
-__global__ void __launch_bounds__(W == 32 ? 128 : W) kv_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(W == 32 ? 128 : W, W == 32 ? 4 : 1024 / W) kv_append_kernel(const AppendArgs a) {
     __shared__ uint32_t part[W / 32];
-    const int q_blocks = a.q ? a.c.rows : 0;
+    const int q_blocks = a.q ? (a.c.rows + a.rows_per_block - 1) / a.rows_per_block : 0;
     if ((int)blockIdx.x < q_blocks) {
-        query_row<TYPE>(a, blockIdx.x);
+        query_rows<TYPE>(a, blockIdx.x);
         return;
     }
     constexpr int kUnits = W == 32 ? 4 : 1;
@@ -164,7 +183,7 @@ __global__ void __launch_bounds__(W == 32 ? 128 : W) kv_append_kernel(const Appe
     int first_page, first;
     if (u >= pages_touched(a, s, first_page, first)) return;
     const int page = first_page + u, base = page << a.c.pt_log2;
-    const int lo = max(first, base), hi = min(s.kv, base + a.c.pt);   // the unit's new positions
+    const int lo = max(first, base), n_new = min(s.kv, base + a.c.pt) - lo;   // the unit's new positions
     const int id = page_of(a.c, b, page);
     if (id < 0) return;
     uint8_t *codes = (which ? a.c.v : a.c.k) + id * a.c.page_stride + ((int64_t)head << a.c.pt_log2) * D;
@@ -173,20 +192,22 @@ __global__ void __launch_bounds__(W == 32 ? 128 : W) kv_append_kernel(const Appe
     const void *src = which ? a.v : a.k;
     const int64_t stride = which ? a.v_stride : a.k_stride;
     const int64_t row0 = s.row0 + s.n - (s.kv - lo);                 // row of position lo
-    const int tpt = D >> 3, t0 = tid / tpt, dim0 = (tid % tpt) * 8, step = W / tpt;
-    const bool turn = !which && a.rot > 0, one = hi - lo <= NP * step;
+    const int items = D >> 4, t0 = tid / items, step = W / items;    // a thread keeps its place in the head
+    const Item it = item_of(a, tid % items, !which && a.rot > 0);
 
-    float x[NP][8];
+    float x[NP][8], y[NP][8];
     uint32_t m = 0u;
-    for (int c = 0; c < hi - lo; c += NP * step) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const int t = c + t0 + i * step;
-            if (t < hi - lo) {
-                load_rotated<TYPE>(a, src, (row0 + t) * stride + (int64_t)head * D, dim0, lo + t, turn, x[i]);
+    for (int i = 0; i < NP; ++i) {
+        const int t = t0 + i * step;
+        if (t < n_new) {
+            float cs[16];
+            load_item<TYPE>(src, (row0 + t) * stride + (int64_t)head * D, it, x[i], y[i]);
+            load_angles(a, it, lo + t, cs);
+            rotate(it, cs, x[i], y[i]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[i][e]) & 0x7FFFFFFFu);
-            }
+            for (int e = 0; e < 8; ++e)
+                m = max(m, max(__float_as_uint(x[i][e]) & 0x7FFFFFFFu, __float_as_uint(y[i][e]) & 0x7FFFFFFFu));
         }
     }
     m = __reduce_max_sync(0xFFFFFFFFu, m);
@@ -200,14 +221,17 @@ __global__ void __launch_bounds__(W == 32 ? 128 : W) kv_append_kernel(const Appe
     }
     const uint32_t byte = max(old, block_scale_byte(m));
     if (tid == 0) *scale = (uint8_t)byte;
-    for (int c = 0; c < hi - lo; c += NP * step) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const int t = c + t0 + i * step;
-            if (t < hi - lo) {
-                if (!one)
-                    load_rotated<TYPE>(a, src, (row0 + t) * stride + (int64_t)head * D, dim0, lo + t, turn, x[i]);
-                *reinterpret_cast<uint2 *>(codes + (int64_t)(lo - base + t) * D + dim0) = encode8(x[i], byte);
+    for (int i = 0; i < NP; ++i) {
+        const int t = t0 + i * step;
+        if (t < n_new) {
+            uint8_t *to = codes + (int64_t)(lo - base + t) * D;
+            const uint2 p = encode8(x[i], byte), q = encode8(y[i], byte);
+            if (it.c1 == it.c0 + 8) {
+                *reinterpret_cast<uint4 *>(to + it.c0) = make_uint4(p.x, p.y, q.x, q.y);
+            } else {
+                *reinterpret_cast<uint2 *>(to + it.c0) = p;
+                *reinterpret_cast<uint2 *>(to + it.c1) = q;
             }
         }
     }
@@ -225,17 +249,24 @@ __global__ void __launch_bounds__(W == 32 ? 128 : W) kv_append_kernel(const Appe
     }
 }
 
+template <int TYPE, int W, int NP>
+cudaError_t launch_units(AppendArgs &a, cudaStream_t s) {
+    const int threads = W == 32 ? 128 : W, kUnits = W == 32 ? 4 : 1;
+    // a whole block a query row while the rows do not fill the GPU, else a warp (4096 rows of 32 heads: 22.3 us, with
+    // 64 threads a row 23.9, with 128 25.6)
+    a.rows_per_block = a.c.rows < 1024 ? 1 : threads / 32;
+    const int64_t q_blocks = a.q ? (a.c.rows + a.rows_per_block - 1) / a.rows_per_block : 0;
+    const int64_t units = (int64_t)a.slots * 2 * a.c.KH;
+    kv_append_kernel<TYPE, W, NP><<<(unsigned)(q_blocks + (units + kUnits - 1) / kUnits), threads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
 template <int TYPE>
 cudaError_t launch_typed(AppendArgs &a, cudaStream_t s) {
-    const int64_t units = (int64_t)a.slots * 2 * a.c.KH;
-    const int64_t q_blocks = a.q ? a.c.rows : 0;
-    // a warp a unit while a sequence adds at most a few tokens, a block a unit for prompts
-    if (a.c.max_rows <= 4) {
-        kv_append_kernel<TYPE, 32, 2><<<(unsigned)(q_blocks + (units + 3) / 4), 128, 0, s>>>(a);
-    } else {
-        kv_append_kernel<TYPE, 256, 4><<<(unsigned)(q_blocks + units), 256, 0, s>>>(a);
-    }
-    return cudaGetLastError();
+    // a warp a unit while a sequence adds at most 4 tokens (4 x 8 items), else a block that holds a page in two items a thread
+    const int items = a.c.pt * a.c.D >> 4;
+    if (a.c.max_rows <= 4) return launch_units<TYPE, 32, 1>(a, s);
+    return items <= 256 ? launch_units<TYPE, 128, 2>(a, s) : items <= 512 ? launch_units<TYPE, 256, 2>(a, s) : launch_units<TYPE, 512, 2>(a, s);
 }
 
 }  // namespace

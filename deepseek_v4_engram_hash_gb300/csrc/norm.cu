@@ -3,11 +3,13 @@
 // codes with one power-of-two scale a block (engram_residual_norm).
 //
 // Memory bound (about 6 flop an element against 7 to 17 bytes): each element is
-// read once and stays in registers between the two uses.  One CTA a row,
-// thread t holding the 8-element chunks t, t + THREADS, ...; the sum of squares
-// goes through shuffles and one shared-memory exchange, a block's largest |y|
-// through shuffles where the block is a power-of-two number of chunks that fits
-// a warp, through shared-memory maxima otherwise.
+// read once and stays in registers between the two uses.  A block takes a row, thread t
+// the 8-element chunks t, t + blockDim.x of it; other blocks' loads run beside a
+// block's exchanges and stores.  (Blocks that go through several rows and ask for the
+// next one ahead measured 118 against 115 us for 16384 x 4096, f32 residual: 109 us of bytes.)
+// The sum of squares goes through shuffles and one shared-memory exchange, a block's
+// largest |y| through shuffles where the block is a power-of-two number of
+// chunks that fits a warp, through shared-memory maxima otherwise.
 #include "sublayer.cuh"
 
 namespace engram {
@@ -16,19 +18,21 @@ namespace {
 
 constexpr int kMaxDim = 16384;
 
-template <int XT, int RT, int THREADS, int NV>
-__global__ void __launch_bounds__(THREADS) residual_norm_kernel(const NormArgs a) {
-    __shared__ float part[THREADS / 32];
+template <int XT, int RT, int NV>
+__global__ void __launch_bounds__(1024) residual_norm_kernel(const NormArgs a) {
+    __shared__ float part[32];
     __shared__ uint32_t amax[kMaxDim / 16];
-    const int64_t row = blockIdx.x;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x;
     const int chunks = a.dim >> 3;
+    const int bc = a.block >> 3;                                  // chunks a block
+    const bool codes = a.fmt != ENGRAM_FMT_BF16, in_warp = bc <= 32 && (bc & (bc - 1)) == 0;
 
+    const int64_t row = blockIdx.x;
     float r[NV][8];
     float ss = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        const int c = tid + v * THREADS;
+        const int c = tid + v * threads;
         if (c < chunks) {
             load8<RT>(a.res, row * a.res_stride + 8 * c, r[v]);
             if (a.x) {
@@ -37,32 +41,33 @@ __global__ void __launch_bounds__(THREADS) residual_norm_kernel(const NormArgs a
 #pragma unroll
                 for (int e = 0; e < 8; ++e) r[v][e] += x[e];
             }
-            if (a.res_out) store8<RT>(a.res_out, row * a.res_stride + 8 * c, r[v]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(r[v][e], r[v][e], ss);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) r[v][e] = 0.f;
         }
     }
 #pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int c = tid + v * threads;
+        if (a.res_out && c < chunks) store8<RT>(a.res_out, row * a.res_stride + 8 * c, r[v]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(r[v][e], r[v][e], ss);
+    }
+#pragma unroll
     for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
     if (lane == 0) part[warp] = ss;
-    const int bc = a.block >> 3;                                  // chunks a block
-    const bool in_warp = a.fmt != ENGRAM_FMT_BF16 && bc <= 32 && (bc & (bc - 1)) == 0;
-    if (a.fmt != ENGRAM_FMT_BF16 && !in_warp)
-        for (int i = tid; i < a.dim / a.block; i += THREADS) amax[i] = 0u;
+    if (codes && !in_warp)
+        for (int i = tid; i < a.dim / a.block; i += threads) amax[i] = 0u;
     __syncthreads();
-    ss = part[0];
+    ss = lane < threads >> 5 ? part[lane] : 0.f;
 #pragma unroll
-    for (int w = 1; w < THREADS / 32; ++w) ss += part[w];
+    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
     const float inv = 1.f / sqrtf(ss / (float)a.dim + a.eps);
-
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        const int c = tid + v * THREADS;
-        float w[8];
+        const int c = tid + v * threads;
         if (a.w && c < chunks) {
+            float w[8];
             load8<ENGRAM_T_F32>(a.w, 8 * c, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) r[v][e] = r[v][e] * inv * w[e];
@@ -71,68 +76,67 @@ __global__ void __launch_bounds__(THREADS) residual_norm_kernel(const NormArgs a
             for (int e = 0; e < 8; ++e) r[v][e] *= inv;
         }
     }
-    if (a.fmt == ENGRAM_FMT_BF16) {
+    if (!codes) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = tid + v * THREADS;
+            const int c = tid + v * threads;
             if (c < chunks) store8<ENGRAM_T_BF16>(a.out, row * a.dim + 8 * c, r[v]);
         }
-        return;
-    }
-    uint32_t m[NV];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        m[v] = 0u;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m[v] = max(m[v], __float_as_uint(r[v][e]) & 0x7FFFFFFFu);
-    }
-    if (in_warp) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-            for (int o = 1; o < bc; o <<= 1) m[v] = max(m[v], __shfl_xor_sync(0xFFFFFFFFu, m[v], o));
     } else {
+        uint32_t m[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = tid + v * THREADS;
-            if (c < chunks) atomicMax(&amax[c / bc], m[v]);
+            m[v] = 0u;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m[v] = max(m[v], __float_as_uint(r[v][e]) & 0x7FFFFFFFu);
         }
-        __syncthreads();
+        if (in_warp) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                for (int o = 1; o < bc; o <<= 1) m[v] = max(m[v], __shfl_xor_sync(0xFFFFFFFFu, m[v], o));
+        } else {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int c = tid + v * threads;
+                if (c < chunks) atomicMax(&amax[c / bc], m[v]);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int c = tid + v * threads;
+                if (c < chunks) m[v] = amax[c / bc];
+            }
+        }
+        const int64_t blocks = a.dim / a.block;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = tid + v * THREADS;
-            if (c < chunks) m[v] = amax[c / bc];
-        }
-    }
-    const int64_t blocks = a.dim / a.block;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int c = tid + v * THREADS;
-        if (c >= chunks) continue;
-        const uint32_t byte = block_scale_byte(m[v]);
-        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + row * a.dim + 8 * c) = encode8(r[v], byte);
-        if (c % bc == 0) {
-            const int64_t i = row * blocks + c / bc;
-            if (a.fmt == ENGRAM_FMT_FP8_E8M0)
-                static_cast<uint8_t *>(a.scales)[i] = (uint8_t)byte;
-            else
-                static_cast<float *>(a.scales)[i] = e8m0_to_f32(byte);
+            const int c = tid + v * threads;
+            if (c >= chunks) continue;
+            const uint32_t byte = block_scale_byte(m[v]);
+            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + row * a.dim + 8 * c) = encode8(r[v], byte);
+            if (c % bc == 0) {
+                const int64_t i = row * blocks + c / bc;
+                if (a.fmt == ENGRAM_FMT_FP8_E8M0)
+                    static_cast<uint8_t *>(a.scales)[i] = (uint8_t)byte;
+                else
+                    static_cast<float *>(a.scales)[i] = e8m0_to_f32(byte);
+            }
         }
     }
 }
 
 template <int XT, int RT>
 cudaError_t launch_typed(const NormArgs &a, cudaStream_t s) {
+    // One chunk a thread or two: two keep more bytes of a 32-bit residual in flight on an SM (16384 rows of
+    // 4096: 115 against 147 us), one shortens a row's time, which counts where a 16-bit residual is read (1537
+    // rows of 5120: 15.3 against 16.2 us) or the rows are few (one row: 2.6 against 3.1 us).
     const int chunks = a.dim >> 3;
-    if (chunks <= 128)
-        residual_norm_kernel<XT, RT, 128, 1><<<a.rows, 128, 0, s>>>(a);
-    else if (chunks <= 256)
-        residual_norm_kernel<XT, RT, 256, 1><<<a.rows, 256, 0, s>>>(a);
-    else if (chunks <= 512)
-        residual_norm_kernel<XT, RT, 256, 2><<<a.rows, 256, 0, s>>>(a);
-    else if (chunks <= 1024)
-        residual_norm_kernel<XT, RT, 256, 4><<<a.rows, 256, 0, s>>>(a);
+    const bool one = chunks <= 256 || (chunks <= 1024 && (RT != ENGRAM_T_F32 || a.rows <= a.sms));
+    const int threads = ((one ? chunks : (chunks + 1) / 2) + 31) / 32 * 32;
+    if (one)
+        residual_norm_kernel<XT, RT, 1><<<a.rows, threads, 0, s>>>(a);
     else
-        residual_norm_kernel<XT, RT, 512, 4><<<a.rows, 512, 0, s>>>(a);
+        residual_norm_kernel<XT, RT, 2><<<a.rows, threads, 0, s>>>(a);
     return cudaGetLastError();
 }
 

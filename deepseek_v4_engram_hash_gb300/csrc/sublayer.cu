@@ -19,6 +19,19 @@ inline cudaStream_t S(uintptr_t s) { return reinterpret_cast<cudaStream_t>(s); }
 inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline int cuda_rc(cudaError_t e) { return e == cudaSuccess ? ENGRAM_OK : ENGRAM_E_CUDA; }
 
+// SMs of the current device, 0 if they cannot be had.
+inline int sm_count() {
+    static int known[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (!known[dev]) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        known[dev] = n;
+    }
+    return known[dev];
+}
+
 // A stride of 0 means dense; others must keep every row 16-byte aligned.
 inline int check_stride(int64_t *stride, int64_t dense) {
     if (*stride == 0) *stride = dense;
@@ -100,6 +113,7 @@ int engram_residual_norm(const void *d_x, int32_t x_type, int64_t x_stride, cons
     a.eps = eps;
     a.out = d_out;
     a.scales = d_scales;
+    if (!(a.sms = sm_count())) return ENGRAM_E_CUDA;
     return cuda_rc(launch_residual_norm(a, S(stream)));
 }
 

@@ -143,6 +143,7 @@ struct NormArgs {
     const float *w;
     int64_t x_stride, res_stride;
     int32_t x_type, res_type, rows, dim, fmt, block;
+    int32_t sms;
     float eps;
     void *out, *scales;
 };
@@ -157,7 +158,7 @@ struct AppendArgs {
     const float *rope;
     int64_t rope_positions;
     int32_t rot, interleaved;
-    int32_t span, slots;                // set by the launcher
+    int32_t span, slots, rows_per_block;    // set by the launcher
 };
 cudaError_t launch_kv_append(AppendArgs a, cudaStream_t s);
 
