@@ -145,9 +145,21 @@ def _ptr(t) -> ctypes.c_void_p:
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream=None) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+def _adr(t):
+    """_ptr as a plain int (or None): what the small calls use."""
+    return t if t is None or type(t) is int else t.data_ptr()
+
+
+# torch.cuda.current_stream() builds a Stream object (3 us on a Grace core); this returns its handle (0.1 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream=None) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and torch.cuda.is_initialized():
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def make_geom(n_layers, max_ngram, n_heads, head_dim, dim, hc, scale_block, vocab) -> engram_geom:
@@ -397,15 +409,15 @@ class Attention:
 
 def engram_residual_norm(d_x, x_type, d_res, res_type, d_res_out, d_weight, rows, dim, eps, out_fmt, scale_block,
                          d_out, d_scales, x_stride=0, res_stride=0, stream=None):
-    _ok(lib().engram_residual_norm(_ptr(d_x), x_type, x_stride, _ptr(d_res), res_type, res_stride, _ptr(d_res_out),
-                                   _ptr(d_weight), rows, dim, eps, out_fmt, scale_block, _ptr(d_out),
-                                   _ptr(d_scales), _stream(stream)), "engram_residual_norm")
+    _ok(lib().engram_residual_norm(_adr(d_x), x_type, x_stride, _adr(d_res), res_type, res_stride, _adr(d_res_out),
+                                   _adr(d_weight), rows, dim, eps, out_fmt, scale_block, _adr(d_out),
+                                   _adr(d_scales), _stream(stream)), "engram_residual_norm")
 
 
 def engram_kv_append(cache: KvCache, batch: KvBatch, type, d_k, k_stride, d_v, v_stride, d_q, q_stride, d_q_out,
                      q_out_stride, n_heads, rope: Rope = None, stream=None):
-    _ok(lib().engram_kv_append(cache.ref, batch.ref, type, _ptr(d_k), k_stride, _ptr(d_v), v_stride, _ptr(d_q),
-                               q_stride, _ptr(d_q_out), q_out_stride, n_heads, rope.ref if rope else None,
+    _ok(lib().engram_kv_append(cache.ref, batch.ref, type, _adr(d_k), k_stride, _adr(d_v), v_stride, _adr(d_q),
+                               q_stride, _adr(d_q_out), q_out_stride, n_heads, rope.ref if rope else None,
                                _stream(stream)), "engram_kv_append")
 
 
@@ -415,8 +427,8 @@ def engram_attn_reset(attn: Attention, stream=None):
 
 def engram_attention(attn: Attention, cache: KvCache, batch: KvBatch, type, d_q, q_stride, n_heads, scale, window,
                      d_out, out_stride, d_lse=None, stream=None):
-    _ok(lib().engram_attention(attn.handle, cache.ref, batch.ref, type, _ptr(d_q), q_stride, n_heads, scale, window,
-                               _ptr(d_out), out_stride, _ptr(d_lse), _stream(stream)), "engram_attention")
+    _ok(lib().engram_attention(attn.handle, cache.ref, batch.ref, type, _adr(d_q), q_stride, n_heads, scale, window,
+                               _adr(d_out), out_stride, _adr(d_lse), _stream(stream)), "engram_attention")
 
 
 def prepare_events(events) -> None:
