@@ -15,8 +15,9 @@
 //   warps 8..11        codes to f16 operand tiles in shared memory (e4m3 to f16 is exact);
 //                      keys and values alike stay [token][dim]: values are the
 //                      MN-major operand of the second product;
-//   warps 12, 14       issue the MMAs of half 0 / 1 (M 128, N 64 / D, K 16): S_h = Q_h K^T
-//                      for 64 tokens at a time, O_h += P_h V with P_h from tensor memory;
+//   warps 12, 14       issue the first product of half 0 / 1, S_h = Q_h K^T for 64 tokens at
+//                      a time (M 128, N 64, K 16);
+//   warps 16, 17       issue the second, O_h += P_h V with P_h from tensor memory (M 128, N D, K 16);
 //   warp 13            pages, scales and TMA copies of the codes;
 //   warp 15            the schedule: entries of the list for all others.
 // A half's scores have two buffers of 64 tokens: while one is in its softmax, the tensor
@@ -42,7 +43,7 @@ using namespace tcg;
 constexpr int kHalf = 128;                           // rows of a half
 constexpr int kRows = 2 * kHalf;
 constexpr int kTok = 128, kPartTok = 64;             // tokens a step, and a score buffer
-constexpr int kThreads = 512, kSoftWarps = 8;
+constexpr int kThreads = 640, kSoftWarps = 8;
 constexpr int kGroups = kTok / 16;                   // scale groups a step (a page is at least 16 tokens)
 constexpr int kMetaRing = 4;
 
@@ -50,6 +51,9 @@ struct TileParams {
     AttnArgs a;
     CUtensorMap mk, mv;
 };
+
+// x / group.
+__device__ __forceinline__ int by_group(const AttnArgs &a, int x) { return a.group_log2 >= 0 ? x >> a.group_log2 : x / a.group; }
 
 // Row tile rt of a sequence: its tokens from `lo`, in `tiles` tiles of 128.
 struct RowTile {
@@ -59,7 +63,7 @@ __device__ __forceinline__ RowTile row_tile(const AttnArgs &a, const Seq &s, int
     RowTile t;
     t.r0 = rt * kRows;
     t.n_rows = min(kRows, s.n * a.group - t.r0);
-    const int first = s.kv - s.n + t.r0 / a.group, last = s.kv - s.n + (t.r0 + t.n_rows - 1) / a.group;
+    const int first = s.kv - s.n + by_group(a, t.r0), last = s.kv - s.n + by_group(a, t.r0 + t.n_rows - 1);
     t.lo = a.window ? max(0, first - a.window + 1) / kTok * kTok : 0;
     t.tiles = max(1, (min(s.kv, last + 1) - t.lo + kTok - 1) / kTok);
     return t;
@@ -98,7 +102,7 @@ struct Entry {
     int b, head, tile0, count;                       // count 0: no more
     int first_cta, last_cta;                         // those that share the row tile
 };
-constexpr int kEntries = 4, kEntryUsers = kSoftWarps + 4 + 3;
+constexpr int kEntries = 4, kEntryUsers = kSoftWarps + 4 + 5;
 
 // This CTA's range, walked by one warp (start) and its lane 0 (next).
 struct Walk {
@@ -114,8 +118,10 @@ struct Walk {
         const int lanes_per = (a.c.batch + 31) / 32;
         int64_t mine = 0;
         if (few) {
+            const Seq q = lane < a.c.batch ? sequence(a.c, lane) : Seq{0, 0, 0};
             for (int i = 0; i < a.c.batch; ++i) {
-                const int64_t n = head_tiles_warp(a, sequence(a.c, i)) * a.c.KH;
+                const Seq at = {0, __shfl_sync(0xFFFFFFFFu, q.n, i), __shfl_sync(0xFFFFFFFFu, q.kv, i)};
+                const int64_t n = head_tiles_warp(a, at) * a.c.KH;
                 if (lane == i) mine = n;
             }
         } else {
@@ -334,8 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
     const AttnArgs &a = p.a;
     const uint32_t base = smem_u32(smem);
     float4 *meta = reinterpret_cast<float4 *>(smem + T::oMeta);           // [kMetaRing][kGroups]: 2^ek, ev, 2^-ev, counts
-    enum { Q_FULL = 0, ST_FULL = 2, ST_EMPTY = 4, K_FULL = 6, K_EMPTY = 8, V_FULL = 10, V_EMPTY = 12, DRAIN = 14, HALF = 16,
-           S_FULL = 18, P_FULL = 22, PV_DONE = 26, E_FULL = 30, E_EMPTY = 34 };      // [2 halves][2 buffers] from S_FULL to PV_DONE
+    enum { Q_FULL = 0, ST_FULL = 2, ST_EMPTY = 4, K_FULL = 6, K_EMPTY = 8, V_FULL = 10, V_EMPTY = 12, HALF = 14, DRAIN = 16,
+           S_FULL = 20, P_FULL = 24, PV_DONE = 28, E_FULL = 32, E_EMPTY = 36 };      // [2 halves][2 buffers] from S_FULL to PV_DONE
     auto bar = [&](int i) { return base + T::oBar + 8u * i; };
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + T::oFlag);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + T::oFlag + 4);
@@ -354,13 +360,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
             mbar_init(bar(K_EMPTY + i), 2);               // both halves' products
             mbar_init(bar(V_FULL + i), 4);
             mbar_init(bar(V_EMPTY + i), 2);
-            mbar_init(bar(DRAIN + i), 1);
             mbar_init(bar(HALF + i), 4);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar(S_FULL + i), 1);
             mbar_init(bar(P_FULL + i), 4);
             mbar_init(bar(PV_DONE + i), 1);
+            mbar_init(bar(DRAIN + i), 1);
         }
         for (int i = 0; i < kEntries; ++i) {
             mbar_init(bar(E_FULL + i), 1);
@@ -390,7 +396,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
         if (lane == 0) mbar_arrive(bar(E_EMPTY + i % kEntries));
     };
 
+    // 640 threads launch with 96 registers each: 2 x 128 x 128 + 128 x 88 + 2 x 128 x 64 stay within them
     if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == 15) {
             // ---- the schedule ----
             Walk w;
@@ -457,74 +465,66 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
             for (int x = 0; x < 2; ++x)
                 while (it > 0 && !mbar_try(bar(ST_FULL + x), (it - 1) & 1) && now_ns() - t0 < 10000000ull) {
                 }
-        } else {
-            // ---- the tensor cores ----
-            const int h = (warp - 12) >> 1;
+        } else if (warp < 18) {
+            // ---- the tensor cores, a warp a product and half (one warp a half for both products waited for each
+            // second one before the next first: 380 against 366 us for 4096 tokens behind 4096) ----
+            const bool second = warp >= 16;
+            const int h = second ? warp - 16 : (warp - 12) >> 1;
+            const int full = second ? V_FULL : K_FULL, empty = second ? V_EMPTY : K_EMPTY;
             bool ok = true;
-            uint32_t n = 0, ns = 0, ent = 0;                              // tiles, score buffers of this half, its entries
-            const uint32_t q_lo = desc_lo(base + T::oQ + h * T::kQ, 16);
-            const uint32_t tS = tmem + T::cS + h * 128, tO = tmem + T::cO + h * D;
-            // the scores of 64 tokens, part s & 1 of tile n, into buffer s & 1
-            auto qk = [&](uint32_t s, uint32_t tile) {
-                tc_fence_after();
-                if (elect()) {
-                    const uint32_t k_lo = desc_lo(base + T::oK + (tile & 1) * T::kF16 + (s & 1) * (kPartTok * 128), 16);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = ((kk >> 2) * T::kSub + (kk & 3) * 32) >> 4;
-                        mma_ss<idesc_f16(kHalf, kPartTok, false)>(tS + (s & 1) * kPartTok, q_lo + off, k_lo + off, kk != 0);
-                    }
-                    commit(bar(S_FULL + 2 * h + (s & 1)));
-                    if (s & 1) commit(bar(K_EMPTY + (tile & 1)));
-                }
-                __syncwarp();
-            };
+            uint32_t n = 0, ns = 0, ent = 0;                              // tiles; score buffers and entries of the half
             for (uint32_t i = 0; ok && (ok = open(i)); close(i++)) {
                 const int count = entry(i).count;
                 if (h && entry(i).rt.n_rows <= kHalf) {
                     // no rows in this half: keep step with the converted tiles (their barriers count both halves)
                     for (int j = 0; j < count; ++j, ++n) {
-                        if (!(ok = wait(K_FULL + (n & 1), n >> 1))) break;
-                        if (lane == 0) mbar_arrive(bar(K_EMPTY + (n & 1)));
-                        if (!(ok = wait(V_FULL + (n & 1), n >> 1))) break;
-                        if (lane == 0) mbar_arrive(bar(V_EMPTY + (n & 1)));
+                        if (!(ok = wait(full + (n & 1), n >> 1))) break;
+                        if (lane == 0) mbar_arrive(bar(empty + (n & 1)));
                     }
                     continue;
                 }
-                if (!(ok = wait(Q_FULL + h, ent++) && wait(K_FULL + (n & 1), n >> 1))) continue;
-                qk(0, n);
-                qk(1, n);
+                if (!second && !(ok = wait(Q_FULL + h, ent++))) continue;
                 for (int s = 0; s < 2 * count; ++s, ++ns) {
-                    ok = ((s & 1) || wait(V_FULL + (n & 1), n >> 1)) && wait(P_FULL + 2 * h + (s & 1), ns >> 1);
+                    // scores go over the probabilities two parts before: their product has to be done
+                    ok = ((s & 1) || wait(full + (n & 1), n >> 1)) &&
+                         (second ? wait(P_FULL + 2 * h + (s & 1), ns >> 1) : s < 2 || wait(PV_DONE + 2 * h + (s & 1), (ns >> 1) - 1));
                     if (!ok) break;
+                    const uint32_t at = base + (second ? T::oV : T::oK) + (n & 1) * T::kF16 + (s & 1) * (kPartTok * 128);
+                    const uint32_t tS = tmem + T::cS + h * 128 + (s & 1) * kPartTok;
                     tc_fence_after();
                     if (elect()) {
-                        const uint32_t v_lo = desc_lo(base + T::oV + (n & 1) * T::kF16 + (s & 1) * (kPartTok * 128), T::kSub);
+                        if (second) {
+                            const uint32_t v_lo = desc_lo(at, T::kSub);
 #pragma unroll
-                        for (int kk = 0; kk < kPartTok / 16; ++kk)
-                            mma_ts<idesc_f16(kHalf, D, true)>(tO, tS + (s & 1) * kPartTok + kk * 8, v_lo + kk * (2048 >> 4), (s | kk) != 0);
-                        commit(bar(PV_DONE + 2 * h + (s & 1)));
-                        if (s & 1) commit(bar(V_EMPTY + (n & 1)));
+                            for (int kk = 0; kk < kPartTok / 16; ++kk)
+                                mma_ts<idesc_f16(kHalf, D, true)>(tmem + T::cO + h * D, tS + kk * 8, v_lo + kk * (2048 >> 4), (s | kk) != 0);
+                            commit(bar(PV_DONE + 2 * h + (s & 1)));
+                        } else {
+                            const uint32_t q_lo = desc_lo(base + T::oQ + h * T::kQ, 16), k_lo = desc_lo(at, 16);
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t off = ((kk >> 2) * T::kSub + (kk & 3) * 32) >> 4;
+                                mma_ss<idesc_f16(kHalf, kPartTok, false)>(tS, q_lo + off, k_lo + off, kk != 0);
+                            }
+                            commit(bar(S_FULL + 2 * h + (s & 1)));
+                        }
+                        if (s & 1) commit(bar(empty + (n & 1)));
                     }
                     __syncwarp();
-                    if (s + 2 < 2 * count) {
-                        // the buffer's next scores go over these probabilities: their product has to be done
-                        ok = ((s & 1) || wait(K_FULL + ((n + 1) & 1), (n + 1) >> 1)) && wait(PV_DONE + 2 * h + (s & 1), ns >> 1);
-                        if (!ok) break;
-                        qk(s, n + 1);
-                    }
                     n += s & 1;
                 }
             }
             __syncwarp();
-            if (elect()) commit(bar(DRAIN + h));                          // from the lane that issued the MMAs
+            const int drain = DRAIN + 2 * second + h;
+            if (elect()) commit(bar(drain));                              // from the lane that issued the MMAs
             const uint64_t t0 = now_ns();
-            while (!mbar_try(bar(DRAIN + h), 0) && now_ns() - t0 < 100000000ull) {
+            while (!mbar_try(bar(drain), 0) && now_ns() - t0 < 100000000ull) {
             }
             __syncwarp();
         }
     } else if (warp >= kSoftWarps) {
         // ---- codes to f16 ----
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         const int wt = threadIdx.x - 32 * kSoftWarps;
         bool ok = true;
         uint32_t n = 0;
@@ -548,6 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
         }
     } else {
         // ---- softmax, one thread a row ----
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
         const int h = warp >> 2, row = (warp & 3) * 32 + lane;            // row of the half = tensor-memory lane
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t tO = lanes + T::cO + h * D;
@@ -569,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
             int hi_col, lo_col, moving;
             float kf;
             {
-                const int rr = e.rt.r0 + h * kHalf + row, tok_i = rr / a.group;
+                const int rr = e.rt.r0 + h * kHalf + row, tok_i = by_group(a, rr);
                 const bool live = h * kHalf + row < e.rt.n_rows;
                 const int64_t q_row = e.s.row0 + tok_i;
                 const int q_head = e.head * a.group + rr - tok_i * a.group;
@@ -582,28 +583,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                 auto pair_of = [&](uint32_t u) {
                     return TYPE == ENGRAM_T_BF16 ? make_float2(bf16_lo(u), bf16_hi(u)) : __half22float2(*reinterpret_cast<__half2 *>(&u));
                 };
-                uint32_t m = 0;
-#pragma unroll 2
+                uint32_t m = 0, w[D / 2];
+#pragma unroll
                 for (int k = 0; k < D / 8; ++k) {
                     const uint4 x = live ? src[k] : make_uint4(0u, 0u, 0u, 0u);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                    w[4 * k] = x.x, w[4 * k + 1] = x.y, w[4 * k + 2] = x.z, w[4 * k + 3] = x.w;
+                }
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float2 f = pair_of(w[q]);
-                        m = max(m, max(__float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu));
-                    }
+                for (int k = 0; k < D / 2; ++k) {
+                    const float2 f = pair_of(w[k]);
+                    m = max(m, max(__float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu));
                 }
                 float down;
                 q_scale(m, a.scale_log2, down, kf);
                 const uint32_t dst = base + T::oQ + h * T::kQ + row * 128;
-#pragma unroll 2
+#pragma unroll
                 for (int k = 0; k < D / 8; ++k) {
-                    const uint4 x = live ? src[k] : make_uint4(0u, 0u, 0u, 0u);
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
                     uint32_t o[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const float2 f = pair_of(w[q]);
+                        const float2 f = pair_of(w[4 * k + q]);
                         o[q] = pack_f16x2(f.x * down, f.y * down);
                     }
                     sts128(dst + (k >> 3) * T::kSub + (((k & 7) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
@@ -700,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
             if (!(ok = wait(PV_DONE + 2 * h + 1, (ns - 1) >> 1))) continue;   // the last product, and all before it
             tc_fence_after();
             const bool alone = e.first_cta == e.last_cta;
-            const int rr = e.rt.r0 + h * kHalf + row, tok_i = rr / a.group;
+            const int rr = e.rt.r0 + h * kHalf + row, tok_i = by_group(a, rr);
             const bool live = h * kHalf + row < e.rt.n_rows;
             const int64_t q_row = e.s.row0 + tok_i;
             const int q_head = e.head * a.group + rr - tok_i * a.group;
@@ -759,31 +758,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                 const float *st = a.ws.part + kRows * D + h * kHalf + row;
                 const int parts = e.last_cta - e.first_cta + 1;
                 auto at = [&](int k) { return ((int64_t)(e.first_cta + k) * 2 + (k == 0 ? 1 : 0)) * T::kPart; };
-                float m = -INFINITY, l = 0.f;
-                for (int k = 0; k < parts; ++k) m = fmaxf(m, __ldcg(st + at(k)));
-                auto factor = [&](int k) {
-                    const float mk = __ldcg(st + at(k));
-                    return mk == -INFINITY ? (__ldcg(st + at(k) + kRows) == 0.f ? 0.f : 1.f) : exp2_approx(mk - m);
-                };
-                for (int k = 0; k < parts; ++k) l = fmaf(__ldcg(st + at(k) + kRows), factor(k), l);
+                // bounds and sums two parts at a time, then 32 dims of two parts at a time
+                float m = -INFINITY, l = 0.f, f01[2] = {1.f, 1.f};
+                auto last_of = [&](int k) { return min(k, parts - 1); };
+                for (int k = 0; k < parts; k += 2) m = fmaxf(m, fmaxf(__ldcg(st + at(k)), __ldcg(st + at(last_of(k + 1)))));
+                auto factor = [&](float mk, float lk) { return mk == -INFINITY ? (lk == 0.f ? 0.f : 1.f) : exp2_approx(mk - m); };
+                for (int k = 0; k < parts; k += 2) {
+                    const float m0 = __ldcg(st + at(k)), l0 = __ldcg(st + at(k) + kRows), m1 = __ldcg(st + at(last_of(k + 1))),
+                                l1 = __ldcg(st + at(last_of(k + 1)) + kRows);
+                    const float f0 = factor(m0, l0), f1 = k + 1 < parts ? factor(m1, l1) : 0.f;
+                    if (k == 0) f01[0] = f0, f01[1] = f1;
+                    l = fmaf(l1, f1, fmaf(l0, f0, l));
+                }
                 const float il = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
-                for (int d = 0; d < D; d += 16) {
-                    float x[16] = {};
+                for (int d = 0; d < D; d += 32) {
+                    float x[32] = {};
 #pragma unroll 1
-                    for (int k = 0; k < parts; ++k) {
-                        const float f = factor(k);
-                        const float4 *src = reinterpret_cast<const float4 *>(a.ws.part + at(k) + of) + d / 4 * kRows;
-                        float4 v[4];
+                    for (int k = 0; k < parts; k += 2) {
+                        const int k1 = last_of(k + 1);
+                        float f0 = f01[0], f1 = f01[1];
+                        if (k) {
+                            f0 = factor(__ldcg(st + at(k)), __ldcg(st + at(k) + kRows));
+                            f1 = k + 1 < parts ? factor(__ldcg(st + at(k1)), __ldcg(st + at(k1) + kRows)) : 0.f;
+                        }
+                        const float4 *p0 = reinterpret_cast<const float4 *>(a.ws.part + at(k) + of) + d / 4 * kRows;
+                        const float4 *p1 = reinterpret_cast<const float4 *>(a.ws.part + at(k1) + of) + d / 4 * kRows;
+                        float4 v[8], w[8];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) v[q] = __ldcg(src + q * kRows);
+                        for (int q = 0; q < 8; ++q) v[q] = __ldcg(p0 + q * kRows), w[q] = __ldcg(p1 + q * kRows);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            x[4 * q] = fmaf(v[q].x, f, x[4 * q]), x[4 * q + 1] = fmaf(v[q].y, f, x[4 * q + 1]);
-                            x[4 * q + 2] = fmaf(v[q].z, f, x[4 * q + 2]), x[4 * q + 3] = fmaf(v[q].w, f, x[4 * q + 3]);
+                        for (int q = 0; q < 8; ++q) {
+                            x[4 * q] = fmaf(w[q].x, f1, fmaf(v[q].x, f0, x[4 * q]));
+                            x[4 * q + 1] = fmaf(w[q].y, f1, fmaf(v[q].y, f0, x[4 * q + 1]));
+                            x[4 * q + 2] = fmaf(w[q].z, f1, fmaf(v[q].z, f0, x[4 * q + 2]));
+                            x[4 * q + 3] = fmaf(w[q].w, f1, fmaf(v[q].w, f0, x[4 * q + 3]));
                         }
                     }
                     put(d, x, il);
+                    put(d + 16, x + 16, il);
                 }
                 put_lse(m, l);
             }

@@ -214,6 +214,7 @@ int engram_attention(engram_attn *attn, const engram_kv_cache *cache, const engr
     a.type = type;
     a.H = n_heads;
     a.group = n_heads / cache->n_kv_heads;
+    a.group_log2 = (a.group & (a.group - 1)) ? -1 : __builtin_ctz(a.group);
     a.window = window >= 1 << 30 ? 0 : window;          // no sequence is longer
     a.scale_log2 = (float)((double)scale * 1.4426950408889634);
     a.sms = attn->sms;

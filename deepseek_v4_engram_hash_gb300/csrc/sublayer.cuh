@@ -176,7 +176,7 @@ struct AttnArgs {
     void *out;
     float *lse;
     int64_t q_stride, out_stride;
-    int32_t type, H, group, window;
+    int32_t type, H, group, group_log2, window;     // group_log2 < 0: not a power of two
     float scale_log2;                   // scale x log2(e)
     int32_t sms;
 };
