@@ -25,8 +25,9 @@
 // them idle for the latencies between product, softmax and product: 432 against 379 us for 4096 tokens behind 4096, 32 query and 8 key/value heads of 128).
 // Tensor memory: S 2 x 2 x 64 columns, O 2 x D; P lies over its S.
 //
-// The call's (sequence, head, row tile, 128-token tile) list is cut evenly
-// over one CTA an SM; ranges that cut a row tile's tokens leave partial
+// The call's (sequence, head, row tile, 128-token tile) list, with kEntryCost places more
+// for each row tile (what beginning and ending one takes), is cut evenly over one CTA an
+// SM; ranges that cut a row tile's tokens leave partial
 // results that the last to arrive joins in CTA order.
 // Every wait is bounded (2 s); on expiry ENGRAM_E_TIMEOUT is raised, every role leaves
 // its loops (all waits are on mbarriers, and a warp votes before it branches on one)
@@ -43,6 +44,7 @@ using namespace tcg;
 constexpr int kHalf = 128;                           // rows of a half
 constexpr int kRows = 2 * kHalf;
 constexpr int kTok = 128, kPartTok = 64;             // tokens a step, and a score buffer
+constexpr int kEntryCost = 6;                        // places of a row tile beside its tiles: 4096 tokens behind 4096 348 us, without 367, with 3 about 356
 constexpr int kThreads = 640, kSoftWarps = 8;
 constexpr int kGroups = kTok / 16;                   // scale groups a step (a page is at least 16 tokens)
 constexpr int kMetaRing = 4;
@@ -83,15 +85,15 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v) {
     }
     return v;
 }
-// Token tiles of one head of sequence s: by one lane, or by a whole warp.
-__device__ __forceinline__ int64_t head_tiles(const AttnArgs &a, const Seq &s) {
+// Places of one head of sequence s in the list: by one lane, or by a whole warp.
+__device__ __forceinline__ int64_t head_places(const AttnArgs &a, const Seq &s) {
     int64_t n = 0;
-    for (int rt = 0; rt < row_tiles(a, s); ++rt) n += row_tile(a, s, rt).tiles;
+    for (int rt = 0; rt < row_tiles(a, s); ++rt) n += row_tile(a, s, rt).tiles + kEntryCost;
     return n;
 }
-__device__ __forceinline__ int64_t head_tiles_warp(const AttnArgs &a, const Seq &s) {
+__device__ __forceinline__ int64_t head_places_warp(const AttnArgs &a, const Seq &s) {
     int64_t n = 0;
-    for (int rt = threadIdx.x & 31; rt < row_tiles(a, s); rt += 32) n += row_tile(a, s, rt).tiles;
+    for (int rt = threadIdx.x & 31; rt < row_tiles(a, s); rt += 32) n += row_tile(a, s, rt).tiles + kEntryCost;
     return warp_sum(n);
 }
 
@@ -106,28 +108,28 @@ constexpr int kEntries = 4, kEntryUsers = kSoftWarps + 4 + 5;
 
 // This CTA's range, walked by one warp (start) and its lane 0 (next).
 struct Walk {
-    int64_t t, end, per;
+    int64_t t, end, per, t0;
     Entry e;
     int row_tile_no;
 
     __device__ __forceinline__ bool start(const AttnArgs &a) {
         const int lane = threadIdx.x & 31;
-        // the sequence that holds this CTA's first tile: up to 32 sequences one by one with the warp on
-        // each one's row tiles, more of them with a lane on each
-        const bool few = a.c.batch <= 32;
+        // the sequence that holds this CTA's first tile: a lane on each sequence, or, where a few sequences
+        // have many row tiles (about 600 clocks a sequence against 60 a row tile), the warp on each one's row tiles
+        const bool few = a.c.batch <= 32 && 10ll * a.c.batch < ((int64_t)a.c.max_rows * a.group + kRows - 1) / kRows;
         const int lanes_per = (a.c.batch + 31) / 32;
         int64_t mine = 0;
         if (few) {
             const Seq q = lane < a.c.batch ? sequence(a.c, lane) : Seq{0, 0, 0};
             for (int i = 0; i < a.c.batch; ++i) {
                 const Seq at = {0, __shfl_sync(0xFFFFFFFFu, q.n, i), __shfl_sync(0xFFFFFFFFu, q.kv, i)};
-                const int64_t n = head_tiles_warp(a, at) * a.c.KH;
+                const int64_t n = head_places_warp(a, at) * a.c.KH;
                 if (lane == i) mine = n;
             }
         } else {
             for (int j = 0; j < lanes_per; ++j) {
                 const int i = lane * lanes_per + j;
-                if (i < a.c.batch) mine += head_tiles(a, sequence(a.c, i)) * a.c.KH;
+                if (i < a.c.batch) mine += head_places(a, sequence(a.c, i)) * a.c.KH;
             }
         }
         const int64_t upto = warp_scan(mine), total = __shfl_sync(0xFFFFFFFFu, upto, 31);
@@ -139,11 +141,11 @@ struct Walk {
         int64_t rel = t - __shfl_sync(0xFFFFFFFFu, upto - mine, owner);
         e.b = owner * lanes_per;
         e.s = sequence(a.c, e.b);
-        int64_t per_head = head_tiles_warp(a, e.s);
+        int64_t per_head = head_places_warp(a, e.s);
         while (rel >= per_head * a.c.KH && e.b + 1 < a.c.batch) {
             rel -= per_head * a.c.KH;
             e.s = sequence(a.c, ++e.b);
-            per_head = head_tiles_warp(a, e.s);
+            per_head = head_places_warp(a, e.s);
         }
         e.head = (int)(rel / per_head);
         rel -= e.head * per_head;
@@ -151,7 +153,7 @@ struct Walk {
         row_tile_no = 0;
         const int n_tiles = row_tiles(a, e.s);
         for (int r0 = 0; r0 < n_tiles; r0 += 32) {
-            const int64_t n = r0 + lane < n_tiles ? row_tile(a, e.s, r0 + lane).tiles : 0, sum = warp_scan(n);
+            const int64_t n = r0 + lane < n_tiles ? row_tile(a, e.s, r0 + lane).tiles + kEntryCost : 0, sum = warp_scan(n);
             const uint32_t has = __ballot_sync(0xFFFFFFFFu, rel < sum);
             if (has) {
                 const int l = __ffs(has) - 1;
@@ -162,20 +164,22 @@ struct Walk {
             rel -= __shfl_sync(0xFFFFFFFFu, sum, 31);
         }
         e.rt = row_tile(a, e.s, row_tile_no);
-        e.tile0 = (int)rel;
+        t0 = t - rel;
         return true;
     }
-    // Completes the entry at t.
-    __device__ __forceinline__ void take() {
-        e.count = (int)min((int64_t)(e.rt.tiles - e.tile0), end - t);
-        const int64_t t0 = t - e.tile0;
-        e.first_cta = (int)(t0 / per);
-        e.last_cta = (int)((t0 + e.rt.tiles - 1) / per);
-        t += e.count;
+    // The entry at t, whose row tile has the places from t0: kEntryCost without a tile, then its tiles.  False if it gets no tile here.
+    __device__ __forceinline__ bool take() {
+        const int64_t tiles0 = t0 + kEntryCost, stop = min(end, tiles0 + e.rt.tiles);
+        e.tile0 = (int)max((int64_t)0, t - tiles0);
+        e.count = (int)max((int64_t)0, stop - max(t, tiles0));
+        e.first_cta = (int)(tiles0 / per);
+        e.last_cta = (int)((tiles0 + e.rt.tiles - 1) / per);
+        t = max(t + 1, stop);
+        return e.count > 0;
     }
-    // Goes to the entry after it, which begins a row tile.
+    // Goes to the row tile after it.
     __device__ __forceinline__ void next(const AttnArgs &a) {
-        e.tile0 = 0;
+        t0 = t;
         if (e.rt.r0 + e.rt.n_rows < e.s.n * a.group) {
             e.rt = row_tile(a, e.s, ++row_tile_no);
             return;
@@ -403,16 +407,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
             // ---- the schedule ----
             Walk w;
             bool more = w.start(a);
-            for (uint32_t i = 0;; ++i) {
+            for (uint32_t i = 0;;) {
+                if (more && !w.take()) {
+                    more = w.t < w.end;
+                    if (more) w.next(a);
+                    continue;
+                }
                 if (!wait(E_EMPTY + i % kEntries, i / kEntries + 1)) break;
-                if (more) w.take();
-                else w.e.count = 0;
+                if (!more) w.e.count = 0;
                 if (lane == 0) *reinterpret_cast<Entry *>(smem + T::oEntry + (i % kEntries) * 64) = w.e;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(E_FULL + i % kEntries));
                 if (!more) break;
-                if (w.t < w.end) w.next(a);
+                ++i;
                 more = w.t < w.end;
+                if (more) w.next(a);
             }
         } else if (warp == 13) {
             // ---- pages, scales, copies ----
