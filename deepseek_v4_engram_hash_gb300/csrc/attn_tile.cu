@@ -4,7 +4,7 @@
 //
 // Mathematics as in attention.cu: t_j = <q, kc_j> c + ev with the value scale in
 // the exponent, p_j = 2^(t_j - M), out = sum p_j vc_j / sum p_j 2^-ev, M raised only
-// when a t passes it by more than 8.
+// when a t passes it by more than 15.
 //
 // A CTA works on up to 256 rows (two halves of 128: rows = new tokens x query
 // heads of one key/value head) and 128 tokens a step, so a converted key or
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
         if (lane == 0) mbar_arrive(bar(E_EMPTY + i % kEntries));
     };
 
-    // 640 threads launch with 96 registers each: 2 x 128 x 128 + 128 x 88 + 2 x 128 x 64 stay within them
+    // 640 threads launch with 96 registers each: 2 x 128 x 136 + 128 x 80 + 2 x 128 x 64 are as many
     if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == 15) {
@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
         }
     } else if (warp >= kSoftWarps) {
         // ---- codes to f16 ----
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         const int wt = threadIdx.x - 32 * kSoftWarps;
         bool ok = true;
         uint32_t n = 0;
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
         }
     } else {
         // ---- softmax, one thread a row ----
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
         const int h = warp >> 2, row = (warp & 3) * 32 + lane;            // row of the half = tensor-memory lane
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t tO = lanes + T::cO + h * D;
@@ -626,7 +626,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                 const uint32_t tS = lanes + T::cS + h * 128 + (j & 1) * kPartTok;
                 if (!(ok = wait(S_FULL + 2 * h + (j & 1), ns >> 1))) break;
                 tc_fence_after();
-                // u_j = t_j - M with the bound so far; what passes it by more than 8 raises the bound
+                // u_j = t_j - M with the bound so far.  The probabilities are formed beside the search for the largest u and
+                // kept unless that passes 15 (2^15 is near f16's largest): then, as on a row's first tokens, M is raised
+                // and they are formed again (waiting for the largest first: 348 against 343 us for 4096 tokens behind 4096).
                 const float4 *mt = meta + (n % kMetaRing) * kGroups + (j & 1) * (kGroups / 2);
                 float t[64];
 #pragma unroll
@@ -650,11 +652,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                     for (int k = 0; k < kPartTok; ++k)
                         if (k >= hi_col || k < lo_col) t[k] = -INFINITY;
                 }
+                uint32_t u[2][16];
+                float l;
+                auto form = [&]() {
+                    l = 0.f;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        uint64_t sum[2][2] = {};
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {
+                                const float x = exp2_approx(t[32 * b + 16 * g + 2 * k]), y = exp2_approx(t[32 * b + 16 * g + 2 * k + 1]);
+                                sum[g][k & 1] = add2(sum[g][k & 1], pack2(x, y));
+                                u[b][8 * g + k] = pack_f16x2(x, y);
+                            }
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            float x, y;
+                            unpack2(add2(sum[g][0], sum[g][1]), x, y);
+                            l = fmaf(x + y, mt[2 * b + g].z, l);
+                        }
+                    }
+                };
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int k = 0; k < kPartTok / 2; ++k) mx[k & 3] = max3(mx[k & 3], t[2 * k], t[2 * k + 1]);
                 const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                if (__any_sync(0xFFFFFFFFu, tmax > (M == -INFINITY ? -INFINITY : kLazy))) {
+                form();
+                if (__any_sync(0xFFFFFFFFu, tmax > (M == -INFINITY ? -INFINITY : kLazyWide))) {
                     const float m2 = fmaxf(M, m0 + tmax), f = M == m2 ? 1.f : exp2_approx(M - m2);
                     if (m2 != -INFINITY) {
                         const float d = m0 - m2;
@@ -675,27 +701,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                             tmem_st16(tO + d, o);
                         }
                     }
+                    form();
                 }
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    uint32_t u[16];
-                    uint64_t sum[2][2] = {};
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-#pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            const float x = exp2_approx(t[32 * b + 16 * g + 2 * k]), y = exp2_approx(t[32 * b + 16 * g + 2 * k + 1]);
-                            sum[g][k & 1] = add2(sum[g][k & 1], pack2(x, y));
-                            u[8 * g + k] = pack_f16x2(x, y);
-                        }
-                    tmem_st16(tS + 16 * b, u);
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        float x, y;
-                        unpack2(add2(sum[g][0], sum[g][1]), x, y);
-                        L = fmaf(x + y, mt[2 * b + g].z, L);
-                    }
-                }
+                tmem_st16(tS, u[0]);
+                tmem_st16(tS + 16, u[1]);
+                L += l;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
