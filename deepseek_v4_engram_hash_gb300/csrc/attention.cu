@@ -86,6 +86,11 @@ __device__ __forceinline__ Plan plan_of(const AttnArgs &a, int b) {
     return p;
 }
 
+// x / y of non-negative numbers, in 32 bits where both fit (several times faster).
+__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
+    return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+}
+
 // An entry's places in the list; none for a sequence without rows.
 __device__ __forceinline__ int64_t places_of(const Plan &p) { return p.tiles ? p.tiles + kEntryCost : 0; }
 
@@ -96,19 +101,31 @@ __device__ __forceinline__ int64_t places_of(const Plan &p) { return p.tiles ? p
 // and the groups are added in order.
 template <int TYPE, int D>
 __device__ __forceinline__ void join_parts(const AttnArgs &a, int row0, int head, int n_rows, int64_t first, int n, uint8_t *smem) {
-    constexpr int kPart = Few<D>::kPart;
+    constexpr int kPart = Few<D>::kPart, kAhead = 16;
     float *fac = reinterpret_cast<float *>(smem) + 4 * kThreads;         // [n_rows][n]
     float4 *sums = reinterpret_cast<float4 *>(smem);                     // [groups][items]
     float *row_m = fac + n_rows * n, *row_l = row_m + kMaxRows;
     const int tid = threadIdx.x, lane = tid & 31;
     auto at = [&](int c) { return a.ws.part + ((first + c) * 2 + (c == 0 ? 1 : 0)) * kPart; };
+    const int items = n_rows * (D / 4), groups = items >= kThreads ? 1 : kThreads / items;
+    const int grp = groups > 1 ? tid / items : 0;
+    float4 x[kAhead];
+    auto load = [&](int i, int c0) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            x[j] = __ldcg(reinterpret_cast<const float4 *>(at(min(c0 + j * groups, n - 1))) + min(i, items - 1));
+    };
+    int i = groups > 1 ? tid % items : tid;
+    load(i, grp);                                                        // beside the factors
     for (int r = tid >> 5; r < n_rows; r += kWarps) {
-        float m = -INFINITY, l = 0.f;
-        for (int c = lane; c < n; c += 32) m = fmaxf(m, __ldcg(at(c) + kMaxRows * D + r));
+        float m = -INFINITY, l = 0.f, mc = -INFINITY, lc = 0.f;
+        if (lane < n) mc = __ldcg(at(lane) + kMaxRows * D + r), lc = __ldcg(at(lane) + kMaxRows * D + kMaxRows + r);
+        m = mc;
+        for (int c = lane + 32; c < n; c += 32) m = fmaxf(m, __ldcg(at(c) + kMaxRows * D + r));
 #pragma unroll
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         for (int c = lane; c < n; c += 32) {
-            const float mc = __ldcg(at(c) + kMaxRows * D + r), lc = __ldcg(at(c) + kMaxRows * D + kMaxRows + r);
+            if (c != lane) mc = __ldcg(at(c) + kMaxRows * D + r), lc = __ldcg(at(c) + kMaxRows * D + kMaxRows + r);
             const float f = mc == -INFINITY ? (lc == 0.f ? 0.f : 1.f) : exp2_approx(mc - m);
             fac[r * n + c] = f;
             l = fmaf(lc, f, l);
@@ -118,18 +135,15 @@ __device__ __forceinline__ void join_parts(const AttnArgs &a, int row0, int head
         if (lane == 0) row_m[r] = m, row_l[r] = l;
     }
     __syncthreads();
-    const int items = n_rows * (D / 4), groups = items >= kThreads ? 1 : kThreads / items;
-    for (int i0 = 0; i0 < items; i0 += kThreads) {
-        const int i = i0 + (groups > 1 ? tid % items : tid), grp = groups > 1 ? tid / items : 0, r = i / (D / 4);
+    for (int i0 = 0; i0 < items; i0 += kThreads, i += kThreads) {
+        const int r = i / (D / 4);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i0) load(i, grp);
         if (i < items && grp < groups) {
-            for (int c0 = grp; c0 < n; c0 += 16 * groups) {
-                float4 x[16];
+            for (int c0 = grp; c0 < n; c0 += kAhead * groups) {
+                if (c0 != grp) load(i, c0);
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    x[j] = __ldcg(reinterpret_cast<const float4 *>(at(min(c0 + j * groups, n - 1))) + i);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
+                for (int j = 0; j < kAhead; ++j) {
                     const int c = c0 + j * groups;
                     const float f = c < n ? fac[r * n + c] : 0.f;
                     if (c < n) acc.x = fmaf(x[j].x, f, acc.x), acc.y = fmaf(x[j].y, f, acc.y), acc.z = fmaf(x[j].z, f, acc.z), acc.w = fmaf(x[j].w, f, acc.w);
@@ -141,8 +155,8 @@ __device__ __forceinline__ void join_parts(const AttnArgs &a, int row0, int head
             __syncthreads();
             if (grp == 0)
                 for (int k = 1; k < groups; ++k) {
-                    const float4 x = sums[k * items + i];
-                    acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
+                    const float4 y = sums[k * items + i];
+                    acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
                 }
         }
         if (i < items && grp == 0) store_row4<TYPE, D>(a, row0, head, r, i % (D / 4), acc, row_m[r], row_l[r]);
@@ -173,27 +187,37 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_few_kernel(const __
     __syncthreads();
 
     // this CTA's range of the list
+    int b = 0;
+    int64_t before = 0, total;
+    Plan pl;
     const int lanes_per = (a.c.batch + 31) / 32;
-    int64_t mine = 0;
-    for (int j = 0; j < lanes_per; ++j) {
-        const int b = lane * lanes_per + j;
-        if (b < a.c.batch) mine += places_of(plan_of(a, b)) * a.c.KH;
-    }
-    int64_t upto = mine;
+    int64_t mine = 0, upto = 0;
+    if (a.c.batch == 1) {
+        pl = plan_of(a, 0);
+        total = places_of(pl) * a.c.KH;
+    } else {
+        for (int j = 0; j < lanes_per; ++j) {
+            const int i = lane * lanes_per + j;
+            if (i < a.c.batch) mine += places_of(plan_of(a, i)) * a.c.KH;
+        }
+        upto = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-        if (lane >= o) upto += x;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        total = __shfl_sync(0xFFFFFFFFu, upto, 31);
     }
-    const int64_t total = __shfl_sync(0xFFFFFFFFu, upto, 31);
-    const int64_t per = max((int64_t)1, (total + gridDim.x - 1) / gridDim.x);
+    const int64_t per = max((int64_t)1, divide(total + gridDim.x - 1, gridDim.x));
     int64_t t = blockIdx.x * per;
     const int64_t end = min(total, t + per);
     if (t >= end) return;
-    const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, t < upto)) - 1;
-    int b = owner * lanes_per;
-    int64_t before = __shfl_sync(0xFFFFFFFFu, upto - mine, owner);
-    Plan pl = plan_of(a, b);
+    if (a.c.batch > 1) {
+        const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, t < upto)) - 1;
+        b = owner * lanes_per;
+        before = __shfl_sync(0xFFFFFFFFu, upto - mine, owner);
+        pl = plan_of(a, b);
+    }
 
     uint32_t phase = 0;                              // parity of each stage's next wait
     int stage = 0;
@@ -203,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_few_kernel(const __
             pl = plan_of(a, ++b);
         }
         const int64_t rel = t - before;
-        const int head = (int)(rel / places_of(pl));
+        const int head = (int)divide(rel, places_of(pl));
         const int64_t tiles_t0 = before + head * places_of(pl) + kEntryCost, stop = min(end, tiles_t0 + pl.tiles);
         const int tile0 = (int)max((int64_t)0, t - tiles_t0), count = (int)max((int64_t)0, stop - max(t, tiles_t0));
         t = max(t + 1, stop);
@@ -224,6 +248,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_few_kernel(const __
             return (uint32_t)a.c.k_scales[i] | (uint32_t)a.c.v_scales[i] << 8;
         };
         int id_cur = load_id(0), id_next = load_id(1);
+        // the queries, asked for beside the page ids
+        uint32_t raw_q[NT][D / 8];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = 8 * nt + g;
+            const int64_t at = (int64_t)(pl.s.row0 + r / a.group) * a.q_stride + (int64_t)(head * a.group + r % a.group) * D + q4 * (D / 4);
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + at);
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                const uint4 x = r < n_rows ? src[k] : make_uint4(0u, 0u, 0u, 0u);
+                raw_q[nt][4 * k] = x.x, raw_q[nt][4 * k + 1] = x.y, raw_q[nt][4 * k + 2] = x.z, raw_q[nt][4 * k + 3] = x.w;
+            }
+        }
         auto issue = [&](int u, int st, int cur_block) {
             const int ids = (u >> 4) == cur_block ? id_cur : id_next;
             const int id0 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (u & 15)), id1 = __shfl_sync(0xFFFFFFFFu, ids, 2 * (u & 15) + 1);
@@ -249,29 +286,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_few_kernel(const __
         int lim[NT][2], low[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int r = 8 * nt + g;
-            const bool live = r < n_rows;
-            const int64_t at = (int64_t)(pl.s.row0 + r / a.group) * a.q_stride + (int64_t)(head * a.group + r % a.group) * D + q4 * (D / 4);
-            float x[D / 4];
             uint32_t m = 0;
 #pragma unroll
-            for (int e = 0; e < D / 4; e += 8) {
-                float y[8] = {};
-                if (live) load8<TYPE>(a.q, at + e, y);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    x[e + k] = y[k];
-                    m = max(m, __float_as_uint(y[k]) & 0x7FFFFFFFu);
-                }
+            for (int k = 0; k < D / 8; ++k) {
+                const float2 f = q_pair<TYPE>(raw_q[nt][k]);
+                m = max(m, max(__float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu));
             }
             m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
             m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
             float down, f;
             q_scale(m, a.scale_log2, down, f);
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                qb[nt][k][0] = pack_f16x2(x[4 * k] * down, x[4 * k + 1] * down);
-                qb[nt][k][1] = pack_f16x2(x[4 * k + 2] * down, x[4 * k + 3] * down);
+            for (int k = 0; k < D / 8; ++k) {
+                const float2 x = q_pair<TYPE>(raw_q[nt][k]);
+                qb[nt][k >> 1][k & 1] = pack_f16x2(x.x * down, x.y * down);
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -435,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_few_kernel(const __
                         make_float4(o[nt][2 * i][e], o[nt][2 * i][2 + e], o[nt][2 * i + 1][e], o[nt][2 * i + 1][2 + e]);
             }
         __syncthreads();
-        const int64_t first_cta = tiles_t0 / per, last_cta = (tiles_t0 + pl.tiles - 1) / per;
+        const int64_t first_cta = divide(tiles_t0, per), last_cta = divide(tiles_t0 + pl.tiles - 1, per);
         const bool alone = first_cta == last_cta;
         float *part = a.ws.part + ((int64_t)blockIdx.x * 2 + (blockIdx.x == first_cta ? 1 : 0)) * F::kPart;
         for (int i = tid; i < n_rows * (D / 4); i += kThreads) {
@@ -461,14 +489,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_few_kernel(const __
         }
         if (!alone) {
             // the last CTA of the entry to arrive joins the partial results, in CTA order
-            __threadfence();
             __syncthreads();
             if (tid == 0) {
                 const int n = (int)(last_cta - first_cta);
-                const bool last = atomicAdd(&a.ws.arrived[first_cta], 1) == n;
+                const bool last = arrive(&a.ws.arrived[first_cta]) == n;
                 if (last) a.ws.arrived[first_cta] = 0;
                 flags[1] = last;
-                __threadfence();
             }
             __syncthreads();
             if (flags[1]) join_parts<TYPE, D>(a, pl.s.row0, head, n_rows, first_cta, (int)(last_cta - first_cta) + 1, smem);

@@ -108,14 +108,18 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
 // Where float4 i of row r lies in a warp's sums (spreads the rows over the banks).
 __device__ __forceinline__ int swz(int r, int i) { return i ^ (r >> 1 & 3); }
 
-// Joins a partial result (bound m2, sum l2, values x) to (m, l, acc).
-__device__ __forceinline__ void join(float &m, float &l, float4 &acc, float m2, float l2, const float4 &x) {
-    if (m2 == -INFINITY && l2 == 0.f) return;                         // saw nothing
-    const float n = fmaxf(m, m2);
-    const float f = m == -INFINITY ? 0.f : exp2_approx(m - n), f2 = m2 == -INFINITY ? 1.f : exp2_approx(m2 - n);
-    m = n;
-    l = l * f + l2 * f2;
-    acc.x = acc.x * f + x.x * f2, acc.y = acc.y * f + x.y * f2, acc.z = acc.z * f + x.z * f2, acc.w = acc.w * f + x.w * f2;
+// Two query elements to f32.
+template <int TYPE>
+__device__ __forceinline__ float2 q_pair(uint32_t u) {
+    return TYPE == ENGRAM_T_BF16 ? make_float2(bf16_lo(u), bf16_hi(u)) : __half22float2(*reinterpret_cast<const __half2 *>(&u));
+}
+
+// One more arrival at a counter: how many came before.  Releases what the block wrote before its last
+// barrier and acquires what the others released.
+__device__ __forceinline__ int arrive(int *counter) {
+    int before;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+    return before;
 }
 
 // Four output values of tile row rr (token rr / group, head rr % group) and, with the first, its lse.

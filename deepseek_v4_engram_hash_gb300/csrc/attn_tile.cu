@@ -589,9 +589,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                 lo_col = live && a.window ? pos - a.window + 1 - tb0 : 0;
                 // the row's largest element, then the row as f16
                 const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + q_row * a.q_stride + (int64_t)q_head * D);
-                auto pair_of = [&](uint32_t u) {
-                    return TYPE == ENGRAM_T_BF16 ? make_float2(bf16_lo(u), bf16_hi(u)) : __half22float2(*reinterpret_cast<__half2 *>(&u));
-                };
                 uint32_t m = 0, w[D / 2];
 #pragma unroll
                 for (int k = 0; k < D / 8; ++k) {
@@ -600,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                 }
 #pragma unroll
                 for (int k = 0; k < D / 2; ++k) {
-                    const float2 f = pair_of(w[k]);
+                    const float2 f = q_pair<TYPE>(w[k]);
                     m = max(m, max(__float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu));
                 }
                 float down;
@@ -611,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                     uint32_t o[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const float2 f = pair_of(w[4 * k + q]);
+                        const float2 f = q_pair<TYPE>(w[4 * k + q]);
                         o[q] = pack_f16x2(f.x * down, f.y * down);
                     }
                     sts128(dst + (k >> 3) * T::kSub + (((k & 7) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
@@ -763,14 +760,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
             float *stat = a.ws.part + slot * T::kPart + kRows * D + h * kHalf + row;
             stat[0] = L == 0.f ? -INFINITY : M;
             stat[kRows] = L;
-            __threadfence();
             if (!(ok = half_sync())) continue;
             if ((warp & 3) == 0 && lane == 0) {
                 int *arrived = a.ws.arrived + e.first_cta * 2 + h;
-                const bool last = atomicAdd(arrived, 1) == e.last_cta - e.first_cta;
+                const bool last = arrive(arrived) == e.last_cta - e.first_cta;
                 if (last) *arrived = 0;
                 last_flag[h] = last;
-                __threadfence();
             }
             if (!(ok = half_sync())) continue;
             if (last_flag[h]) {
