@@ -19,7 +19,7 @@ namespace {
 constexpr int kMaxDim = 16384;
 
 template <int XT, int RT, int NV>
-__global__ void __launch_bounds__(1024) residual_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(1024, 2) residual_norm_kernel(const NormArgs a) {
     __shared__ float part[32];
     __shared__ uint32_t amax[kMaxDim / 16];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, threads = blockDim.x;
@@ -127,11 +127,11 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const NormArgs a) {
 
 template <int XT, int RT>
 cudaError_t launch_typed(const NormArgs &a, cudaStream_t s) {
-    // One chunk a thread or two: two keep more bytes of a 32-bit residual in flight on an SM (16384 rows of
-    // 4096: 115 against 147 us), one shortens a row's time, which counts where a 16-bit residual is read (1537
-    // rows of 5120: 15.3 against 16.2 us) or the rows are few (one row: 2.6 against 3.1 us).
+    // Two chunks a thread keep more bytes in flight on an SM (16384 rows of 4096, 32-bit residual: 115 against 147
+    // us; 1537 rows of 5120, 16-bit: 16.0 against 17.1); one a thread shortens the time of a row, which counts while
+    // the rows do not fill the SMs (one row: 2.6 against 3.1 us).
     const int chunks = a.dim >> 3;
-    const bool one = chunks <= 256 || (chunks <= 1024 && (RT != ENGRAM_T_F32 || a.rows <= a.sms));
+    const bool one = chunks <= 256 || (chunks <= 1024 && a.rows <= a.sms);
     const int threads = ((one ? chunks : (chunks + 1) / 2) + 31) / 32 * 32;
     if (one)
         residual_norm_kernel<XT, RT, 1><<<a.rows, threads, 0, s>>>(a);
