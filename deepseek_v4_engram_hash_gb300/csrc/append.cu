@@ -9,7 +9,7 @@
 // order matters.  Further blocks rotate the queries.
 // Bound by memory for prompts and by launch and load latency for single tokens.  64 registers a thread
 // keep 1024 threads on an SM: a 4096-token prompt of 32 query and 8 key/value heads of
-// 128 (94 MB, 13.9 us at the copy rate) takes 22.3 us; without the bound 26.6 us.
+// 128 (94 MB, 13.9 us at the copy rate) takes 21.4 us; without the bound over 26 us.
 #include "sublayer.cuh"
 
 namespace engram {
@@ -107,24 +107,25 @@ __device__ __forceinline__ void rotate(const Item &it, const float (&t)[16], flo
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float c = t[2 * e], s = t[2 * e + 1], u = x[e], w = y[e];
-            x[e] = __fsub_rn(__fmul_rn(u, c), __fmul_rn(w, s));
-            y[e] = __fadd_rn(__fmul_rn(w, c), __fmul_rn(u, s));
+            x[e] = fmaf(u, c, -(w * s));
+            y[e] = fmaf(w, c, u * s);
         }
     } else if (it.turn == kAdjacent) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float c = t[2 * e], s = t[2 * e + 1], u = x[2 * e], w = x[2 * e + 1];
-            x[2 * e] = __fsub_rn(__fmul_rn(u, c), __fmul_rn(w, s));
-            x[2 * e + 1] = __fadd_rn(__fmul_rn(w, c), __fmul_rn(u, s));
+            x[2 * e] = fmaf(u, c, -(w * s));
+            x[2 * e + 1] = fmaf(w, c, u * s);
             const float c2 = t[8 + 2 * e], s2 = t[9 + 2 * e], u2 = y[2 * e], w2 = y[2 * e + 1];
-            y[2 * e] = __fsub_rn(__fmul_rn(u2, c2), __fmul_rn(w2, s2));
-            y[2 * e + 1] = __fadd_rn(__fmul_rn(w2, c2), __fmul_rn(u2, s2));
+            y[2 * e] = fmaf(u2, c2, -(w2 * s2));
+            y[2 * e + 1] = fmaf(w2, c2, u2 * s2);
         }
     }
 }
 
 // Query rows, `per` of a block at a time: a thread keeps its place in a head (and its angles) and goes
-// through the heads, the first loaded beside the row's sequence and angles.  It writes what it read alone, so q_out may be q.
+// through the heads, the first loaded beside the row's sequence and angles.
+// It writes what it read alone, so q_out may be q.
 template <int TYPE>
 __device__ __forceinline__ void query_rows(const AppendArgs &a, int block) {
     const int per = a.rows_per_block, threads = blockDim.x / per, t = threadIdx.x % threads;
@@ -134,9 +135,18 @@ __device__ __forceinline__ void query_rows(const AppendArgs &a, int block) {
     const int step = threads / items;
     const Item it = item_of(a, t % items, a.rot > 0);
     const int64_t in = (int64_t)r * a.q_stride, to = (int64_t)r * a.q_out_stride;
-    float x[8], y[8];
+    constexpr int kHeads = TYPE == ENGRAM_T_F32 ? 1 : 2;              // loaded at a time (64 registers a thread)
+    Raw8<TYPE> x[kHeads], y[kHeads];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i)
+            if (h + i * step < a.H) {
+                x[i].load(a.q, in + (int64_t)(h + i * step) * a.c.D + it.c0);
+                y[i].load(a.q, in + (int64_t)(h + i * step) * a.c.D + it.c1);
+            }
+    };
     int h = t / items;
-    if (h < a.H) load_item<TYPE>(a.q, in + (int64_t)h * a.c.D, it, x, y);
+    load(h);
     const int b = sequence_of_row(a.c, r);
     if (b >= a.c.batch) return;
     const Seq s = sequence(a.c, b);
@@ -148,16 +158,24 @@ __device__ __forceinline__ void query_rows(const AppendArgs &a, int block) {
     float cs[16];
     if (!empty) load_angles(a, it, pos, cs);
     while (h < a.H) {
-        if (empty) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
-        } else {
-            rotate(it, cs, x, y);
+        for (int i = 0; i < kHeads; ++i) {
+            float u[8], w[8];
+            x[i].get(u);
+            y[i].get(w);
+            if (empty) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[e] = w[e] = 0.f;
+            } else {
+                rotate(it, cs, u, w);
+            }
+            if (h + i * step < a.H) {
+                store8<TYPE>(a.q_out, to + (int64_t)(h + i * step) * a.c.D + it.c0, u);
+                store8<TYPE>(a.q_out, to + (int64_t)(h + i * step) * a.c.D + it.c1, w);
+            }
         }
-        store8<TYPE>(a.q_out, to + (int64_t)h * a.c.D + it.c0, x);
-        store8<TYPE>(a.q_out, to + (int64_t)h * a.c.D + it.c1, y);
-        h += step;
-        if (h < a.H) load_item<TYPE>(a.q, in + (int64_t)h * a.c.D, it, x, y);
+        h += kHeads * step;
+        if (h < a.H) load(h);
     }
 }
 
@@ -196,7 +214,7 @@ __global__ void __launch_bounds__(W == 32 ? 128 : W, W == 32 ? 4 : 1024 / W) kv_
     const Item it = item_of(a, tid % items, !which && a.rot > 0);
 
     float x[NP][8], y[NP][8];
-    uint32_t m = 0u;
+    float big = 0.f;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const int t = t0 + i * step;
@@ -206,11 +224,10 @@ __global__ void __launch_bounds__(W == 32 ? 128 : W, W == 32 ? 4 : 1024 / W) kv_
             load_angles(a, it, lo + t, cs);
             rotate(it, cs, x[i], y[i]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                m = max(m, max(__float_as_uint(x[i][e]) & 0x7FFFFFFFu, __float_as_uint(y[i][e]) & 0x7FFFFFFFu));
+            for (int e = 0; e < 8; ++e) big = amax3(big, x[i][e], y[i][e]);
         }
     }
-    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(big));   // bits of numbers, then infinity, then NaN
     if (W > 32) {
         if ((tid & 31) == 0) part[tid >> 5] = m;
         __syncthreads();
@@ -252,8 +269,8 @@ __global__ void __launch_bounds__(W == 32 ? 128 : W, W == 32 ? 4 : 1024 / W) kv_
 template <int TYPE, int W, int NP>
 cudaError_t launch_units(AppendArgs &a, cudaStream_t s) {
     const int threads = W == 32 ? 128 : W, kUnits = W == 32 ? 4 : 1;
-    // a whole block a query row while the rows do not fill the GPU, else a warp (4096 rows of 32 heads: 22.3 us, with
-    // 64 threads a row 23.9, with 128 25.6)
+    // a whole block a query row while the rows do not fill the GPU, else a warp (4096 rows of 32 heads: 21.4 us, with
+    // 64 threads a row 22.9)
     a.rows_per_block = a.c.rows < 1024 ? 1 : threads / 32;
     const int64_t q_blocks = a.q ? (a.c.rows + a.rows_per_block - 1) / a.rows_per_block : 0;
     const int64_t units = (int64_t)a.slots * 2 * a.c.KH;

@@ -86,9 +86,10 @@ __global__ void __launch_bounds__(1024, 2) residual_norm_kernel(const NormArgs a
         uint32_t m[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            m[v] = 0u;
+            float big = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) m[v] = max(m[v], __float_as_uint(r[v][e]) & 0x7FFFFFFFu);
+            for (int e = 0; e < 8; e += 2) big = amax3(big, r[v][e], r[v][e + 1]);
+            m[v] = __float_as_uint(big);                          // ordered: numbers, infinity, NaN
         }
         if (in_warp) {
 #pragma unroll

@@ -33,6 +33,18 @@ __device__ __forceinline__ void load8(const void *p, int64_t i, float (&x)[8]) {
     }
 }
 
+// Eight elements as they lie in memory.
+template <int TYPE>
+struct Raw8 {
+    uint4 v[TYPE == ENGRAM_T_F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void *p, int64_t i) {
+        const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p) + i * (TYPE == ENGRAM_T_F32 ? 4 : 2));
+        v[0] = s[0];
+        if (TYPE == ENGRAM_T_F32) v[sizeof(v) / 16 - 1] = s[1];
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const { load8<TYPE>(v, 0, x); }
+};
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
@@ -56,6 +68,12 @@ __device__ __forceinline__ void store8(void *p, int64_t i, const float (&x)[8]) 
 // ---------------------------------------------------------------------------
 // 8-bit blocks
 // ---------------------------------------------------------------------------
+// The larger of m and |x|, |y|; a NaN among them stays.
+__device__ __forceinline__ float amax3(float m, float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(x)), "f"(fabsf(y)));
+    return r;
+}
 // The e8m0 byte of a block whose largest |value| has the f32 bits `amax`: the
 // smallest 2^e with amax <= 448 2^e.  With amax = m 2^x, 1 <= m < 2, and 448 =
 // 1.75 x 2^8, that is e = x - 8, one more when m > 1.75.  Infinities and NaN
