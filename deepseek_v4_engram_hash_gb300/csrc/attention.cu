@@ -54,7 +54,7 @@ struct Few {
     static constexpr int oBars = kRegion + 2 * kWarps * kMaxRows * 4, oFlags = oBars + kWarps * kStages * 8;
     static constexpr size_t kSmem = 1024 + oFlags + 16;
     static_assert(kMaxRows * D * 4 <= kRing && kCtasPerSm * (kSmem + 1024) <= 227 * 1024, "shared memory");
-    static_assert(kThreads * 16 + (kMaxRows * kCtasPerSm * 160 + 2 * kMaxRows) * 4 <= kRegion, "factors of a join");
+    static_assert(kThreads * 16 + (kMaxRows * kCtasPerSm * kMaxSms + 2 * kMaxRows) * 4 <= kRegion, "factors of a join");
     static constexpr int kPart = kMaxRows * (D + 2); // floats of a partial result
 };
 

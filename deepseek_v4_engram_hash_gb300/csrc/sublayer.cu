@@ -165,9 +165,12 @@ int engram_attn_create(engram_attn **out) {
     *out = nullptr;
     engram_attn *h = new (std::nothrow) engram_attn();
     if (!h) return ENGRAM_E_CUDA;
-    if (cudaGetDevice(&h->device) != cudaSuccess ||
-        cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
-        cudaMalloc(&h->ws.part, attn_part_floats(h->sms) * sizeof(float)) != cudaSuccess ||
+    h->sms = sm_count();
+    if (h->sms > kMaxSms) {
+        delete h;
+        return ENGRAM_E_UNSUPPORTED;
+    }
+    if (!h->sms || cudaGetDevice(&h->device) != cudaSuccess || cudaMalloc(&h->ws.part, attn_part_floats(h->sms) * sizeof(float)) != cudaSuccess ||
         cudaMalloc(&h->ws.arrived, attn_counters(h->sms) * sizeof(int)) != cudaSuccess ||
         cudaMemset(h->ws.arrived, 0, attn_counters(h->sms) * sizeof(int)) != cudaSuccess || !error_word()) {
         engram_attn_destroy(h);
@@ -204,7 +207,9 @@ int engram_attention(engram_attn *attn, const engram_kv_cache *cache, const engr
     if (batch->rows == 0) return ENGRAM_OK;
     if (!d_q || !d_out) return ENGRAM_E_NULL;
     if (!aligned(d_q, 16) || !aligned(d_out, 16) || !aligned(d_lse, 4)) return ENGRAM_E_ALIGN;
-    if (!(a.c.err = error_word())) return ENGRAM_E_CUDA;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || !(a.c.err = error_word())) return ENGRAM_E_CUDA;
+    if (dev != attn->device) return ENGRAM_E_INVALID;
     a.ws = attn->ws;
     a.q = d_q;
     a.out = d_out;

@@ -180,6 +180,7 @@ struct AppendArgs {
 };
 cudaError_t launch_kv_append(AppendArgs a, cudaStream_t s);
 
+constexpr int kMaxSms = 160;            // what the joins' shared memory is sized for (GB300: 152)
 // Workspace of the attention: two partial results a CTA and one arrival counter a CTA.
 struct AttnWorkspace {
     float *part;

@@ -342,7 +342,9 @@ int engram_selftest_wait_timeout(int32_t limit_us, uintptr_t stream);
 /* ---------------------------------------------------------------------------
  * The attention sub-layer behind the engram: norm, cache append, attention.
  * (The pages have no counterpart: these entry points belong to this library's
- * ABI.)  The projections between them are engram_project.
+ * ABI.)  The projections between them are engram_project.  All of them only
+ * enqueue work and can be captured (engram_attn_create, which looks up the
+ * device's error word, comes before any capture).
  *
  * 8-bit blocks.  A block of values is held as e4m3 codes with one power-of-two
  * scale: the smallest 2^e, e >= -126, with amax <= 448 * 2^e;
@@ -436,8 +438,10 @@ int engram_kv_append(const engram_kv_cache *cache, const engram_kv_batch *batch,
 
 /* The attention's workspace on the current device: partial results of the
  * splits along the cache and their arrival counters (zero between calls).  Its size
- * does not depend on the calls it serves.  One call at a time on a workspace:
- * calls that may overlap on the GPU need one each. */
+ * does not depend on the calls it serves (about 41 MB on a GB300).  One call at
+ * a time on a workspace: calls that may overlap on the GPU need one each.
+ * ENGRAM_E_UNSUPPORTED on a GPU of more than 160 SMs; engram_attention refuses a
+ * workspace of another device with ENGRAM_E_INVALID. */
 typedef struct engram_attn engram_attn;
 int engram_attn_create(engram_attn **out);
 /* Zeroes the counters (enqueued on `stream`); after ENGRAM_E_TIMEOUT they may not be. */

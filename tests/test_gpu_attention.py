@@ -307,3 +307,40 @@ def test_captured_decode_steps(E, attn):
 def test_attn_reset(E, attn):
     E.engram_attn_reset(attn)
     _case(E, attn, [1], [2000], 4, 2, 128, 16, 0)
+
+
+@pytest.mark.parametrize("n,H", [(16, 1), (17, 1), (128, 1), (129, 1), (256, 1), (257, 1), (4, 4), (32, 8), (33, 8), (51, 5)])
+def test_row_tile_edges(E, attn, n, H):
+    """Rows of one key/value head around 16, 128 and 256, query groups that do and do not divide them."""
+    _case(E, attn, [n], [n + 100], H, 1, 64, 16, 0, seed=n)
+    _case(E, attn, [n, n], [n, n + 300], H, 1, 128, 64, 1, window=77, seed=n)
+
+
+@pytest.mark.parametrize("batch,new", [(33, 1), (300, 1), (40, 30), (300, 9)])
+def test_many_sequences(E, attn, batch, new):
+    """More sequences than lanes of a warp, some without rows or tokens."""
+    news = [0 if b % 11 == 5 else new if b % 3 else max(1, new // 2) for b in range(batch)]
+    kv = [0 if b % 13 == 4 else news[b] + (b * 37) % 90 for b in range(batch)]
+    _case(E, attn, news, kv, 4, 2, 64, 16, 0, seed=batch)
+
+
+def test_two_workspaces_at_once(E, attn):
+    """Calls that overlap on two streams, each with its own workspace."""
+    other = E.Attention()
+    KH, H, D, pt, n = 2, 8, 128, 64, 20000
+    table = U.pages_for([n], pt, 320)
+    cache = U.Cache(E, 320, KH, pt, D)
+    U.fill_random(cache, table, [n], 3)
+    for new in (1, 40):
+        q = _queries(new, H, D, 0, 5)
+        plan = U.batch(E, table, [new], [n])
+        want = _run(E, attn, cache, plan, q, H, 0.1, 0, 0)
+        outs = []
+        torch.cuda.synchronize()
+        streams = torch.cuda.Stream(), torch.cuda.Stream()
+        for i in range(6):
+            o = torch.empty_like(q)
+            E.engram_attention((attn, other)[i & 1], cache.desc, plan, 0, q, 0, H, 0.1, 0, o, 0, stream=streams[i & 1])
+            outs.append(o)
+        torch.cuda.synchronize()
+        assert E.engram_check() == 0 and all(torch.equal(o, want[0]) for o in outs)
