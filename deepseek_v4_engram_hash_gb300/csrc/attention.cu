@@ -35,7 +35,8 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kUnit = 32, kSub = 16;                 // tokens a warp step, in two parts of one page each
 constexpr int kTile = kUnit * kWarps;                // tokens a CTA step
 constexpr int kMaxRows = 16;
-constexpr int kCtasPerSm = 3;
+constexpr int kCtasPerSm = 3;                        // 2 for 16 rows (248 registers instead of spills at 168: 32 sequences of 4
+                                                     // rows a head of 4 query heads 57 against 68 us)
 constexpr int kEntryCost = 2;                        // places of an entry in the list beside its tiles: 64 sequences 97.3 us, without 104.7
 constexpr uint32_t kNever = 0x7FFFFFFF;
 
@@ -165,7 +166,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs &a, int row0, int head
 
 // NT: groups of 8 query rows.
 template <int TYPE, int D, int NT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_few_kernel(const __grid_constant__ FewParams p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm + 1 - NT) attn_few_kernel(const __grid_constant__ FewParams p) {
     using F = Few<D>;
     constexpr int KS = D / 16;                       // k steps of K Q^T, and 16-dim tiles of V^T P^T
     extern __shared__ uint8_t smem_raw[];
@@ -526,7 +527,7 @@ cudaError_t launch_few(const AttnArgs &a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         attr[dev] = true;
     }
-    attn_few_kernel<TYPE, D, NT><<<a.sms * kCtasPerSm, kThreads, Few<D>::kSmem, s>>>(p);
+    attn_few_kernel<TYPE, D, NT><<<a.sms * (kCtasPerSm + 1 - NT), kThreads, Few<D>::kSmem, s>>>(p);
     return cudaGetLastError();
 }
 
