@@ -623,9 +623,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                 const uint32_t tS = lanes + T::cS + h * 128 + (j & 1) * kPartTok;
                 if (!(ok = wait(S_FULL + 2 * h + (j & 1), ns >> 1))) break;
                 tc_fence_after();
-                // u_j = t_j - M with the bound so far.  The probabilities are formed beside the search for the largest u and
-                // kept unless that passes 15 (2^15 is near f16's largest): then, as on a row's first tokens, M is raised
-                // and they are formed again (waiting for the largest first: 348 against 343 us for 4096 tokens behind 4096).
+                // u_j = t_j - M with the bound so far.  The probabilities 2^u are formed at once and kept unless the sum of
+                // 16 passes 2^15 (f16 holds what is below); then, as on a row's first tokens, the largest u is found, M
+                // raised, and they are formed again.  (The search for the largest u beside each: NEWFIG.)
                 const float4 *mt = meta + (n % kMetaRing) * kGroups + (j & 1) * (kGroups / 2);
                 float t[64];
 #pragma unroll
@@ -650,9 +650,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                         if (k >= hi_col || k < lo_col) t[k] = -INFINITY;
                 }
                 uint32_t u[2][16];
-                float l;
+                float l, big;                                             // their sum, and the largest sum of 16
                 auto form = [&]() {
-                    l = 0.f;
+                    l = big = 0.f;
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         uint64_t sum[2][2] = {};
@@ -669,15 +669,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                             float x, y;
                             unpack2(add2(sum[g][0], sum[g][1]), x, y);
                             l = fmaf(x + y, mt[2 * b + g].z, l);
+                            big = fmaxf(big, x + y);
                         }
                     }
                 };
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int k = 0; k < kPartTok / 2; ++k) mx[k & 3] = max3(mx[k & 3], t[2 * k], t[2 * k + 1]);
-                const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 form();
-                if (__any_sync(0xFFFFFFFFu, tmax > (M == -INFINITY ? -INFINITY : kLazyWide))) {
+                if (__any_sync(0xFFFFFFFFu, M == -INFINITY || big > kLazySum)) {
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int k = 0; k < kPartTok / 2; ++k) mx[k & 3] = max3(mx[k & 3], t[2 * k], t[2 * k + 1]);
+                    const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     const float m2 = fmaxf(M, m0 + tmax), f = M == m2 ? 1.f : exp2_approx(M - m2);
                     if (m2 != -INFINITY) {
                         const float d = m0 - m2;
