@@ -87,11 +87,6 @@ __device__ __forceinline__ Plan plan_of(const AttnArgs &a, int b) {
     return p;
 }
 
-// x / y of non-negative numbers, in 32 bits where both fit (several times faster).
-__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
-    return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
-}
-
 // An entry's places in the list; none for a sequence without rows.
 __device__ __forceinline__ int64_t places_of(const Plan &p) { return p.tiles ? p.tiles + kEntryCost : 0; }
 

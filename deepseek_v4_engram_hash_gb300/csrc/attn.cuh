@@ -42,6 +42,11 @@ __device__ __forceinline__ void q_scale(uint32_t m, float scale_log2, float &dow
     kf = scale_log2 * (e == 0 ? 5.877471754111438e-39f : __uint_as_float((uint32_t)e << 23));
 }
 
+// x / y of non-negative numbers, in 32 bits where both fit (several times faster).
+__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
+    return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+}
+
 // The low / high two codes of a word as f16x2 (exact).
 __device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
     uint32_t h;

@@ -44,7 +44,7 @@ using namespace tcg;
 constexpr int kHalf = 128;                           // rows of a half
 constexpr int kRows = 2 * kHalf;
 constexpr int kTok = 128, kPartTok = 64;             // tokens a step, and a score buffer
-constexpr int kEntryCost = 6;                        // places of a row tile beside its tiles: 4096 tokens behind 4096 348 us, without 367, with 3 about 356
+constexpr int kEntryCost = 4;                        // places of a row tile beside its tiles (2: 309 us, 6: 308, 4: 308 for 4096 tokens behind 4096)
 constexpr int kThreads = 640, kSoftWarps = 8;
 constexpr int kGroups = kTok / 16;                   // scale groups a step (a page is at least 16 tokens)
 constexpr int kMetaRing = 4;
@@ -133,7 +133,7 @@ struct Walk {
             }
         }
         const int64_t upto = warp_scan(mine), total = __shfl_sync(0xFFFFFFFFu, upto, 31);
-        per = max((int64_t)1, (total + gridDim.x - 1) / gridDim.x);
+        per = max((int64_t)1, divide(total + gridDim.x - 1, gridDim.x));
         t = blockIdx.x * per;
         end = min(total, t + per);
         if (t >= total) return false;
@@ -147,7 +147,7 @@ struct Walk {
             e.s = sequence(a.c, ++e.b);
             per_head = head_places_warp(a, e.s);
         }
-        e.head = (int)(rel / per_head);
+        e.head = (int)divide(rel, per_head);
         rel -= e.head * per_head;
         // its row tile, 32 at a time
         row_tile_no = 0;
@@ -172,8 +172,8 @@ struct Walk {
         const int64_t tiles0 = t0 + kEntryCost, stop = min(end, tiles0 + e.rt.tiles);
         e.tile0 = (int)max((int64_t)0, t - tiles0);
         e.count = (int)max((int64_t)0, stop - max(t, tiles0));
-        e.first_cta = (int)(tiles0 / per);
-        e.last_cta = (int)((tiles0 + e.rt.tiles - 1) / per);
+        e.first_cta = (int)divide(tiles0, per);
+        e.last_cta = (int)divide(tiles0 + e.rt.tiles - 1, per);
         t = max(t + 1, stop);
         return e.count > 0;
     }
@@ -335,6 +335,11 @@ __device__ __forceinline__ void convert_tile(uint32_t src, uint32_t dst, int wt,
         sts128(row + ((k ^ (r & 7)) << 4), e4m3_lo(x.x), e4m3_hi(x.x), e4m3_lo(x.y), e4m3_hi(x.y));
         sts128(row + (((k + 1) ^ (r & 7)) << 4), e4m3_lo(x.z), e4m3_hi(x.z), e4m3_lo(x.w), e4m3_hi(x.w));
     }
+}
+
+// 16 bytes to shared memory behind the thread's back; zeros unless `real`.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
 }
 
 template <int TYPE, int D>
@@ -567,6 +572,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
             if (lane == 0) mbar_arrive(bar(HALF + h));
             return wait(HALF + h, half_syncs++);
         };
+        // a row of the half is kChunks chunks of 16 bytes (swizzled, 64 dims a sub-tile); a warp moves kPerLoad rows at a time
+        constexpr int kChunks = D / 8, kPerLoad = 32 / kChunks;
+        auto q_chunk = [&](int r, int k) { return base + T::oQ + h * T::kQ + (k >> 3) * T::kSub + r * 128 + (((k & 7) ^ (r & 7)) << 4); };
         bool ok = true;
         for (uint32_t i = 0; ok && (ok = open(i)); close(i++)) {
             const Entry &e = entry(i);
@@ -587,31 +595,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                 moving = live ? kPartTok : 0;
                 hi_col = live ? pos + 1 - tb0 : kPartTok;
                 lo_col = live && a.window ? pos - a.window + 1 - tb0 : 0;
-                // the row's largest element, then the row as f16
-                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + q_row * a.q_stride + (int64_t)q_head * D);
-                uint32_t m = 0, w[D / 2];
-#pragma unroll
-                for (int k = 0; k < D / 8; ++k) {
-                    const uint4 x = live ? src[k] : make_uint4(0u, 0u, 0u, 0u);
-                    w[4 * k] = x.x, w[4 * k + 1] = x.y, w[4 * k + 2] = x.z, w[4 * k + 3] = x.w;
+                // the warp's rows come in kPerLoad whole rows a copy, then each thread scales its own (loads of 16 bytes of 32 rows
+                // each: 4.1 against 2.2 us an entry)
+                const int64_t off = live ? q_row * a.q_stride + (int64_t)q_head * D : -1;
+#pragma unroll 4
+                for (int k = 0; k < kChunks; ++k) {
+                    const int r = k * kPerLoad + lane / kChunks, chunk = lane % kChunks;
+                    const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r);
+                    copy16(q_chunk((warp & 3) * 32 + r, chunk), static_cast<const uint16_t *>(a.q) + (o < 0 ? 0 : o + 8 * chunk), o >= 0);
                 }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                __syncwarp();
+                uint32_t m2 = 0;
 #pragma unroll
-                for (int k = 0; k < D / 2; ++k) {
-                    const float2 f = q_pair<TYPE>(w[k]);
-                    m = max(m, max(__float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu));
+                for (int k = 0; k < kChunks; ++k) {
+                    const uint4 x = lds_v4(q_chunk(row, k));
+                    m2 = __vmaxu2(__vmaxu2(m2, __vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu)), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
                 }
+                const float2 m = q_pair<TYPE>(m2);
                 float down;
-                q_scale(m, a.scale_log2, down, kf);
-                const uint32_t dst = base + T::oQ + h * T::kQ + row * 128;
-#pragma unroll
-                for (int k = 0; k < D / 8; ++k) {
-                    uint32_t o[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float2 f = q_pair<TYPE>(w[4 * k + q]);
-                        o[q] = pack_f16x2(f.x * down, f.y * down);
-                    }
-                    sts128(dst + (k >> 3) * T::kSub + (((k & 7) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
+                q_scale(max(__float_as_uint(m.x), __float_as_uint(m.y)), a.scale_log2, down, kf);
+#pragma unroll 4
+                for (int k = 0; k < kChunks; ++k) {
+                    const uint32_t at = q_chunk(row, k);
+                    const uint4 x = lds_v4(at);
+                    auto scaled = [&](uint32_t w) {
+                        const float2 f = q_pair<TYPE>(w);
+                        return pack_f16x2(f.x * down, f.y * down);
+                    };
+                    sts128(at, scaled(x.x), scaled(x.y), scaled(x.z), scaled(x.w));
                 }
             }
             fence_async_smem();
@@ -625,7 +637,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                 tc_fence_after();
                 // u_j = t_j - M with the bound so far.  The probabilities 2^u are formed at once and kept unless the sum of
                 // 16 passes 2^15 (f16 holds what is below); then, as on a row's first tokens, the largest u is found, M
-                // raised, and they are formed again.  (The search for the largest u beside each: NEWFIG.)
+                // raised, and they are formed again.  (With the search for the largest u beside each:
+                // 334 against 329 us for 4096 tokens behind 4096.)
                 const float4 *mt = meta + (n % kMetaRing) * kGroups + (j & 1) * (kGroups / 2);
                 float t[64];
 #pragma unroll
@@ -720,16 +733,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
             const bool live = h * kHalf + row < e.rt.n_rows;
             const int64_t q_row = e.s.row0 + tok_i;
             const int q_head = e.head * a.group + rr - tok_i * a.group;
-            uint16_t *out = static_cast<uint16_t *>(a.out) + q_row * a.out_stride + (int64_t)q_head * D;
+            // the output goes through the place of the half's queries (no product reads them any more), for whole rows a store
             auto put = [&](int d, const float *x, float f) {              // 16 values from dim d
-                if (!live) return;
                 uint32_t w[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    w[k] = TYPE == ENGRAM_T_BF16 ? pack_bf16x2(x[2 * k] * f, x[2 * k + 1] * f) : pack_f16x2(x[2 * k] * f, x[2 * k + 1] * f);
-                uint4 *dst = reinterpret_cast<uint4 *>(out + d);
-                dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    w[k] = TYPE == ENGRAM_T_BF16 ? pack_bf16x2(x[2 * k] * f, x[2 * k + 1] * f)
+                                                 : pack_f16x2(x[2 * k] * f, x[2 * k + 1] * f);
+                sts128(q_chunk(row, d / 8), w[0], w[1], w[2], w[3]);
+                sts128(q_chunk(row, d / 8 + 1), w[4], w[5], w[6], w[7]);
+            };
+            auto put_rows = [&]() {
+                const int64_t off = live ? q_row * a.out_stride + (int64_t)q_head * D : -1;
+                __syncwarp();
+#pragma unroll 4
+                for (int k = 0; k < kChunks; ++k) {
+                    const int r = k * kPerLoad + lane / kChunks;
+                    const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r);
+                    const uint4 v = lds_v4(q_chunk((warp & 3) * 32 + r, lane % kChunks));
+                    if (o >= 0) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + o + lane % kChunks * 8) = v;
+                }
+                __syncwarp();
             };
             auto put_lse = [&](float m, float l) {
                 if (live && a.lse) a.lse[q_row * a.H + q_head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
@@ -755,6 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
             }
             tc_fence_before();                                            // the sums are read: the next entry may overwrite them
             if (alone) {
+                put_rows();
                 put_lse(M, L);
                 continue;
             }
@@ -813,6 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                     put(d, x, il);
                     put(d + 16, x + 16, il);
                 }
+                put_rows();
                 put_lse(m, l);
             }
         }
