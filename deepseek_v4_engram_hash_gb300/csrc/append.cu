@@ -87,7 +87,8 @@ __device__ __forceinline__ Item item_of(const AppendArgs &a, int j, bool turn) {
     if (turn && !a.interleaved && 16 * j < a.rot) return {8 * j, (a.rot >> 1) + 8 * j, kHalves};
     return {16 * j, 16 * j + 8, turn && 16 * j < a.rot ? kAdjacent : kPlain};
 }
-// The (cos, sin) pairs of an item at a position: eight of them (kHalves: elements c0 .. c0 + 7; kAdjacent: 16 elements from c0).
+// The (cos, sin) pairs of an item at a position: eight of them (kHalves: elements c0 .. c0 + 7; kAdjacent: 16 elements
+// from c0).
 __device__ __forceinline__ void load_angles(const AppendArgs &a, const Item &it, int64_t pos, float (&t)[16]) {
     if (it.turn == kPlain) return;
     const float *cs = a.rope + pos * a.rot + (it.turn == kHalves ? 2 * it.c0 : it.c0);
@@ -283,7 +284,8 @@ cudaError_t launch_typed(AppendArgs &a, cudaStream_t s) {
     // a warp a unit while a sequence adds at most 4 tokens (4 x 8 items), else a block that holds a page in two items a thread
     const int items = a.c.pt * a.c.D >> 4;
     if (a.c.max_rows <= 4) return launch_units<TYPE, 32, 1>(a, s);
-    return items <= 256 ? launch_units<TYPE, 128, 2>(a, s) : items <= 512 ? launch_units<TYPE, 256, 2>(a, s) : launch_units<TYPE, 512, 2>(a, s);
+    if (items <= 256) return launch_units<TYPE, 128, 2>(a, s);
+    return items <= 512 ? launch_units<TYPE, 256, 2>(a, s) : launch_units<TYPE, 512, 2>(a, s);
 }
 
 }  // namespace

@@ -35,9 +35,11 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kUnit = 32, kSub = 16;                 // tokens a warp step, in two parts of one page each
 constexpr int kTile = kUnit * kWarps;                // tokens a CTA step
 constexpr int kMaxRows = 16;
-constexpr int kCtasPerSm = 3;                        // 2 for 16 rows (248 registers instead of spills at 168: 32 sequences of 4
-                                                     // rows a head of 4 query heads 57 against 68 us)
-constexpr int kEntryCost = 2;                        // places of an entry in the list beside its tiles: 64 sequences 97.3 us, without 104.7
+// CTAs an SM; one less for 9 to 16 rows, which need 248 registers (with 168 they spill: 32 sequences of 4 tokens, 4 query
+// heads a key/value head, behind 4000: 57 against 68 us).
+constexpr int kCtasPerSm = 3;
+// Places of an entry in the list beside its tiles: 64 single tokens behind 500 to 8191 take 97.3 us, without 104.7.
+constexpr int kEntryCost = 2;
 constexpr uint32_t kNever = 0x7FFFFFFF;
 
 struct FewParams {
@@ -96,7 +98,8 @@ __device__ __forceinline__ int64_t places_of(const Plan &p) { return p.tiles ? p
 // a thread adds up one float4 over every groups-th part, sixteen loads at a time,
 // and the groups are added in order.
 template <int TYPE, int D>
-__device__ __forceinline__ void join_parts(const AttnArgs &a, int row0, int head, int n_rows, int64_t first, int n, uint8_t *smem) {
+__device__ __forceinline__ void join_parts(const AttnArgs &a, int row0, int head, int n_rows, int64_t first, int n,
+                                           uint8_t *smem) {
     constexpr int kPart = Few<D>::kPart, kAhead = 16;
     float *fac = reinterpret_cast<float *>(smem) + 4 * kThreads;         // [n_rows][n]
     float4 *sums = reinterpret_cast<float4 *>(smem);                     // [groups][items]

@@ -20,10 +20,16 @@
 //   warps 16, 17       issue the second, O_h += P_h V with P_h from tensor memory (M 128, N D, K 16);
 //   warp 13            pages, scales and TMA copies of the codes;
 //   warp 15            the schedule: entries of the list for all others.
-// A half's scores have two buffers of 64 tokens: while one is in its softmax, the tensor
-// cores fill the other and take the probabilities before (a chain of one score buffer a half left
-// them idle for the latencies between product, softmax and product: 432 against 379 us for 4096 tokens behind 4096, 32 query and 8 key/value heads of 128).
-// Tensor memory: S 2 x 2 x 64 columns, O 2 x D; P lies over its S.
+// A half's scores have two buffers of 64 tokens: while one is in its softmax, the
+// tensor cores fill the other and take the probabilities before (with one buffer a
+// half they were idle for the latencies between product, softmax and product: 432
+// against 379 us).  Tensor memory: S 2 x 2 x 64 columns, O 2 x D; P lies over its S.
+//
+// Bound by the softmax: two in-order warps a scheduler, about 1000 clocks for 64 tokens
+// of both beside the converters, against 512 of tensor work a half.  4096 tokens
+// behind 4096, 32 query and 8 key/value heads of 128 (412 GFLOP in the visible pairs):
+// 308 us, 71 % of the measured bf16 rate; an entry costs about 5 us in which the
+// tensor cores wait (output, queries, first scores).  Times below are this call's.
 //
 // The call's (sequence, head, row tile, 128-token tile) list, with kEntryCost places more
 // for each row tile (what beginning and ending one takes), is cut evenly over one CTA an
@@ -44,7 +50,8 @@ using namespace tcg;
 constexpr int kHalf = 128;                           // rows of a half
 constexpr int kRows = 2 * kHalf;
 constexpr int kTok = 128, kPartTok = 64;             // tokens a step, and a score buffer
-constexpr int kEntryCost = 4;                        // places of a row tile beside its tiles (2: 309 us, 6: 308, 4: 308 for 4096 tokens behind 4096)
+// Places of a row tile beside its tiles: 8 x 512 tokens behind 512 take 78 us, with 3 or 6 81, with 5 80.
+constexpr int kEntryCost = 4;
 constexpr int kThreads = 640, kSoftWarps = 8;
 constexpr int kGroups = kTok / 16;                   // scale groups a step (a page is at least 16 tokens)
 constexpr int kMetaRing = 4;
@@ -167,7 +174,8 @@ struct Walk {
         t0 = t - rel;
         return true;
     }
-    // The entry at t, whose row tile has the places from t0: kEntryCost without a tile, then its tiles.  False if it gets no tile here.
+    // The entry at t, whose row tile has the places from t0: kEntryCost without a tile, then its tiles.  False if it gets
+    // no tile here.
     __device__ __forceinline__ bool take() {
         const int64_t tiles0 = t0 + kEntryCost, stop = min(end, tiles0 + e.rt.tiles);
         e.tile0 = (int)max((int64_t)0, t - tiles0);
@@ -304,7 +312,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // Uses of these registers stay behind the wait before it.
 __device__ __forceinline__ void pin32(float *r) {
-    asm volatile("" : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31]));
+    asm volatile(""
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                   "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]),
+                   "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]),
+                   "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31]));
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&u)[16]) {
@@ -350,7 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
     const uint32_t base = smem_u32(smem);
     float4 *meta = reinterpret_cast<float4 *>(smem + T::oMeta);           // [kMetaRing][kGroups]: 2^ek, ev, 2^-ev, counts
     enum { Q_FULL = 0, ST_FULL = 2, ST_EMPTY = 4, K_FULL = 6, K_EMPTY = 8, V_FULL = 10, V_EMPTY = 12, HALF = 14, DRAIN = 16,
-           S_FULL = 20, P_FULL = 24, PV_DONE = 28, E_FULL = 32, E_EMPTY = 36 };      // [2 halves][2 buffers] from S_FULL to PV_DONE
+           S_FULL = 20, P_FULL = 24, PV_DONE = 28,                        // [2 halves][2 buffers]
+           E_FULL = 32, E_EMPTY = 36 };
     auto bar = [&](int i) { return base + T::oBar + 8u * i; };
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + T::oFlag);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + T::oFlag + 4);
@@ -396,9 +409,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
     const uint32_t tmem = *tmem_slot;
     int *err = a.c.err;
     // A whole warp waits, and agrees on the outcome.
-    auto wait = [&](int i, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait_bar(bar(i), parity & 1, abort_flag, err)) != 0; };
+    auto wait = [&](int i, uint32_t parity) {
+        return __all_sync(0xFFFFFFFFu, wait_bar(bar(i), parity & 1, abort_flag, err)) != 0;
+    };
     // Entry number i of the CTA, and its release.
-    auto entry = [&](uint32_t i) -> const Entry & { return *reinterpret_cast<const Entry *>(smem + T::oEntry + (i % kEntries) * 64); };
+    auto entry = [&](uint32_t i) -> const Entry & {
+        return *reinterpret_cast<const Entry *>(smem + T::oEntry + (i % kEntries) * 64);
+    };
     auto open = [&](uint32_t i) { return wait(E_FULL + i % kEntries, i / kEntries) && entry(i).count > 0; };
     auto close = [&](uint32_t i) {
         __syncwarp();
@@ -461,14 +478,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                     __syncwarp();
                     if (lane == 0) mbar_expect_tx(bar(ST_FULL + 0), T::kFp8);
                     __syncwarp();
-                    if (leader) tma_load_4d(base + T::oS + at * D, &p.mk, 0, (tok0 + at) & (a.c.pt - 1), head, page, bar(ST_FULL + 0));
+                    const int in_page = (tok0 + at) & (a.c.pt - 1);
+                    if (leader) tma_load_4d(base + T::oS + at * D, &p.mk, 0, in_page, head, page, bar(ST_FULL + 0));
                     if (!(ok = wait(ST_EMPTY + 1, it + 1))) {
                         ++it;
                         break;
                     }
                     if (lane == 0) mbar_expect_tx(bar(ST_FULL + 1), T::kFp8);
                     __syncwarp();
-                    if (leader) tma_load_4d(base + T::oS + T::kFp8 + at * D, &p.mv, 0, (tok0 + at) & (a.c.pt - 1), head, page, bar(ST_FULL + 1));
+                    if (leader) tma_load_4d(base + T::oS + T::kFp8 + at * D, &p.mv, 0, in_page, head, page, bar(ST_FULL + 1));
                     id = id1;
                     sc = sc1;
                     id1 = id2;
@@ -501,7 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                 for (int s = 0; s < 2 * count; ++s, ++ns) {
                     // scores go over the probabilities two parts before: their product has to be done
                     ok = ((s & 1) || wait(full + (n & 1), n >> 1)) &&
-                         (second ? wait(P_FULL + 2 * h + (s & 1), ns >> 1) : s < 2 || wait(PV_DONE + 2 * h + (s & 1), (ns >> 1) - 1));
+                         (second ? wait(P_FULL + 2 * h + (s & 1), ns >> 1)
+                                 : s < 2 || wait(PV_DONE + 2 * h + (s & 1), (ns >> 1) - 1));
                     if (!ok) break;
                     const uint32_t at = base + (second ? T::oV : T::oK) + (n & 1) * T::kF16 + (s & 1) * (kPartTok * 128);
                     const uint32_t tS = tmem + T::cS + h * 128 + (s & 1) * kPartTok;
@@ -511,7 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                             const uint32_t v_lo = desc_lo(at, T::kSub);
 #pragma unroll
                             for (int kk = 0; kk < kPartTok / 16; ++kk)
-                                mma_ts<idesc_f16(kHalf, D, true)>(tmem + T::cO + h * D, tS + kk * 8, v_lo + kk * (2048 >> 4), (s | kk) != 0);
+                                mma_ts<idesc_f16(kHalf, D, true)>(tmem + T::cO + h * D, tS + kk * 8, v_lo + kk * (2048 >> 4),
+                                                                  (s | kk) != 0);
                             commit(bar(PV_DONE + 2 * h + (s & 1)));
                         } else {
                             const uint32_t q_lo = desc_lo(base + T::oQ + h * T::kQ, 16), k_lo = desc_lo(at, 16);
@@ -574,7 +594,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
         };
         // a row of the half is kChunks chunks of 16 bytes (swizzled, 64 dims a sub-tile); a warp moves kPerLoad rows at a time
         constexpr int kChunks = D / 8, kPerLoad = 32 / kChunks;
-        auto q_chunk = [&](int r, int k) { return base + T::oQ + h * T::kQ + (k >> 3) * T::kSub + r * 128 + (((k & 7) ^ (r & 7)) << 4); };
+        auto q_chunk = [&](int r, int k) {
+            return base + T::oQ + h * T::kQ + (k >> 3) * T::kSub + r * 128 + (((k & 7) ^ (r & 7)) << 4);
+        };
         bool ok = true;
         for (uint32_t i = 0; ok && (ok = open(i)); close(i++)) {
             const Entry &e = entry(i);
@@ -602,7 +624,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                 for (int k = 0; k < kChunks; ++k) {
                     const int r = k * kPerLoad + lane / kChunks, chunk = lane % kChunks;
                     const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r);
-                    copy16(q_chunk((warp & 3) * 32 + r, chunk), static_cast<const uint16_t *>(a.q) + (o < 0 ? 0 : o + 8 * chunk), o >= 0);
+                    copy16(q_chunk((warp & 3) * 32 + r, chunk),
+                           static_cast<const uint16_t *>(a.q) + (o < 0 ? 0 : o + 8 * chunk), o >= 0);
                 }
                 asm volatile("cp.async.wait_all;" ::: "memory");
                 __syncwarp();
@@ -610,7 +633,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
 #pragma unroll
                 for (int k = 0; k < kChunks; ++k) {
                     const uint4 x = lds_v4(q_chunk(row, k));
-                    m2 = __vmaxu2(__vmaxu2(m2, __vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu)), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+                    m2 = __vmaxu2(__vmaxu2(m2, __vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu)),
+                                  __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
                 }
                 const float2 m = q_pair<TYPE>(m2);
                 float down;
@@ -637,8 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                 tc_fence_after();
                 // u_j = t_j - M with the bound so far.  The probabilities 2^u are formed at once and kept unless the sum of
                 // 16 passes 2^15 (f16 holds what is below); then, as on a row's first tokens, the largest u is found, M
-                // raised, and they are formed again.  (With the search for the largest u beside each:
-                // 334 against 329 us for 4096 tokens behind 4096.)
+                // raised, and they are formed again.  (A search for the largest u beside each: 334 against 329 us.)
                 const float4 *mt = meta + (n % kMetaRing) * kGroups + (j & 1) * (kGroups / 2);
                 float t[64];
 #pragma unroll
@@ -673,7 +696,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                         for (int k = 0; k < 8; ++k)
 #pragma unroll
                             for (int g = 0; g < 2; ++g) {
-                                const float x = exp2_approx(t[32 * b + 16 * g + 2 * k]), y = exp2_approx(t[32 * b + 16 * g + 2 * k + 1]);
+                                const float *at = t + 32 * b + 16 * g + 2 * k;
+                                const float x = exp2_approx(at[0]), y = exp2_approx(at[1]);
                                 sum[g][k & 1] = add2(sum[g][k & 1], pack2(x, y));
                                 u[b][8 * g + k] = pack_f16x2(x, y);
                             }
@@ -774,10 +798,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                 } else {
                     float4 *part = reinterpret_cast<float4 *>(a.ws.part + slot * T::kPart + of) + d / 4 * kRows;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) part[k * kRows] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                    for (int k = 0; k < 4; ++k)
+                        part[k * kRows] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
                 }
             }
-            tc_fence_before();                                            // the sums are read: the next entry may overwrite them
+            tc_fence_before();                                            // read: the next entry may overwrite them
             if (alone) {
                 put_rows();
                 put_lse(M, L);
@@ -802,7 +827,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
                 float m = -INFINITY, l = 0.f, f01[2] = {1.f, 1.f};
                 auto last_of = [&](int k) { return min(k, parts - 1); };
                 for (int k = 0; k < parts; k += 2) m = fmaxf(m, fmaxf(__ldcg(st + at(k)), __ldcg(st + at(last_of(k + 1)))));
-                auto factor = [&](float mk, float lk) { return mk == -INFINITY ? (lk == 0.f ? 0.f : 1.f) : exp2_approx(mk - m); };
+                auto factor = [&](float mk, float lk) {
+                    return mk == -INFINITY ? (lk == 0.f ? 0.f : 1.f) : exp2_approx(mk - m);
+                };
                 for (int k = 0; k < parts; k += 2) {
                     const float m0 = __ldcg(st + at(k)), l0 = __ldcg(st + at(k) + kRows), m1 = __ldcg(st + at(last_of(k + 1))),
                                 l1 = __ldcg(st + at(last_of(k + 1)) + kRows);

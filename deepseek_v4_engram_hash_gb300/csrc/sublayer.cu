@@ -170,7 +170,8 @@ int engram_attn_create(engram_attn **out) {
         delete h;
         return ENGRAM_E_UNSUPPORTED;
     }
-    if (!h->sms || cudaGetDevice(&h->device) != cudaSuccess || cudaMalloc(&h->ws.part, attn_part_floats(h->sms) * sizeof(float)) != cudaSuccess ||
+    if (!h->sms || cudaGetDevice(&h->device) != cudaSuccess ||
+        cudaMalloc(&h->ws.part, attn_part_floats(h->sms) * sizeof(float)) != cudaSuccess ||
         cudaMalloc(&h->ws.arrived, attn_counters(h->sms) * sizeof(int)) != cudaSuccess ||
         cudaMemset(h->ws.arrived, 0, attn_counters(h->sms) * sizeof(int)) != cudaSuccess || !error_word()) {
         engram_attn_destroy(h);
