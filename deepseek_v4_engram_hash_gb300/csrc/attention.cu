@@ -8,8 +8,9 @@
 // the exponent: t_j = s_j + ev, p_j = 2^(t_j - M) with M a running bound of the
 // row's t, out = sum p_j vc_j / L, L = sum p_j 2^-ev, so the f16 probabilities
 // always hold the row's largest contributions with full precision, whatever
-// the scales.  M moves (and the sums are rescaled) only when a t exceeds it by more
-// than 8: until then p <= 2^8, which f16 and the f32 sums hold.
+// the scales.  M is set 7 under the row's largest t so far, and moves (and the sums are
+// rescaled) only when a t exceeds it by more than 15: until then p <= 2^15, which f16
+// and the f32 sums hold.
 //
 // Bound by the cache's bytes, so what counts is instructions a byte.  The tokens are
 // the M side of both products (m16n8k16 with f16 operands: S^T = K Q^T and
@@ -41,6 +42,9 @@ constexpr int kCtasPerSm = 3;
 // Places of an entry in the list beside its tiles: 64 single tokens behind 500 to 8191 take 97.3 us, without 104.7.
 constexpr int kEntryCost = 2;
 constexpr uint32_t kNever = 0x7FFFFFFF;
+// A row's bound M is set kRoom (log2) under its largest t so far, and t may pass M by kLazy: the probabilities go up to
+// f16's 2^15, and one 2^-32 of the row's largest is still half of f16's least number.
+constexpr float kRoom = 7.f, kLazy = 15.f;
 
 struct FewParams {
     AttnArgs a;
@@ -387,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm + 1 - NT) attn_few_kernel
                         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
                         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-                        m = fmaxf(m, M[nt][e]);
+                        m = fmaxf(m - kRoom, M[nt][e]);
                         const float f = M[nt][e] == m ? 1.f : exp2_approx(M[nt][e] - m);
                         M[nt][e] = m;
                         L[nt][e] *= f;

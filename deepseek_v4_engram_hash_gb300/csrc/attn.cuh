@@ -9,8 +9,6 @@
 namespace engram {
 namespace attn {
 
-constexpr float kLazy = 8.f;            // log2: how far a row's scores may pass its bound M before the sums are rescaled
-constexpr float kLazySum = 32768.f;     // the tile kernel: a sum of 16 probabilities that stays below (f16 holds each of them)
 // Value blocks with smaller scales (2^-66) count as zeros: the least exponent that
 // joins the scores, so that a block of zeros (scale 2^-126) beside ordinary ones
 // keeps its weight in the row's sum.

@@ -458,8 +458,10 @@ void engram_attn_destroy(engram_attn *a);
  *   bf16 or f16; d_out the same with out_stride; d_lse [rows, n_heads] f32 or NULL.
  *   Rows that see nothing: out = 0, lse = -inf.
  * Scores, statistics and sums are f32; q is brought to f16 by a power of two
- * per row and head (f16 products of codes are exact); the probabilities are
- * rounded to f16 for the product with v.  A value block whose scale is under
+ * per row and head (f16 products of codes are exact; elements under 2^-13 of the
+ * row's largest may lose bits, those under 2^-25 of it are lost); the probabilities are
+ * rounded to f16 for the product with v (so a token whose weight is under 2^-29 of the
+ * row's largest may count there as nothing).  A value block whose scale is under
  * 2^-66 counts as zeros.  Codes 127 and 255 (NaN) are not allowed at positions
  * below kv_len; the cache may hold anything elsewhere.
  * n_heads a multiple of n_kv_heads; scale finite; window >= 0; strides multiples of 8,

@@ -1,0 +1,54 @@
+"""engram_attention at the ends of its ranges, against its definition in 64 bits.
+
+test_gpu_attention.py has the bounds of ordinary inputs; here the inputs are such
+that a tighter one can be derived, which each test does.
+"""
+import math
+
+import pytest
+import torch
+
+import sublayer_glue as U
+import sublayer_ref as R
+import test_gpu_attention as A
+
+pytestmark = pytest.mark.gpu
+LN2 = float(torch.tensor(math.log(2.0), dtype=torch.float32))    # times log2(e): 1 to within 2^-24
+
+
+@pytest.fixture(scope="module")
+def E():
+    import __graft_entry__
+    __graft_entry__.build()
+    from deepseek_v4_engram_hash_gb300 import _lib
+    assert torch.cuda.is_available()
+    return _lib
+
+
+@pytest.fixture(scope="module")
+def attn(E):
+    return E.Attention()
+
+
+@pytest.mark.parametrize("new", [1, 20])
+def test_weights_far_under_the_largest_count(E, attn, new):
+    """One token of weight 1 and value 0, all others of weight 2^-28 and value 1: out = m 2^-28 / (1 + m 2^-28) for m others.
+
+    The scores in log2 units are whole to within 2^-24 of 28; with a bound at least 4 under the row's largest the weights
+    are multiples of f16's least number, 2^-24, so out keeps 2^-10 of itself before it is rounded to bf16.  With the
+    bound at the largest they would be 0 in the product and not in the sum."""
+    KH, D, pt, n = 304, 64, 128, 2048                     # as many heads as it takes for whole sequences on one SM
+    table = U.pages_for([n], pt, 16)
+    cache = U.Cache(E, 16, KH, pt, D, fill=0, scale=127)
+    cache.k[:, :, :, 0] = 0xDE                            # -28
+    cache.v.fill_(0x38)                                   # 1
+    first = int(table[0, 0])
+    cache.k[first, :, 0, 0], cache.v[first, :, 0] = 0, 0
+    q = torch.zeros(new, KH, D, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 1
+    out, lse = A._run(E, attn, cache, U.batch(E, table, [new], [n]), q.view(new, -1), KH, LN2, 0, 0)
+    others = torch.arange(n - new, n, device="cuda", dtype=torch.float64)[:, None]
+    want = others * 2.0 ** -28 / (1 + others * 2.0 ** -28)
+    got = out.double()
+    assert ((got - want).abs() <= (2.0 ** -8 + 2.0 ** -10) * want).all(), (got.min(), got.max())
+    assert ((lse.double() - torch.log1p(others * 2.0 ** -28)).abs() <= 2.0 ** -20).all()
