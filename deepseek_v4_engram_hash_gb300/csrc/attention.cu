@@ -80,15 +80,16 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-// A sequence's entries, one a head, each of `tiles` 128-token tiles from token lo.
+// A sequence's entries, one a head, each of `tiles` 128-token tiles from token lo; its rows see tokens from `first` on.
 struct Plan {
     Seq s;
-    int lo, tiles;
+    int first, lo, tiles;
 };
 __device__ __forceinline__ Plan plan_of(const AttnArgs &a, int b) {
     Plan p;
     p.s = sequence(a.c, b);
-    p.lo = a.window ? max(0, p.s.kv - p.s.n - a.window + 1) / kUnit * kUnit : 0;
+    p.first = a.window ? max(0, p.s.kv - p.s.n - a.window + 1) : 0;
+    p.lo = p.first / kUnit * kUnit;
     p.tiles = p.s.n == 0 ? 0 : max(1, (p.s.kv - p.lo + kTile - 1) / kTile);
     return p;
 }
@@ -240,10 +241,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm + 1 - NT) attn_few_kernel
         const int units = tok0 < tok1 ? (tok1 - tok0 + kTile - 1) / kTile : 0;
         const int n_rows = min(8 * NT, pl.s.n * a.group);
 
-        // pages and scales of 16 units at a time, one part a lane: id, key byte | value byte << 8
+        // pages and scales of 16 units at a time, one part a lane: id, key byte | value byte << 8.  A page that ends before
+        // the first token that a row sees is not looked up: a sliding window's pages may have been given back.
         auto load_id = [&](int k) {
             const int tok = tok0 + (16 * k + (lane >> 1)) * kTile + (lane & 1) * kSub;
-            return tok < tok1 ? page_of(a.c, b, tok >> a.c.pt_log2) : -1;
+            return tok < tok1 && (tok | (a.c.pt - 1)) >= pl.first ? page_of(a.c, b, tok >> a.c.pt_log2) : -1;
         };
         auto load_scales = [&](int id) {
             if (id < 0) return 0u;
@@ -319,7 +321,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm + 1 - NT) attn_few_kernel
         float o[NT][KS][4] = {};
         float M[NT][2], L[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) M[nt][0] = M[nt][1] = -INFINITY, L[nt][0] = L[nt][1] = 0.f;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)                                 // places without a row never ask for a rescaling
+                M[nt][e] = 8 * nt + 2 * q4 + e < n_rows ? -INFINITY : INFINITY, L[nt][e] = 0.f;
 #pragma unroll 1
         for (int u = 0; u < units; ++u) {
             const int tb = tok0 + u * kTile;
@@ -415,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm + 1 - NT) attn_few_kernel
                 }
             }
             // out: mma rows g and g + 8 of tile i are the dims D / 8 g + 2 i and + 1, k slots the tokens 2 q4, 2 q4 + 1 (+ 8)
-            const bool cut = tb + kUnit > pl.s.kv || (int)min(sc[0], sc[1]) >> 8 < kLeastValueByte;
+            const bool cut = tb + kUnit > pl.s.kv || tb < pl.first || (int)min(sc[0], sc[1]) >> 8 < kLeastValueByte;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 constexpr int VW = D / 32;                              // 32-bit words of a lane's dims
@@ -424,10 +429,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm + 1 - NT) attn_few_kernel
                 for (int r = 0; r < 4; ++r) load_v_row<D>(vs, kSub * h + 2 * q4 + (r & 1) + 8 * (r >> 1), g, v[r]);
                 if (cut) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (tb + kSub * h + 2 * q4 + (r & 1) + 8 * (r >> 1) >= pl.s.kv || (int)(sc[h] >> 8) < kLeastValueByte)
+                    for (int r = 0; r < 4; ++r) {
+                        const int tok = tb + kSub * h + 2 * q4 + (r & 1) + 8 * (r >> 1);
+                        if (tok >= pl.s.kv || tok < pl.first || (int)(sc[h] >> 8) < kLeastValueByte)
 #pragma unroll
-                            for (int i = 0; i < VW; ++i) v[r][i] = 0u;  // nothing is written there, or it does not count
+                            for (int i = 0; i < VW; ++i) v[r][i] = 0u;  // anything may be there, or it does not count
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < VW; ++i) {

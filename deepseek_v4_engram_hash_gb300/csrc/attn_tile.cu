@@ -68,16 +68,17 @@ struct TileParams {
 // x / group.
 __device__ __forceinline__ int by_group(const AttnArgs &a, int x) { return a.group_log2 >= 0 ? x >> a.group_log2 : x / a.group; }
 
-// Row tile rt of a sequence: its tokens from `lo`, in `tiles` tiles of 128.
+// Row tile rt of a sequence: its tokens from `lo`, in `tiles` tiles of 128; its rows see tokens from `first` on.
 struct RowTile {
-    int r0, n_rows, lo, tiles;
+    int r0, n_rows, first, lo, tiles;
 };
 __device__ __forceinline__ RowTile row_tile(const AttnArgs &a, const Seq &s, int rt) {
     RowTile t;
     t.r0 = rt * kRows;
     t.n_rows = min(kRows, s.n * a.group - t.r0);
     const int first = s.kv - s.n + by_group(a, t.r0), last = s.kv - s.n + by_group(a, t.r0 + t.n_rows - 1);
-    t.lo = a.window ? max(0, first - a.window + 1) / kTok * kTok : 0;
+    t.first = a.window ? max(0, first - a.window + 1) : 0;
+    t.lo = t.first / kTok * kTok;
     t.tiles = max(1, (min(s.kv, last + 1) - t.lo + kTok - 1) / kTok);
     return t;
 }
@@ -336,16 +337,20 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// One staged tile of codes to f16: [token][dim], 64-dim sub-tiles of 128-byte swizzled rows.  128 threads.
+// One staged tile of codes to f16: [token][dim], 64-dim sub-tiles of 128-byte swizzled rows.  128 threads.  Values of
+// tokens outside from .. valid - 1 become zeros.
 template <int D>
-__device__ __forceinline__ void convert_tile(uint32_t src, uint32_t dst, int wt, bool values, int valid, const float4 *meta) {
+__device__ __forceinline__ void convert_tile(uint32_t src, uint32_t dst, int wt, bool values, int from, int valid,
+                                             const float4 *meta) {
     const int lane = wt & 31, w = wt >> 5;
+    const int rel = w * 32 + (lane & 7) - from;       // from <= r < valid in one comparison
+    const uint32_t span = (uint32_t)max(0, valid - from);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {                // a warp: 8 tokens x 4 chunks of 16 codes a pass
         const int it = i * 4 + (lane >> 3);           // chunk index over (token group of 8, chunk)
         const int r = w * 32 + (it / (D / 16)) * 8 + (lane & 7), c = it % (D / 16);
         uint4 x = lds_v4(src + chunk_at<D>(r, c));
-        if (values && (r >= valid || meta[r >> 4].w == 0.f)) x = make_uint4(0u, 0u, 0u, 0u);
+        if (values && ((uint32_t)(rel + it / (D / 16) * 8) >= span || meta[r >> 4].w == 0.f)) x = make_uint4(0u, 0u, 0u, 0u);
         const uint32_t row = dst + (c >> 2) * Tile<D>::kSub + r * 128;
         const int k = 2 * c & 7;
         sts128(row + ((k ^ (r & 7)) << 4), e4m3_lo(x.x), e4m3_hi(x.x), e4m3_lo(x.y), e4m3_hi(x.y));
@@ -456,11 +461,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
             for (uint32_t i = 0; ok && (ok = open(i)); close(i++)) {
                 const Entry &e = entry(i);
                 const int tok0 = e.rt.lo + e.tile0 * kTok, kv = e.s.kv, b = e.b, head = e.head, count = e.count;
+                const int first = e.rt.first;
                 const int at = 16 * (lane & 7);
                 const bool leader = lane < 8 && (at & (a.c.pt - 1)) == 0;
+                // a page that ends before the first token that a row sees is not looked up: a sliding window's pages may
+                // have been given back
                 auto page_at = [&](int j) {
                     const int tok = tok0 + j * kTok + at;
-                    return lane < 8 && j < count && tok < kv ? page_of(a.c, b, tok >> a.c.pt_log2) : -1;
+                    return lane < 8 && j < count && tok < kv && (tok | (a.c.pt - 1)) >= first ? page_of(a.c, b, tok >> a.c.pt_log2) : -1;
                 };
                 auto scales_of = [&](int id) {
                     if (id < 0) return 0u;
@@ -567,14 +575,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
         bool ok = true;
         uint32_t n = 0;
         for (uint32_t i = 0; ok && (ok = open(i)); close(i++)) {
-            const int left = entry(i).s.kv - (entry(i).rt.lo + entry(i).tile0 * kTok), count = entry(i).count;
+            const int tok0 = entry(i).rt.lo + entry(i).tile0 * kTok, count = entry(i).count;
+            const int left = entry(i).s.kv - tok0, unseen = max(0, entry(i).rt.first - tok0);   // under 128: the first tile's
             for (int j = 0; j < count && ok; ++j, ++n) {
                 const int valid = left - j * kTok;                        // tokens of the tile that exist
                 for (int x = 0; x < 2; ++x) {
                     ok = wait(ST_FULL + x, n) && wait((x ? V_EMPTY : K_EMPTY) + (n & 1), (n >> 1) + 1);
                     if (!ok) break;
-                    convert_tile<D>(base + T::oS + x * T::kFp8, base + (x ? T::oV : T::oK) + (n & 1) * T::kF16, wt, x != 0, valid,
-                                    meta + (n % kMetaRing) * kGroups);
+                    convert_tile<D>(base + T::oS + x * T::kFp8, base + (x ? T::oV : T::oK) + (n & 1) * T::kF16, wt, x != 0,
+                                    j == 0 ? unseen : 0, valid, meta + (n % kMetaRing) * kGroups);
                     fence_async_smem();
                     __syncwarp();
                     if (lane == 0) {
@@ -658,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const __grid_con
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(Q_FULL + h));
 
-            float M = -INFINITY, L = 0.f;
+            float M = h * kHalf + row < e.rt.n_rows ? -INFINITY : INFINITY, L = 0.f;   // no row: never asks for a rescaling
             for (int j = 0; j < 2 * count; ++j, ++ns, hi_col -= moving, lo_col -= moving) {
                 const uint32_t tS = lanes + T::cS + h * 128 + (j & 1) * kPartTok;
                 if (!(ok = wait(S_FULL + 2 * h + (j & 1), ns >> 1))) break;

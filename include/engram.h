@@ -463,7 +463,9 @@ void engram_attn_destroy(engram_attn *a);
  * rounded to f16 for the product with v (so a token whose weight is under 2^-29 of the
  * row's largest may count there as nothing).  A value block whose scale is under
  * 2^-66 counts as zeros.  Codes 127 and 255 (NaN) are not allowed at positions
- * below kv_len; the cache may hold anything elsewhere.
+ * from the first that a row of the sequence sees to kv_len - 1; the cache may hold
+ * anything elsewhere, and page-table entries of pages that end before that first
+ * position are not read (a sliding window's pages may be given back).
  * n_heads a multiple of n_kv_heads; scale finite; window >= 0; strides multiples of 8,
  * tensors 16-byte aligned. */
 int engram_attention(engram_attn *a, const engram_kv_cache *cache, const engram_kv_batch *batch, int32_t type,

@@ -52,3 +52,32 @@ def test_weights_far_under_the_largest_count(E, attn, new):
     got = out.double()
     assert ((got - want).abs() <= (2.0 ** -8 + 2.0 ** -10) * want).all(), (got.min(), got.max())
     assert ((lse.double() - torch.log1p(others * 2.0 ** -28)).abs() <= 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("pt", [16, 32, 64, 128])
+@pytest.mark.parametrize("H,new,D,ty", [(4, 1, 128, 0), (6, 5, 64, 1), (16, 40, 128, 0), (2, 300, 64, 0)])
+def test_nothing_behind_the_window_is_read(E, attn, H, new, D, ty, pt):
+    """Pages that no row sees may be given back: their entries hold anything, their bytes and those before the first
+    visible token of a page are NaN.  No error, and the same bits."""
+    KH, window = 2, 100
+    kv = [1337, 333, 1025]
+    news = [new, min(new, 333), max(1, new // 2)]
+    table = U.pages_for(kv, pt, sum(-(-t // pt) for t in kv) + 1, seed=pt)
+    cache = U.Cache(E, sum(-(-t // pt) for t in kv) + 1, KH, pt, D)
+    free = (set(range(cache.n_pages)) - set(table.flatten().tolist())).pop()
+    U.fill_random(cache, table, kv, 3)
+    q = A._queries(sum(news), H, D, ty, 5)
+    want = A._run(E, attn, cache, U.batch(E, table, news, kv), q, H, 0.1, window, ty)
+    A._check(cache, table, news, kv, q, H, 0.1, window, ty, *want)
+    for b, (n, t) in enumerate(zip(news, kv)):
+        first = max(0, t - n - window + 1)
+        for i in range(first // pt):
+            page = int(table[b, i])
+            for codes, scales in ((cache.k, cache.ks), (cache.v, cache.vs)):
+                codes[page], scales[page] = 127, 255
+            table[b, i] = (-7, cache.n_pages, 1 << 30, free, page)[i % 5]
+        if first % pt:
+            page = int(table[b, first // pt])
+            cache.k[page, :, : first % pt], cache.v[page, :, : first % pt] = 127, 255
+    got = A._run(E, attn, cache, U.batch(E, table, news, kv), q, H, 0.1, window, ty)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
