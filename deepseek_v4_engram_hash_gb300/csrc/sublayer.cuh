@@ -83,9 +83,10 @@ __device__ __forceinline__ uint32_t block_scale_byte(uint32_t amax) {
     const int b = (int)(amax >> 23) - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0);
     return b < 1 ? 1u : (uint32_t)b;
 }
-// 1 / 2^(byte - 127), exact for the bytes 1..253 that block_scale_byte gives; 0 for 255 (codes of a NaN block).
+// 1 / 2^(byte - 127) for the bytes 1..254 (block_scale_byte gives up to 247, a caller's cache may hold more), exact: 2^-127,
+// for 254, is subnormal.  0 for 255 (codes of a NaN block).
 __device__ __forceinline__ float inv_scale(uint32_t byte) {
-    return byte == 255u ? 0.f : __uint_as_float((254u - byte) << 23);
+    return __uint_as_float(byte < 254u ? (254u - byte) << 23 : byte == 254u ? 0x00400000u : 0u);
 }
 // Four values times `inv` as e4m3 codes, nearest even.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {

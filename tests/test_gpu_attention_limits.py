@@ -81,3 +81,19 @@ def test_nothing_behind_the_window_is_read(E, attn, H, new, D, ty, pt):
             cache.k[page, :, : first % pt], cache.v[page, :, : first % pt] = 127, 255
     got = A._run(E, attn, cache, U.batch(E, table, news, kv), q, H, 0.1, window, ty)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("H,new", [(4, 1), (16, 40)])
+@pytest.mark.parametrize("vbyte", [61, 127, 247, 253, 254])
+def test_every_value_scale_up_to_the_largest(E, attn, H, new, vbyte):
+    """Value blocks of one scale, up to 2^127: outputs are those of scale 1 times it, and the log-sum-exp is the same."""
+    KH, D, pt, n = 2, 64, 16, 200
+    table = U.pages_for([n], pt, 14)
+    cache = U.Cache(E, 14, KH, pt, D)
+    U.fill_random(cache, table, [n], 3, spread=0)
+    cache.v.copy_(torch.where(cache.v & 127 == 127, cache.v, cache.v & 0xB7))    # under 2: no output past bf16's range
+    q = A._queries(new, H, D, 0, 5)
+    plan = U.batch(E, table, [new], [n])
+    cache.vs.fill_(vbyte)
+    out, lse = A._run(E, attn, cache, plan, q, H, 0.1, 0, 0)
+    A._check(cache, table, [new], [n], q, H, 0.1, 0, 0, out, lse)

@@ -274,3 +274,21 @@ def test_offsets_past_32_bits(E):
         assert torch.equal(a[49], b[1]) and torch.equal(a[0], b[0])
     assert not cache.raw[0][(KH * pt * D):stride].any()
     del want, tol
+
+
+@pytest.mark.parametrize("old", [248, 253, 254])
+def test_append_under_the_largest_scales(E, old):
+    """A page whose scale is the caller's own, past what this library writes (247): new codes are the values at that scale."""
+    KH, D, pt = 2, 64, 16
+    table = U.pages_for([5], pt, 2)
+    cache = U.Cache(E, 2, KH, pt, D)
+    p = int(table[0, 0])
+    for codes, scales in ((cache.k, cache.ks), (cache.v, cache.vs)):
+        codes[p, :, :4], scales[p] = 0x38, old
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k, v = ((torch.rand(1, KH * D, generator=g, device="cuda") - 0.5) * 2.0 ** 127 for _ in "kv")
+    want, tol = _expect(cache, table, [1], [5], k, v, None, 0, 0)
+    E.engram_kv_append(cache.desc, U.batch(E, table, [1], [5]), 2, k, 0, v, 0, None, 0, None, 0, 0)
+    assert E.engram_check() == 0
+    _compare(cache, want, tol)
+    assert (cache.k[p, :, 4] & 127 != 0).any() and (cache.v[p, :, 4] & 127 != 0).any()
