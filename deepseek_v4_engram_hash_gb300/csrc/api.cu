@@ -68,6 +68,16 @@ int *err_ptr() {
 
 namespace engram {
 int *error_word() { return err_ptr(); }
+
+cudaError_t zero_now(void *p, size_t bytes) {
+    cudaStream_t s = nullptr;
+    cudaError_t e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+    if (e != cudaSuccess) return e;
+    e = cudaMemsetAsync(p, 0, bytes, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    const cudaError_t d = cudaStreamDestroy(s);
+    return e != cudaSuccess ? e : d;
+}
 }  // namespace engram
 
 namespace {

@@ -173,7 +173,7 @@ int engram_attn_create(engram_attn **out) {
     if (!h->sms || cudaGetDevice(&h->device) != cudaSuccess ||
         cudaMalloc(&h->ws.part, attn_part_floats(h->sms) * sizeof(float)) != cudaSuccess ||
         cudaMalloc(&h->ws.arrived, attn_counters(h->sms) * sizeof(int)) != cudaSuccess ||
-        cudaMemset(h->ws.arrived, 0, attn_counters(h->sms) * sizeof(int)) != cudaSuccess || !error_word()) {
+        zero_now(h->ws.arrived, attn_counters(h->sms) * sizeof(int)) != cudaSuccess || !error_word()) {
         engram_attn_destroy(h);
         return ENGRAM_E_CUDA;
     }

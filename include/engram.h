@@ -438,7 +438,8 @@ int engram_kv_append(const engram_kv_cache *cache, const engram_kv_batch *batch,
 
 /* The attention's workspace on the current device: partial results of the
  * splits along the cache and their arrival counters (zero between calls).  Its size
- * does not depend on the calls it serves (about 41 MB on a GB300).  One call at
+ * does not depend on the calls it serves (about 41 MB on a GB300).  It is ready on
+ * every stream when engram_attn_create returns.  One call at
  * a time on a workspace: calls that may overlap on the GPU need one each.
  * ENGRAM_E_UNSUPPORTED on a GPU of more than 160 SMs; engram_attention refuses a
  * workspace of another device with ENGRAM_E_INVALID. */
