@@ -225,8 +225,8 @@ int engram_hasher_create(const engram_tables *t, int32_t batch, int64_t max_seq,
     cudaGetDevice(&h->device);
     const size_t bytes = (size_t)batch * max_seq * sizeof(int64_t);
     const size_t sched_bytes = 2 * kMaxLayers * sizeof(int);
-    if (cudaMalloc(&h->cache, bytes) != cudaSuccess || cudaMemset(h->cache, 0, bytes) != cudaSuccess ||
-        cudaMalloc(&h->sched, sched_bytes) != cudaSuccess || cudaMemset(h->sched, 0, sched_bytes) != cudaSuccess ||
+    if (cudaMalloc(&h->cache, bytes) != cudaSuccess || zero_now(h->cache, bytes) != cudaSuccess ||
+        cudaMalloc(&h->sched, sched_bytes) != cudaSuccess || zero_now(h->sched, sched_bytes) != cudaSuccess ||
         cudaStreamCreateWithFlags(&h->aux, cudaStreamNonBlocking) != cudaSuccess ||
         cudaEventCreateWithFlags(&h->ev_main, cudaEventDisableTiming) != cudaSuccess ||
         cudaEventCreateWithFlags(&h->ev_h, cudaEventDisableTiming) != cudaSuccess) {
@@ -269,7 +269,7 @@ int engram_check(uintptr_t stream) {
     if (!p) return ENGRAM_E_CUDA;
     int v = 0;
     if (cudaMemcpy(&v, p, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return ENGRAM_E_CUDA;
-    if (v != 0 && cudaMemset(p, 0, sizeof(int)) != cudaSuccess) return ENGRAM_E_CUDA;
+    if (v != 0 && zero_now(p, sizeof(int)) != cudaSuccess) return ENGRAM_E_CUDA;
     return v;
 }
 

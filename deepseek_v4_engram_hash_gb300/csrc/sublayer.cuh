@@ -8,7 +8,7 @@
 namespace engram {
 
 int *error_word();                  // the device error word (api.cu), null if it cannot be had
-// Zeroes new device memory and waits for that alone (api.cu).  cudaMemset would queue it on the legacy stream: behind
+// Zeroes device memory that nothing uses yet (or any more) and waits for that alone (api.cu).  cudaMemset would queue it on the legacy stream: behind
 // whatever that holds, and unordered with the non-blocking streams that use the memory next.
 cudaError_t zero_now(void *p, size_t bytes);
 

@@ -4,6 +4,7 @@ import torch
 
 import sublayer_glue as U
 import test_gpu_attention as A
+from deepseek_v4_engram_hash_gb300 import configs, synth
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +51,24 @@ def test_attention_on_a_new_workspace(E, new):
     assert E.engram_check(side) == 0
     torch.cuda.synchronize()
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_hash_on_a_new_hasher(E):
+    """Positions behind tokens that were never hashed look back on zeros, on a non-blocking stream at once after the create."""
+    cfg = configs.TINY
+    t = synth.hash_tables(cfg)
+    g = E.make_geom(cfg.n_layers, cfg.max_ngram, cfg.n_heads, cfg.head_dim, cfg.dim, cfg.hc, cfg.scale_block, cfg.vocab)
+    tabs = E.Tables(g, t["token_map"], t["pad_token_id"], t["multipliers"], t["primes"], t["offsets"])
+    d_ids = torch.from_numpy(synth.token_ids(cfg, "new-hasher", 5)[None]).cuda()
+    want, got = (torch.zeros((1, 5, cfg.n_layers, cfg.cols), dtype=torch.int64, device="cuda") for _ in range(2))
+    settled = E.Hasher(tabs, 1, 4096)
+    torch.cuda.synchronize()
+    E.engram_hash(settled, d_ids, 5, 7, want)
+    side = torch.cuda.Stream()
+    _leave_old_bytes()
+    _busy_default_stream()
+    hs = E.Hasher(tabs, 1, 4096)
+    E.engram_hash(hs, d_ids, 5, 7, got, stream=side)
+    assert E.engram_check(side) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
