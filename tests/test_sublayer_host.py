@@ -131,3 +131,12 @@ def test_refusals_raise_in_the_binding(E):
         E.engram_kv_append(c, b, 0, A, 0, A, 0, None, 0, None, 0, 0, stream=type("S", (), {"cuda_stream": 0}))
     assert e.value.code == UNSUPPORTED
     assert ctypes.sizeof(E.engram_kv_cache) == 64 and ctypes.sizeof(E.engram_kv_batch) == 48
+
+
+def test_every_source_is_built():
+    """No kernel file lies beside the build's lists: a stray one is in no library, and its symbols may be another's."""
+    import glob
+    import os
+    from deepseek_v4_engram_hash_gb300 import build
+    have = {os.path.basename(p) for p in glob.glob(os.path.join(build.CSRC, "*.cu"))}
+    assert have == set(build.ENGRAM_SRCS) | set(build.SYNTH_SRCS)
