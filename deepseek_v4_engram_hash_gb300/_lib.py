@@ -358,10 +358,36 @@ def engram_workspace_layout(geom: engram_geom, tokens: int) -> list:
 
 # ---- attention sub-layer ---------------------------------------------------
 
+def _check(t, what, elements, dtype=None, strides=None):
+    """Refuses (ENGRAM_E_INVALID) a tensor that a descriptor would misread: of another element type (dtype None: one byte
+    each), not readable by the GPU, laid out otherwise (dense, or with these strides) or with fewer elements."""
+    if not isinstance(t, torch.Tensor):
+        return
+    if t.element_size() != 1 if dtype is None else t.dtype != dtype:
+        raise EngramError(-1, f"{what} of {t.dtype}")
+    if strides is None or t.dim() != len(strides):
+        dense = t.is_contiguous()
+    else:
+        dense = all(n == 1 or a == b for n, a, b in zip(t.shape, t.stride(), strides))
+    if not dense:
+        raise EngramError(-1, f"{what} with strides {tuple(t.stride())}")
+    room = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() if strides else t.numel()
+    if room < elements:
+        raise EngramError(-1, f"{what}: {room} elements where {elements} are read")
+    if not (t.is_cuda or (torch.cuda.is_available() and t.is_pinned())):
+        raise EngramError(-1, f"{what} on {t.device}")
+
+
 class KvCache:
     """An `engram_kv_cache` descriptor; keeps its tensors alive."""
 
     def __init__(self, d_k, d_v, d_k_scales, d_v_scales, n_pages, n_kv_heads, page_tokens, head_dim, page_stride=0):
+        page = n_kv_heads * page_tokens * head_dim
+        stride = page_stride or page
+        for t, s, name in ((d_k, d_k_scales, "k"), (d_v, d_v_scales, "v")):
+            _check(t, "KvCache: " + name, (n_pages - 1) * stride + page,
+                   strides=(stride, page_tokens * head_dim, head_dim, 1))
+            _check(s, f"KvCache: {name}_scales", n_pages * n_kv_heads)
         self._keep = (d_k, d_v, d_k_scales, d_v_scales)
         self.desc = engram_kv_cache(*(_ptr(t).value for t in self._keep), int(n_pages), int(page_stride),
                                     int(n_kv_heads), int(page_tokens), int(head_dim))
@@ -372,6 +398,10 @@ class KvBatch:
     """An `engram_kv_batch` descriptor; keeps its device arrays alive."""
 
     def __init__(self, d_page_table, d_kv_len, d_row_start, batch, max_pages, rows, max_rows, table_stride=0):
+        stride = table_stride or max_pages
+        _check(d_page_table, "KvBatch: page_table", (batch - 1) * stride + max_pages, torch.int32, (stride, 1))
+        _check(d_kv_len, "KvBatch: kv_len", batch, torch.int32)
+        _check(d_row_start, "KvBatch: row_start", batch + 1, torch.int32)
         self._keep = (d_page_table, d_kv_len, d_row_start)
         self.desc = engram_kv_batch(*(_ptr(t).value for t in self._keep), int(table_stride), int(batch),
                                     int(max_pages), int(rows), int(max_rows))
@@ -382,6 +412,7 @@ class Rope:
     """An `engram_rope` descriptor; keeps its table alive."""
 
     def __init__(self, d_table, positions, dim, interleaved=False):
+        _check(d_table, "Rope: table", positions * dim, torch.float32)
         self._keep = d_table
         self.desc = engram_rope(_ptr(d_table).value, int(positions), int(dim), int(interleaved))
         self.ref = ctypes.addressof(self.desc)

@@ -140,3 +140,54 @@ def test_every_source_is_built():
     from deepseek_v4_engram_hash_gb300 import build
     have = {os.path.basename(p) for p in glob.glob(os.path.join(build.CSRC, "*.cu"))}
     assert have == set(build.ENGRAM_SRCS) | set(build.SYNTH_SRCS)
+
+
+def _cache_of(E, k=None, ks=None, n_pages=8, page_stride=0):
+    import torch
+    k = torch.zeros(8, 2, 16, 64, dtype=torch.uint8) if k is None else k
+    ks = torch.zeros(8, 2, dtype=torch.uint8) if ks is None else ks
+    return lambda: E.KvCache(k, A, ks, A, n_pages, 2, 16, 64, page_stride)
+
+
+def test_descriptors_refuse_tensors_that_they_would_misread(E):
+    """Element types, strides and sizes that do not fit, and tensors of the CPU: refused where the descriptor is made."""
+    import torch
+    i32, i64, u8, f32, f64 = torch.int32, torch.int64, torch.uint8, torch.float32, torch.float64
+
+    def batch(table=None, lens=None, start=None, stride=0):
+        table = torch.zeros(3, 4, dtype=i32) if table is None else table
+        return lambda: E.KvBatch(table, lens, start, 3, 4, 6, 2, stride)
+
+    cases = [
+        (_cache_of(E, k=torch.zeros(8, 2, 16, 64, dtype=torch.int16)), "int16"),
+        (_cache_of(E, k=torch.zeros(8, 16, 2, 64, dtype=u8).transpose(1, 2)), "strides"),
+        (_cache_of(E, k=torch.zeros(16, 2, 16, 64, dtype=u8)[::2]), "strides"),
+        (_cache_of(E, n_pages=9), "elements"),
+        (_cache_of(E, k=torch.zeros(8 * 4096, dtype=u8), page_stride=8192), "elements"),
+        (_cache_of(E, k=A, ks=torch.zeros(8, 2, dtype=f32)), "float32"),
+        (_cache_of(E, k=A, ks=torch.zeros(2, 8, dtype=u8).T), "strides"),
+        (_cache_of(E, k=A, ks=torch.zeros(15, dtype=u8)), "elements"),
+        (_cache_of(E), "cpu"),
+        (_cache_of(E, k=torch.zeros(16, 2, 16, 64, dtype=u8)[::2], page_stride=4096), "cpu"),   # its stride is given
+        (batch(table=torch.zeros(3, 4, dtype=i64)), "int64"),
+        (batch(table=torch.zeros(4, 3, dtype=i32).T), "strides"),
+        (batch(table=torch.zeros(3, 8, dtype=i32)[:, :4]), "strides"),
+        (batch(table=torch.zeros(2, 4, dtype=i32)), "elements"),
+        (batch(table=torch.zeros(3, 8, dtype=i32)[:, :4], stride=8), "cpu"),
+        (batch(table=A, lens=torch.zeros(3, dtype=i64)), "int64"),
+        (batch(table=A, lens=torch.zeros(6, dtype=i32)[::2]), "strides"),
+        (batch(table=A, lens=torch.zeros(2, dtype=i32)), "elements"),
+        (batch(table=A, lens=A, start=torch.zeros(3, dtype=i32)), "elements"),
+        (batch(table=A, lens=A, start=torch.zeros(4, dtype=i32)), "cpu"),
+        (lambda: E.Rope(torch.zeros(64, 32, 2, dtype=f64), 64, 64), "float64"),
+        (lambda: E.Rope(torch.zeros(32, 64, 2).transpose(0, 1), 64, 64), "strides"),
+        (lambda: E.Rope(torch.zeros(63, 32, 2), 64, 64), "elements"),
+        (lambda: E.Rope(torch.zeros(64, 32, 2), 64, 64), "cpu"),
+    ]
+    for i, (make, why) in enumerate(cases):
+        with pytest.raises(E.EngramError) as e:
+            make()
+        assert e.value.code == INVALID and why in str(e.value), (i, str(e.value))
+    E.KvCache(A, A, A, A, 8, 2, 16, 64)                      # addresses are taken as they are
+    E.KvBatch(A, A, None, 3, 4, 6, 2)
+    E.Rope(A, 64, 64)
