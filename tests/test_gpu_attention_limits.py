@@ -97,3 +97,66 @@ def test_every_value_scale_up_to_the_largest(E, attn, H, new, vbyte):
     cache.vs.fill_(vbyte)
     out, lse = A._run(E, attn, cache, plan, q, H, 0.1, 0, 0)
     A._check(cache, table, [new], [n], q, H, 0.1, 0, 0, out, lse)
+
+
+@pytest.mark.parametrize("H,KH,D,pt,new,kv", [(8, 2, 128, 16, [1, 1, 1], [900, 33, 130]), (4, 1, 64, 64, [3], [700]),
+                                              (8, 2, 128, 64, [70, 5], [300, 290]), (16, 1, 64, 16, [257], [600])])
+@pytest.mark.parametrize("down", [0, 6])
+def test_large_scores_with_exact_products(E, attn, H, KH, D, pt, new, kv, down):
+    """Whole-number queries and keys: every sum of products is a whole number under 2^24, so it is exact in any order.
+
+    With scale = ln 2 2^-down the scores in log2 units are whole multiples of 2^-down (up to thousands) to within the
+    roundings of the scale, of the sum with the value's exponent, of the bound and of the differences with it: under
+    6 x 2^-24 T, T the largest |t|.  So a weight is right to 2^-22 T, and its quotient by the sum to 2^-21 T, to 2^-20
+    (the exponentials) and to 2^-11 (f16), or to 2^-32 of the largest where f16 has no more bits; sums are f32."""
+    scale = LN2 * 2.0 ** -down
+    table = U.pages_for(kv, pt, sum(-(-t // pt) for t in kv) + 2)
+    cache = U.Cache(E, sum(-(-t // pt) for t in kv) + 2, KH, pt, D)
+    U.fill_random(cache, table, kv, 3)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    whole = torch.randint(-8, 9, cache.k.shape, generator=g, device="cuda").float().to(torch.float8_e4m3fn).view(torch.uint8)
+    cache.k.copy_(torch.where(cache.k & 127 == 127, cache.k, whole))             # what no token holds stays NaN
+    cache.ks.copy_(torch.where(cache.ks == 255, cache.ks, torch.full_like(cache.ks, 127)))
+    q = (torch.randint(-8, 9, (sum(new), H * D), generator=g, device="cuda") * 8).bfloat16()
+    out, lse = A._run(E, attn, cache, U.batch(E, table, new, kv), q, H, scale, 0, 0)
+    row = 0
+    for b, (n, t) in enumerate(zip(new, kv)):
+        k, v = U.sequence_tokens(R, cache, table, b, t)
+        pos = torch.arange(t - n, t, device="cuda")
+        qs = q[row: row + n].double().view(n, H, D)
+        want, wl, mass, _, big = R.attention(qs, k, v, pos, scale, 0)
+        T = 16 + max(float((qs[:, h] @ k[:, h // (H // KH)].T).abs().max()) for h in range(H)) * 2.0 ** -down
+        got, gl = out[row: row + n].double().view(n, H, D), lse[row: row + n].double()
+        tol = 2.0 ** -8 * want.abs() + (2.0 ** -10 + 2.0 ** -20 * T) * mass + (t * 2.0 ** -31 + 2.0 ** -22) * big[..., None]
+        assert ((got - want).abs() <= tol).all(), (b, T, ((got - want).abs() / tol.clamp(min=1e-30)).max())
+        assert ((gl - wl).abs() <= 2.0 ** -21 * T + 2.0 ** -20 * (1 + wl.abs())).all()
+        row += n
+
+
+@pytest.mark.parametrize("ty", [0, 1])
+def test_prompt_and_chunks_leave_the_same_pages_and_outputs(E, attn, ty):
+    """96 tokens at once and as 64 + 31 + 1 from the same inputs: the two pages that the first chunk fills are equal bit
+    for bit, and each output is within its bound of the 64-bit one over its own cache."""
+    KH, H, D, pt, n = 2, 8, 128, 32, 96
+    table = U.pages_for([n], pt, 4)
+    w = A._queries(n, H + 2 * KH, D, ty, 4)
+    st = w.stride(0)
+    caches = []
+    for parts in ((96,), (64, 31, 1)):
+        cache = U.Cache(E, 4, KH, pt, D)
+        at = 0
+        for T in parts:
+            x = w[at: at + T]
+            q, k, v = x[:, : H * D], x[:, H * D: (H + KH) * D], x[:, (H + KH) * D:]
+            plan = U.batch(E, table, [T], [at + T])
+            E.engram_kv_append(cache.desc, plan, ty, k, st, v, st, None, 0, None, 0, 0)
+            out, lse = torch.empty(T, H * D, dtype=w.dtype, device="cuda"), torch.empty(T, H, device="cuda")
+            E.engram_attention(attn, cache.desc, plan, ty, q, st, H, D ** -0.5, 0, out, 0, lse)
+            assert E.engram_check() == 0
+            A._check(cache, table, [T], [at + T], q, H, D ** -0.5, 0, ty, out, lse)
+            at += T
+            if at == 64:
+                first = [c[table[0, :2].long()].clone() for c in cache.tensors()]
+        caches.append(cache)
+    for one, chunked in zip(caches[0].tensors(), first):
+        assert torch.equal(one[table[0, :2].long()], chunked)
