@@ -7,8 +7,8 @@
 // and  out = sum_j 2^(s_j) 2^ev vc_j / sum_j 2^(s_j).  The value scale goes into
 // the exponent: t_j = s_j + ev, p_j = 2^(t_j - M) with M a running bound of the
 // row's t, out = sum p_j vc_j / L, L = sum p_j 2^-ev, so the f16 probabilities
-// always hold the row's largest contributions with full precision, whatever
-// the scales.  M is set 7 under the row's largest t so far, and moves (and the sums are
+// always hold the row's largest contributions with full precision, while L keeps the
+// weight of a token whose p 2^-ev counts: of value scales up to 2^100 apart.  M is set 7 under the row's largest t so far, and moves (and the sums are
 // rescaled) only when a t exceeds it by more than 15: until then p <= 2^15, which f16
 // and the f32 sums hold.
 //

@@ -461,9 +461,11 @@ void engram_attn_destroy(engram_attn *a);
  * Scores, statistics and sums are f32; q is brought to f16 by a power of two
  * per row and head (f16 products of codes are exact; elements under 2^-13 of the
  * row's largest may lose bits, those under 2^-25 of it are lost); the probabilities are
- * rounded to f16 for the product with v (so a token whose weight is under 2^-29 of the
- * row's largest may count there as nothing).  A value block whose scale is under
- * 2^-66 counts as zeros.  Codes 127 and 255 (NaN) are not allowed at positions
+ * rounded to f16 for the product with v (so a token whose weight times its value scale
+ * is under 2^-29 of the row's largest such product may count there as nothing).  A
+ * value block whose scale is under 2^-66 counts as zeros; the value scales of a
+ * sequence may lie 2^100 apart (further apart, tokens of the smallest may lose their
+ * weight).  Codes 127 and 255 (NaN) are not allowed at positions
  * from the first that a row of the sequence sees to kv_len - 1; the cache may hold
  * anything elsewhere, and page-table entries of pages that end before that first
  * position are not read (a sliding window's pages may be given back).

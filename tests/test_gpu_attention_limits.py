@@ -160,3 +160,18 @@ def test_prompt_and_chunks_leave_the_same_pages_and_outputs(E, attn, ty):
         caches.append(cache)
     for one, chunked in zip(caches[0].tensors(), first):
         assert torch.equal(one[table[0, :2].long()], chunked)
+
+
+@pytest.mark.parametrize("H,new", [(4, 1), (16, 40)])
+@pytest.mark.parametrize("apart", [60, 100])
+def test_value_scales_far_apart(E, attn, H, new, apart):
+    """Value blocks of one sequence up to 2^100 apart, the smallest at 2^-66: the small ones keep their whole weight."""
+    KH, D, pt, n = 2, 128, 16, 160
+    table = U.pages_for([n], pt, 12)
+    cache = U.Cache(E, 12, KH, pt, D)
+    U.fill_random(cache, table, [n], 3, spread=0)
+    for i, p in enumerate(table[0].tolist()):
+        cache.vs[p] = 61 + (apart if i % 2 else 0)
+    q = A._queries(new, H, D, 0, 5)
+    out, lse = A._run(E, attn, cache, U.batch(E, table, [new], [n]), q, H, 0.09, 0, 0)
+    A._check(cache, table, [new], [n], q, H, 0.09, 0, 0, out, lse)
