@@ -97,7 +97,7 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
     return lo | hi << 16;
 }
-// The codes of eight values of a block; a NaN block's codes are zero.
+// The codes of eight values of a block; zero for a NaN block.
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], uint32_t byte) {
     if (byte == 255u) return make_uint2(0u, 0u);
     const float s = inv_scale(byte);

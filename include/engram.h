@@ -349,7 +349,8 @@ int engram_selftest_wait_timeout(int32_t limit_us, uintptr_t stream);
  * 8-bit blocks.  A block of values is held as e4m3 codes with one power-of-two
  * scale: the smallest 2^e, e >= -126, with amax <= 448 * 2^e;
  * code = e4m3_rne(value / 2^e).  A block that holds an infinity or a NaN has a
- * NaN scale (e8m0 byte 255) and zero codes: all its values read as NaN.
+ * NaN scale (e8m0 byte 255): all its values read as NaN, whatever its codes.  Those
+ * written with it or after it are zero; a page's earlier ones stay as they are.
  * ------------------------------------------------------------------------- */
 
 /* Residual addition and root-mean-square norm, per row:
