@@ -7,9 +7,10 @@
 // page's earlier codes are read and encoded again only when the scale grew.
 // One group of threads owns a unit, so nothing is shared between units and no
 // order matters.  Further blocks rotate the queries.
-// Bound by memory for prompts and by launch and load latency for single tokens.  64 registers a thread
-// keep 1024 threads on an SM: a 4096-token prompt of 32 query and 8 key/value heads of
-// 128 (94 MB, 13.9 us at the copy rate) takes 21.4 us; without the bound over 26 us.
+// Bound by latency: of launch and loads for single tokens, for prompts of 2.6 waves of blocks that each load, take a
+// maximum and store.  64 registers a thread keep 1024 threads on an SM and spill (block-wide forms: 48 to 64 bytes stored,
+// 64 to 104 loaded a thread): a 4096-token prompt of 32 query and 8 key/value heads of
+// 128 (94 MB, 13.9 us at the copy rate) takes 21.4 to 22.1 us; without the bound over 26 us.
 #include "sublayer.cuh"
 
 namespace engram {

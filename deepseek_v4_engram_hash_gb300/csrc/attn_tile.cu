@@ -25,11 +25,13 @@
 // half they were idle for the latencies between product, softmax and product: 432
 // against 379 us).  Tensor memory: S 2 x 2 x 64 columns, O 2 x D; P lies over its S.
 //
-// Bound by the softmax: two in-order warps a scheduler, about 1000 clocks for 64 tokens
-// of both beside the converters, against 512 of tensor work a half.  4096 tokens
+// Bound by latency between the roles: the longest is the softmax, two in-order warps a
+// scheduler and about 1000 clocks for 64 tokens of both beside the converters, against 512 of
+// tensor work a half, but no pipe is busy for more than 57 % of the time.  4096 tokens
 // behind 4096, 32 query and 8 key/value heads of 128 (412 GFLOP in the visible pairs):
-// 308 us, 71 % of the measured bf16 rate; an entry costs about 5 us in which the
-// tensor cores wait (output, queries, first scores).  Times below are this call's.
+// 320 us, 69 % of the measured bf16 rate; an entry costs about 5 us in which the
+// tensor cores wait (output, queries, first scores).  Times below are this call's, those of
+// steps before kRoom with a bound at the row's largest score (11 us less).
 //
 // The call's (sequence, head, row tile, 128-token tile) list, with kEntryCost places more
 // for each row tile (what beginning and ending one takes), is cut evenly over one CTA an
@@ -50,7 +52,7 @@ using namespace tcg;
 constexpr int kHalf = 128;                           // rows of a half
 constexpr int kRows = 2 * kHalf;
 constexpr int kTok = 128, kPartTok = 64;             // tokens a step, and a score buffer
-// Places of a row tile beside its tiles: 8 x 512 tokens behind 512 take 78 us, with 3 or 6 81, with 5 80.
+// Places of a row tile beside its tiles: 8 x 512 tokens behind 512 took 78 us, with 3 or 6 81, with 5 80 (81 with kRoom).
 constexpr int kEntryCost = 4;
 constexpr int kThreads = 640, kSoftWarps = 8;
 constexpr int kGroups = kTok / 16;                   // scale groups a step (a page is at least 16 tokens)
@@ -118,7 +120,7 @@ struct Entry {
 };
 constexpr int kEntries = 4, kEntryUsers = kSoftWarps + 4 + 5;
 
-// This CTA's range, walked by one warp (start) and its lane 0 (next).
+// This CTA's range, walked by one warp; all of its lanes hold the same.
 struct Walk {
     int64_t t, end, per, t0;
     Entry e;

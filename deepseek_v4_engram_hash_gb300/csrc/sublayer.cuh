@@ -185,7 +185,7 @@ struct AppendArgs {
 cudaError_t launch_kv_append(AppendArgs a, cudaStream_t s);
 
 constexpr int kMaxSms = 160;            // what the joins' shared memory is sized for (GB300: 152)
-// Workspace of the attention: two partial results a CTA and one arrival counter a CTA.
+// Workspace of the attention: two partial results a CTA and its arrival counters (one, on row tiles one a half).
 struct AttnWorkspace {
     float *part;
     int *arrived;
