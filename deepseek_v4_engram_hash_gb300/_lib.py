@@ -25,6 +25,9 @@ ENGRAM_T_BF16 = 0
 ENGRAM_T_F16 = 1
 ENGRAM_T_F32 = 2
 
+ENGRAM_SCORE_SIGMOID = 0
+ENGRAM_SCORE_SOFTMAX = 1
+
 
 class EngramError(RuntimeError):
     def __init__(self, code: int, what: str):
@@ -61,6 +64,22 @@ class engram_kv_batch(ctypes.Structure):
 class engram_rope(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_int64), ("dim", ctypes.c_int32),
                 ("interleaved", ctypes.c_int32)]
+
+
+class engram_router(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("n_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32), ("group_best", ctypes.c_int32),
+                ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class engram_expert_lists(ctypes.Structure):
+    _fields_ = [("offsets", ctypes.c_void_p), ("pairs", ctypes.c_void_p), ("n_experts", ctypes.c_int32),
+                ("top_k", ctypes.c_int32), ("tokens", ctypes.c_int32)]
+
+
+class engram_fp8_weight(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("fmt", ctypes.c_int32),
+                ("n_experts", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("gated", ctypes.c_int32)]
 
 
 _lib = None
@@ -117,6 +136,11 @@ def lib() -> ctypes.CDLL:
             "engram_attn_reset": ([P, st], ctypes.c_int),
             "engram_attn_destroy": ([P], None),
             "engram_attention": ([P, P, P, i32, P, i64, i32, ctypes.c_float, i32, P, i64, P, st], ctypes.c_int),
+            "engram_route_workspace_bytes": ([i32, i32], sz),
+            "engram_route": ([P, i32, P, i64, P, i32, P, P, P, P, sz, st], ctypes.c_int),
+            "engram_project_fp8": ([P, i64, P, i32, i32, P, P, i32, P, i64, st], ctypes.c_int),
+            "engram_glu_fp8": ([P, i64, P, i32, i32, P, P, ctypes.c_float, i32, P, P, st], ctypes.c_int),
+            "engram_combine": ([P, i32, i64, P, i32, i32, i32, P, i32, i64, i32, P, i64, st], ctypes.c_int),
             "engram_check": ([st], ctypes.c_int),
             "engram_strerror": ([ctypes.c_int], ctypes.c_char_p),
         }
@@ -460,6 +484,72 @@ def engram_attention(attn: Attention, cache: KvCache, batch: KvBatch, type, d_q,
                      d_out, out_stride, d_lse=None, stream=None):
     _ok(lib().engram_attention(attn.handle, cache.ref, batch.ref, type, _adr(d_q), q_stride, n_heads, scale, window,
                                _adr(d_out), out_stride, _adr(d_lse), _stream(stream)), "engram_attention")
+
+
+# ---- experts' sub-layer ----------------------------------------------------
+
+class Router:
+    """An `engram_router`: how tokens choose experts."""
+
+    def __init__(self, n_experts, top_k, score=ENGRAM_SCORE_SIGMOID, n_groups=1, top_groups=1, group_best=2,
+                 renormalise=True, scale=1.0):
+        self.desc = engram_router(int(n_experts), int(top_k), int(score), int(n_groups), int(top_groups), int(group_best),
+                                  int(bool(renormalise)), float(scale))
+        self.ref = ctypes.addressof(self.desc)
+
+
+class ExpertLists:
+    """An `engram_expert_lists` descriptor; keeps its device arrays alive."""
+
+    def __init__(self, d_offsets, d_pairs, n_experts, top_k, tokens):
+        _check(d_offsets, "ExpertLists: offsets", n_experts + 1, torch.int32)
+        _check(d_pairs, "ExpertLists: pairs", tokens * top_k, torch.int32)
+        self._keep = (d_offsets, d_pairs)
+        self.desc = engram_expert_lists(_ptr(d_offsets).value, _ptr(d_pairs).value, int(n_experts), int(top_k), int(tokens))
+        self.ref = ctypes.addressof(self.desc)
+
+
+class Fp8Weight:
+    """An `engram_fp8_weight` descriptor; keeps its tensors alive."""
+
+    def __init__(self, d_codes, d_scales, fmt, n_experts, n, k, gated=False):
+        mats = n_experts * (2 if gated else 1)
+        _check(d_codes, "Fp8Weight: codes", mats * n * k)
+        _check(d_scales, "Fp8Weight: scales", mats * (-(-n // 128)) * (-(-k // 128)),
+               torch.float32 if fmt == ENGRAM_FMT_FP8 else None)
+        self._keep = (d_codes, d_scales)
+        self.desc = engram_fp8_weight(_ptr(d_codes).value, _ptr(d_scales).value, int(fmt), int(n_experts), int(n), int(k),
+                                      int(bool(gated)))
+        self.ref = ctypes.addressof(self.desc)
+
+
+def engram_route_workspace_bytes(n_experts: int, tokens: int) -> int:
+    return int(lib().engram_route_workspace_bytes(int(n_experts), int(tokens)))
+
+
+def engram_route(router: Router, type, d_logits, stride, d_bias, tokens, d_ids, d_weights, lists: ExpertLists = None,
+                 d_ws=None, ws_bytes=0, stream=None):
+    _ok(lib().engram_route(router.ref, type, _adr(d_logits), stride, _adr(d_bias), tokens, _adr(d_ids), _adr(d_weights),
+                           lists.ref if lists else None, _adr(d_ws), ws_bytes, _stream(stream)), "engram_route")
+
+
+def engram_project_fp8(d_x, x_stride, d_x_scales, x_fmt, rows, weight: Fp8Weight, lists: ExpertLists, out_type, d_out,
+                       out_stride, stream=None):
+    _ok(lib().engram_project_fp8(_adr(d_x), x_stride, _adr(d_x_scales), x_fmt, rows, weight.ref,
+                                 lists.ref if lists else None, out_type, _adr(d_out), out_stride, _stream(stream)),
+        "engram_project_fp8")
+
+
+def engram_glu_fp8(d_x, x_stride, d_x_scales, x_fmt, rows, weight: Fp8Weight, lists: ExpertLists, limit, out_fmt, d_out,
+                   d_out_scales, stream=None):
+    _ok(lib().engram_glu_fp8(_adr(d_x), x_stride, _adr(d_x_scales), x_fmt, rows, weight.ref, lists.ref if lists else None,
+                             limit, out_fmt, _adr(d_out), _adr(d_out_scales), _stream(stream)), "engram_glu_fp8")
+
+
+def engram_combine(d_y, y_type, y_stride, d_weights, tokens, top_k, dim, d_add, add_type, add_stride, out_type, d_out,
+                   out_stride, stream=None):
+    _ok(lib().engram_combine(_adr(d_y), y_type, y_stride, _adr(d_weights), tokens, top_k, dim, _adr(d_add), add_type,
+                             add_stride, out_type, _adr(d_out), out_stride, _stream(stream)), "engram_combine")
 
 
 def prepare_events(events) -> None:

@@ -266,6 +266,23 @@ bool make_map_u8_4d(CUtensorMap *map, const void *ptr, const uint64_t (&dims)[4]
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_map_u8(CUtensorMap *map, const void *ptr, int rank, const uint64_t *dims, const uint64_t *strides,
+                 const uint32_t *box) {
+    auto fn = encode_fn();
+    if (!fn || rank < 2 || rank > 4) return false;
+    cuuint64_t d[4], st[3];
+    cuuint32_t b[4], estr[4];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        estr[i] = 1;
+        if (i) st[i - 1] = strides[i - 1];
+    }
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void *>(ptr), d, st, b, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool have_tensor_maps() { return encode_fn() != nullptr; }
 
 }  // namespace tcg

@@ -13,14 +13,10 @@ struct engram_attn {
     int device, sms;
 };
 
-namespace {
-
-inline cudaStream_t S(uintptr_t s) { return reinterpret_cast<cudaStream_t>(s); }
-inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-inline int cuda_rc(cudaError_t e) { return e == cudaSuccess ? ENGRAM_OK : ENGRAM_E_CUDA; }
+namespace engram {
 
 // SMs of the current device, 0 if they cannot be had.
-inline int sm_count() {
+int sm_count() {
     static int known[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
@@ -31,6 +27,14 @@ inline int sm_count() {
     }
     return known[dev];
 }
+
+}  // namespace engram
+
+namespace {
+
+inline cudaStream_t S(uintptr_t s) { return reinterpret_cast<cudaStream_t>(s); }
+inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline int cuda_rc(cudaError_t e) { return e == cudaSuccess ? ENGRAM_OK : ENGRAM_E_CUDA; }
 
 // A stride of 0 means dense; others must keep every row 16-byte aligned.
 inline int check_stride(int64_t *stride, int64_t dense) {

@@ -11,6 +11,7 @@ int *error_word();                  // the device error word (api.cu), null if i
 // Zeroes device memory that nothing uses yet (or any more) and waits for that alone (api.cu).  cudaMemset would queue it on the legacy stream: behind
 // whatever that holds, and unordered with the non-blocking streams that use the memory next.
 cudaError_t zero_now(void *p, size_t bytes);
+int sm_count();                     // SMs of the current device (sublayer.cu), 0 if they cannot be had
 
 // ---------------------------------------------------------------------------
 // Eight consecutive elements (16-byte aligned) to f32 and back.

@@ -88,6 +88,10 @@ bool make_map(CUtensorMap *map, const void *ptr, uint64_t inner, uint64_t outer,
 // the swizzle of that width), boxes {dims[0], box1, 1, 1}.
 bool make_map_u8_4d(CUtensorMap *map, const void *ptr, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
                     uint32_t box1);
+// Byte tensor map of 2 to 4 dimensions (dims, byte strides of all but the first, and box innermost first), 128-byte
+// swizzle (box[0] 128).
+bool make_map_u8(CUtensorMap *map, const void *ptr, int rank, const uint64_t *dims, const uint64_t *strides,
+                 const uint32_t *box);
 bool have_tensor_maps();
 
 }  // namespace tcg

@@ -476,6 +476,119 @@ int engram_attention(engram_attn *a, const engram_kv_cache *cache, const engram_
                      const void *d_q, int64_t q_stride, int32_t n_heads, float scale, int32_t window, void *d_out,
                      int64_t out_stride, float *d_lse, uintptr_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The experts' sub-layer behind the attention: routing, products of 8-bit rows
+ * with 8-bit weights, and the sum of the experts' outputs.  (As above: entry
+ * points of this library's ABI without a counterpart on the pages.)  All of them
+ * only enqueue work; captured, they read their inputs anew at every replay.  Make
+ * a process's first call of each outside of captures (it loads the kernels).
+ * Results do not depend on timing: no floating-point atomics.
+ * ------------------------------------------------------------------------- */
+
+#define ENGRAM_SCORE_SIGMOID 0
+#define ENGRAM_SCORE_SOFTMAX 1
+
+/* How tokens choose experts.  1 <= n_experts <= 1024; n_groups divides
+ * n_experts, 1 <= n_groups <= 32; 1 <= top_groups <= n_groups; group_best 1 or
+ * 2; 1 <= top_k <= 32 and top_k <= top_groups * n_experts / n_groups. */
+typedef struct {
+    int32_t n_experts, top_k, score, n_groups, top_groups, group_best, renormalise;
+    float scale;
+} engram_router;
+
+/* The (token, choice) pairs of a call's tokens by expert: pair t * top_k + j is
+ * choice j of token t; the pairs of expert e are pairs[offsets[e]] ..
+ * pairs[offsets[e + 1] - 1], in rising order.  offsets [n_experts + 1], pairs
+ * [tokens * top_k] (those behind offsets[n_experts] have no meaning).  Device
+ * arrays, 4-byte aligned; the products read them when their kernels run.  An
+ * expert whose offsets fall or leave 0 .. tokens * top_k raises ENGRAM_E_LENGTH and
+ * counts as one without pairs; a pair outside 0 .. tokens * top_k - 1 raises
+ * ENGRAM_E_ROW. */
+typedef struct {
+    int32_t *offsets, *pairs;
+    int32_t n_experts, top_k, tokens;
+} engram_expert_lists;
+
+/* Routing, for each token t with the logits l [n_experts]:
+ *   s = 1 / (1 + exp(-l)) (ENGRAM_SCORE_SIGMOID) or softmax(l);
+ *   c = s + bias; with bias NULL the order of c is that of l;
+ *   groups (top_groups < n_groups): of the n_groups groups of n_experts / n_groups
+ *     consecutive experts those top_groups stay whose group_best largest c (s where
+ *     bias is NULL) have the largest sums;
+ *   the choices are the top_k experts of those groups with the largest c, in
+ *     falling order; of equal ones (experts or groups) the lower index;
+ *   weight_j = scale * s_j, divided by sum_j s_j + 1e-20 if renormalise.
+ * Choices are those of 64-bit scores: where 32-bit ones are too near to tell, the
+ * row's are formed again in 64 bits.  An expert whose logit is -inf is masked: it
+ * is never chosen and adds nothing to a softmax or a group (a group of masked experts
+ * alone ranks behind all others).  A token with fewer than top_k experts left has
+ * id -1 and weight 0 in the places that remain, and those are in no list (a
+ * padded batch masks its idle tokens this way).  A NaN logit masks its expert and
+ * makes all weights of its token NaN; so does +inf under softmax.
+ *   d_logits [tokens, n_experts] `type`, rows `stride` elements apart (0 = dense);
+ *   d_bias [n_experts] f32 (finite) or NULL; d_ids [tokens, top_k] int32, d_weights
+ *   [tokens, top_k] f32; lists NULL (no lists), or with n_experts, top_k and tokens
+ *   as here: offsets and pairs are written (not behind offsets[n_experts]).
+ *   d_ws: engram_route_workspace_bytes(n_experts, tokens) bytes, 4-byte aligned,
+ *   any content, for lists alone (else unused, may be NULL); calls that may overlap need one each.
+ * tokens = 0 writes offsets alone. */
+size_t engram_route_workspace_bytes(int32_t n_experts, int32_t tokens);
+int engram_route(const engram_router *router, int32_t type, const void *d_logits, int64_t stride, const float *d_bias,
+                 int32_t tokens, int32_t *d_ids, float *d_weights, const engram_expert_lists *lists, void *d_ws,
+                 size_t ws_bytes, uintptr_t stream);
+
+/* e4m3 weights with a scale for each block of 128 x 128: codes [n_experts, parts, n,
+ * k] (parts: 2 if gated, the gate's rows before the other's, else 1), 16-byte
+ * aligned; scales [n_experts, parts, ceil(n / 128), ceil(k / 128)], fmt
+ * ENGRAM_FMT_FP8: f32 of any value (4-byte aligned), ENGRAM_FMT_FP8_E8M0: bytes.
+ * k % 16 == 0, k <= 65536; n <= 2^24; 1 <= n_experts <= 1024.  Codes 127 and 255 are NaN, as is an
+ * e8m0 byte of 255. */
+typedef struct {
+    const uint8_t *codes;
+    const void *scales;
+    int32_t fmt, n_experts, n, k, gated;
+} engram_fp8_weight;
+
+/* out = x W^T of e4m3 rows: row r is
+ *   out[r, n] = sum_b (sx[r, b] sw[n / 128, b]) sum_{128 b <= k < 128 (b + 1)} x[r, k] W[n, k],
+ * products of codes exact, sums and scales in f32, rounded once to out_type.
+ *   d_x [rows, k] codes, rows x_stride bytes apart (0 = k; a multiple of 16), 16-byte
+ *   aligned; d_x_scales [rows, ceil(k / 128)] dense, x_fmt ENGRAM_FMT_FP8 (f32) or
+ *   ENGRAM_FMT_FP8_E8M0: what engram_residual_norm and engram_glu_fp8 write with blocks of 128;
+ *   d_out [rows, n] out_type (bf16, f16, f32), rows out_stride elements apart (0 = n), aligned to its elements.
+ * lists NULL: one matrix (w->n_experts 1) for all rows.  Otherwise rows ==
+ * lists->tokens * lists->top_k; x has the rows in the lists' order (row p belongs
+ * to pair pairs[p] and its expert's matrix, as engram_glu_fp8 leaves them) and
+ * out has them by pair: row p goes to out[pairs[p]].  Rows of pairs in no list are not written. */
+int engram_project_fp8(const uint8_t *d_x, int64_t x_stride, const void *d_x_scales, int32_t x_fmt, int32_t rows,
+                       const engram_fp8_weight *w, const engram_expert_lists *lists, int32_t out_type, void *d_out,
+                       int64_t out_stride, uintptr_t stream);
+
+/* The gated product: g and u are the rows' products (as above, in f32) with the two
+ * parts of a gated weight; limit > 0: g = min(g, limit), u = max(-limit, min(u, limit));
+ *   a = g / (1 + exp(-g)) * u,
+ * written as e4m3 codes d_out [.., n] (dense, 16-byte aligned, n % 16 == 0) with a power-of-two
+ * scale for each block of 128 of a row (8-bit blocks, above), d_out_scales [..,
+ * ceil(n / 128)], out_fmt ENGRAM_FMT_FP8 (f32) or ENGRAM_FMT_FP8_E8M0 (bytes).
+ * lists NULL: output row r from x row r.  Otherwise rows == lists->tokens, and
+ * output row p is that of pair pairs[p]: x row pairs[p] / top_k, expert p's matrices; rows behind
+ * offsets[n_experts] are not written.  x: as above.  limit: 0 (none) or finite and > 0. */
+int engram_glu_fp8(const uint8_t *d_x, int64_t x_stride, const void *d_x_scales, int32_t x_fmt, int32_t rows,
+                   const engram_fp8_weight *w, const engram_expert_lists *lists, float limit, int32_t out_fmt,
+                   uint8_t *d_out, void *d_out_scales, uintptr_t stream);
+
+/* The experts' outputs back to their tokens:
+ *   out[t] = sum_j weights[t, j] y[t * top_k + j]  (+ add[t]), in f32, rounded once;
+ * choices are summed in rising j, add last; a choice of weight 0 is not read (its row may hold anything).
+ *   d_y [tokens * top_k, dim] y_type, d_add [tokens, dim] add_type or NULL, d_out
+ *   [tokens, dim] out_type; rows *_stride elements apart (0 = dense); d_weights
+ *   [tokens, top_k] f32.  d_out may be d_add itself (the same type and stride).
+ * dim % 8 == 0, dim <= 65536; strides multiples of 8; tensors 16-byte aligned (weights
+ * 4); 1 <= top_k <= 32. */
+int engram_combine(const void *d_y, int32_t y_type, int64_t y_stride, const float *d_weights, int32_t tokens,
+                   int32_t top_k, int32_t dim, const void *d_add, int32_t add_type, int64_t add_stride,
+                   int32_t out_type, void *d_out, int64_t out_stride, uintptr_t stream);
+
 const char *engram_strerror(int code);
 
 #ifdef __cplusplus
