@@ -22,7 +22,8 @@ FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
 
 ENGRAM_SRCS = ["api.cu", "hash.cu", "rows.cu", "gemv.cu", "gemm.cu", "gemm_simt.cu", "gemm_tc.cu", "gemm_tc2.cu",
                "gate.cu", "noalloc.cu", "selftest.cu", "sublayer.cu", "norm.cu", "append.cu", "attention.cu",
-               "attn_tile.cu", "experts.cu", "route.cu", "product.cu", "combine.cu"]
+               "attn_tile.cu", "experts.cu", "route.cu", "product.cu", "product_rows.cu",
+               "combine.cu"]
 SYNTH_SRCS = ["synth.cu"]
 
 LIBENGRAM = os.path.join(PKG, "libengram.so")

@@ -1,0 +1,441 @@
+// product_rows.cu -- the products of product.cu for many rows (prompts): 128 rows of x
+// on the M side of the MMA, 256 weight rows (or 128 of the gate and the other's 128) on its N side.
+//
+// With weights on M a factor belongs to a column, and reading it from shared memory for
+// every column, beside operands that two N = 128 MMAs read twice, bounds a block at 1500
+// clocks.  Here a thread has one row: its factors sx sw are two registers a block, an
+// MMA of M 128, N 256, K 32 reads 12 KB for 128 clocks, and a row's largest output is
+// found by the threads that hold it.
+//
+// Roles (16 warps):
+//   warp 0       TMA: a block's 256 weight rows and, unless they are gathered, its 128 rows of x;
+//   warp 1       issues the MMAs, two 256-column buffers in tensor memory;
+//   warps 2, 3   scales of a block's rows and weights, to shared memory;
+//   warps 4..7   rows of x that the lists gather, by 16-byte asynchronous copies (a block of 128 rows
+//                takes four warps 290 clocks, one warp 690; as tile::gather4 2200 to 2900);
+//   warps 8..15  take a block's sums into their f32 accumulators (thread: a row, 128 columns,
+//                for glu 64 of each part; 128 KB of them in about 300 clocks); at the end of a tile they write it.
+// Waits are bounded as in product.cu.
+#include "product.cuh"
+
+#include <type_traits>
+
+namespace engram {
+
+namespace {
+
+using namespace product;
+
+constexpr int kRows = 128, kCols = 256;
+constexpr int kScaleWarp = 2, kCopyWarp = 4, kCopyWarps = 4, kEpiWarp = 8, kEpiWarps = 8, kThreads = 32 * (kEpiWarp + kEpiWarps);
+constexpr uint32_t kStage = 3 * kTileA;              // x, then the weights
+constexpr int kStages = 4, kSlots = kStages + 2;     // of scales: [128] of rows, 2 of weights
+constexpr uint32_t oScale = kStages * kStage;
+constexpr uint32_t kSlotBytes = kRows * 4 + 16;
+constexpr uint32_t oMax = oScale + kSlots * kSlotBytes;   // glu: [2][2 groups][128] f32 bits
+constexpr uint32_t oBar = oMax + 2 * 2 * kRows * 4;
+constexpr uint32_t oFlag = oBar + 8 * (2 * kStages + 2 * kSlots + 4 + 2);
+constexpr uint32_t oLists = oFlag + 16;
+constexpr size_t smem_bytes(int E) { return 1024 + oLists + (3 * (size_t)E + 1) * 4; }
+
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+// acc += u f, with f in both halves of a register pair.
+__device__ __forceinline__ void add32(uint64_t (&acc)[16], uint32_t (&u)[32], uint64_t f) {
+    tmem_wait_ld();
+    asm volatile(""
+                 : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]), "+r"(u[6]), "+r"(u[7]),
+                   "+r"(u[8]), "+r"(u[9]), "+r"(u[10]), "+r"(u[11]), "+r"(u[12]), "+r"(u[13]), "+r"(u[14]), "+r"(u[15]),
+                   "+r"(u[16]), "+r"(u[17]), "+r"(u[18]), "+r"(u[19]), "+r"(u[20]), "+r"(u[21]), "+r"(u[22]), "+r"(u[23]),
+                   "+r"(u[24]), "+r"(u[25]), "+r"(u[26]), "+r"(u[27]), "+r"(u[28]), "+r"(u[29]), "+r"(u[30]), "+r"(u[31]));
+#pragma unroll
+    for (int j = 0; j < 16; ++j) acc[j] = fma2(pack2(u[2 * j], u[2 * j + 1]), f, acc[j]);
+}
+// 32 outputs of one row from column `col` on, of which `left` exist.
+template <class T>
+__device__ __forceinline__ void store32(void *out, int64_t at, const uint64_t (&acc)[16], int left, bool wide) {
+    if (left <= 0) return;
+    T *o = static_cast<T *>(out) + at;
+    if (wide && left >= 32) {
+        constexpr int kWords = sizeof(T) == 4 ? 32 : 16;
+        uint32_t w[kWords];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            float x, y;
+            unpack2(acc[j], x, y);
+            if (sizeof(T) == 4) {
+                w[(2 * j) % kWords] = __float_as_uint(x), w[(2 * j + 1) % kWords] = __float_as_uint(y);
+            } else {
+                w[j] = sizeof(T) == 2 && std::is_same<T, __half>::value ? pack_f16x2(x, y) : pack_bf16x2(x, y);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kWords; j += 4)
+            reinterpret_cast<uint4 *>(o)[j / 4] = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        float x, y;
+        unpack2(acc[j], x, y);
+        if (2 * j < left) o[2 * j] = T(x);
+        if (2 * j + 1 < left) o[2 * j + 1] = T(y);
+    }
+}
+
+template <bool GLU>
+__global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_constant__ Params p) {
+    constexpr int ST = kStages, FS = kSlots;
+    extern __shared__ uint8_t smem_raw[];
+    const ProductArgs &a = p.a;
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base - raw);
+    auto full = [&](int s) { return base + oBar + 8u * s; };
+    auto empty = [&](int s) { return base + oBar + 8u * (ST + s); };
+    auto ffull = [&](int s) { return base + oBar + 8u * (2 * ST + s); };
+    auto fempty = [&](int s) { return base + oBar + 8u * (2 * ST + FS + s); };
+    auto tfull = [&](int b) { return base + oBar + 8u * (2 * ST + 2 * FS + b); };
+    auto tempty = [&](int b) { return base + oBar + 8u * (2 * ST + 2 * FS + 2 + b); };
+    const uint32_t drain = base + oBar + 8u * (2 * ST + 2 * FS + 4);
+    const uint32_t together = drain + 8;
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + oFlag);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + oFlag + 4);
+    int *first = reinterpret_cast<int *>(smem + oLists), *count = first + a.E, *before = count + a.E;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool gather = GLU && a.pairs;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(full(s), gather ? 1 + kCopyWarps : 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int s = 0; s < FS; ++s) {
+            mbar_init(ffull(s), 2);
+            mbar_init(fempty(s), kEpiWarps);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(tfull(b), 1);
+            mbar_init(tempty(b), kEpiWarps);
+        }
+        mbar_init(drain, 1);
+        mbar_init(together, kEpiWarps);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32((const void *)tmem_slot)), "r"(512u) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    set_lists(a, first, count, before, kRows, kThreads);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    const int t0 = blockIdx.x, t_step = gridDim.x, tiles = before[a.E] * p.m_tiles, KB = p.KB;
+    auto tile_at = [&](int t) { return tile_of(p, first, count, before, t, GLU ? kM : kCols); };
+    // whether the tile has weight rows for its second 128 columns
+    auto two = [&](const TileAt &t) { return GLU || t.m0 + kM < a.N; };
+    auto wait_one = [&](uint32_t bar, uint32_t parity) {
+        return mbar_try(bar, parity & 1) || mbar_wait(bar, parity & 1, abort_flag, a.err);
+    };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait_one(bar, parity)) != 0; };
+
+    // 512 threads launch with 128 registers each: 256 x 56 + 256 x 200 are as many
+    if (warp < kEpiWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0) {
+        // ---- weights, and rows that stand together ----
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = t0; t < tiles && ok; t += t_step) {
+            const TileAt w = tile_at(t);
+            for (int kb = 0; kb < KB; ++kb, ++it) {
+                const int s = it % ST;
+                if (!(ok = wait(empty(s), it / ST ^ 1))) break;
+                if (elect()) {
+                    const uint32_t at = base + s * kStage, bar = full(s);
+                    mbar_expect_tx(bar, gather ? 2 * kTileA : 3 * kTileA);
+                    tma_weights(at + kTileA, &p.mw, kb * 128, w.m0, 0, w.e, bar);
+                    if (!gather) tma_rows(at, &p.mx, kb * 128, w.row, bar);
+                }
+                __syncwarp();
+            }
+        }
+        // copies already issued land before the CTA can leave
+        for (uint32_t d = 1; d <= (uint32_t)ST && d <= it; ++d) {
+            const uint32_t last = it - d;
+            const uint64_t began = now_ns();
+            while (!mbar_try(full(last % ST), (last / ST) & 1) && now_ns() - began < 10000000ull) {
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---- MMA ----
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = t0; t < tiles && ok; t += t_step) {
+            const TileAt w = tile_at(t);
+            const uint32_t idesc = idesc_f8(two(w) ? kCols : kM);
+            for (int kb = 0; kb < KB; ++kb, ++it) {
+                const int s = it % ST, b = it & 1;
+                if (!(ok = wait(tempty(b), it >> 1 ^ 1) && wait(full(s), it / ST))) break;
+                tc_fence_after();
+                const uint32_t at = base + s * kStage, d = tmem + b * kCols;
+                const uint64_t da = sdesc(at), db = sdesc(at + kTileA);
+                if (elect()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mma_f8(d, da + 2u * k, db + 2u * k, idesc, k != 0);
+                    commit(empty(s));
+                    commit(tfull(b));
+                }
+                __syncwarp();
+            }
+        }
+        // every MMA issued has finished before tensor memory can be freed
+        if (elect()) commit(drain);
+        __syncwarp();
+        const uint64_t began = now_ns();
+        while (!mbar_try(drain, 0) && now_ns() - began < 100000000ull) {
+        }
+        __syncwarp();
+    } else if (warp < kCopyWarp) {
+        // ---- scales: 64 rows a warp ----
+        const int c0 = (warp - kScaleWarp) * 64 + lane;
+        const bool vec_x = four_at_once(a.x_scales, a.x_fmt, KB), vec_w = four_at_once(a.w_scales, a.w_fmt, KB);
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = t0; t < tiles && ok; t += t_step) {
+            const TileAt w = tile_at(t);
+            const bool both = two(w);
+            int xi[2];
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const int c = c0 + v * 32;
+                xi[v] = c < w.n ? gather ? token_of(a, w.row + c) : w.row + c : -1;
+            }
+            const int64_t w0 = ((int64_t)w.e * (GLU ? 2 : 1) * p.NB + w.m0 / kM) * KB, w1 = w0 + (int64_t)(GLU ? p.NB : 1) * KB;
+            // the next four blocks' scales are on their way while these are written
+            uint4 next_x[2], next_w[2];
+            auto fetch = [&](int kb4) {
+                const int left = KB - kb4;
+#pragma unroll
+                for (int v = 0; v < 2; ++v)
+                    if (xi[v] >= 0) next_x[v] = load_scales(a.x_scales, a.x_fmt, vec_x, (int64_t)xi[v] * KB + kb4, left);
+                next_w[0] = load_scales(a.w_scales, a.w_fmt, vec_w, w0 + kb4, left);
+                if (both) next_w[1] = load_scales(a.w_scales, a.w_fmt, vec_w, w1 + kb4, left);
+            };
+            fetch(0);
+            for (int kb4 = 0; kb4 < KB && ok; kb4 += 4) {
+                uint4 x[2];
+#pragma unroll
+                for (int v = 0; v < 2; ++v) x[v] = next_x[v];
+                const uint4 s0 = next_w[0], s1 = both ? next_w[1] : s0;
+                if (kb4 + 4 < KB) fetch(kb4 + 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (kb4 + j >= KB || !ok) continue;
+                    const int s = it % FS;
+                    if (!(ok = wait(fempty(s), it / FS ^ 1))) continue;
+                    float *f = reinterpret_cast<float *>(smem + oScale + s * kSlotBytes);
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) f[c0 + v * 32] = xi[v] >= 0 ? scale_at(x[v], a.x_fmt, vec_x, j) : 0.f;
+                    if (warp == kScaleWarp && lane < 2) f[kRows + lane] = scale_at(lane ? s1 : s0, a.w_fmt, vec_w, j);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(ffull(s));
+                    ++it;
+                }
+            }
+        }
+    } else if (warp < kEpiWarp) {
+        // ---- gathered rows: eight lanes a row of 128 bytes, this warp's four of each 16 rows ----
+        constexpr int LAG = 2, NR = kRows / (4 * kCopyWarps);   // blocks in flight behind the newest; rows a lane
+        const int r0 = (warp - kCopyWarp) * 4 + (lane >> 3), chunk = lane & 7;
+        uint32_t it = 0;
+        bool ok = true;
+        // the copies of block `done` have landed: its stage is full as far as this warp goes
+        auto landed = [&](uint32_t done) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full(done % ST));
+        };
+        for (int t = t0; t < tiles && ok && gather; t += t_step) {
+            const TileAt w = tile_at(t);
+            uint32_t from[NR];                       // where the rows begin, in 16 bytes
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                const int r = r0 + i * 4 * kCopyWarps;
+                from[i] = r < w.n ? (uint32_t)(token_of(a, w.row + r) * (a.x_stride >> 4)) : 0u;
+            }
+            for (int kb = 0; kb < KB; ++kb, ++it) {
+                const int s = it % ST;
+                if (!(ok = wait(empty(s), it / ST ^ 1))) break;
+                const bool real = kb * 128 + chunk * 16 < a.K;
+                const uint8_t *src = a.x + (real ? kb * 128 + chunk * 16 : 0);
+                // rows 16 apart have the same place in the swizzle
+                const uint32_t at = base + s * kStage + r0 * 128 + (chunk ^ (r0 & 7)) * 16;
+#pragma unroll
+                for (int i = 0; i < NR; ++i)
+                    if (16 * i < w.n) cp16(at + i * 2048, src + (uint64_t)from[i] * 16, real);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                if (it >= LAG) {
+                    cp_wait<LAG>();
+                    landed(it - LAG);
+                }
+            }
+        }
+        cp_wait<0>();
+        for (uint32_t done = it > LAG ? it - LAG : 0; ok && gather && done < it; ++done) landed(done);
+        __syncwarp();
+    } else {
+        // ---- sums and output ----
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        const int g = (warp - kEpiWarp) >> 2, q = warp & 3, row = 32 * q + lane;
+        // this thread's columns: 128 g .. + 127 in quarters, or 64 g .. + 63 of both parts in halves (parts in turn)
+        auto column = [&](int i) { return GLU ? (i & 1) * kM + 64 * g + (i >> 1) * 32 : kM * g + 32 * i; };
+        const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
+        uint32_t it = 0, turn = 0;
+        bool ok = true;
+        for (int t = t0; t < tiles && ok; t += t_step) {
+            const TileAt w = tile_at(t);
+            int to = row < w.n ? w.row + row : -1;
+            if (!GLU && a.pairs && to >= 0) to = out_row_of(a, to);
+            const bool mine = GLU || w.m0 + kM * g < a.N;     // columns that exist
+            uint64_t acc[4][16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) acc[i][j] = 0;
+            for (int kb = 0; kb < KB; ++kb, ++it) {
+                const int b = it & 1, s = it % FS;
+                if (!(ok = wait(ffull(s), it / FS))) break;
+                const float *f = reinterpret_cast<const float *>(smem + oScale + s * kSlotBytes);
+                const float sx = f[row], f0 = sx * f[kRows + (GLU ? 0 : g)], f1 = GLU ? sx * f[kRows + 1] : f0;
+                if (!(ok = wait(tfull(b), it >> 1))) break;
+                tc_fence_after();
+                if (mine) {
+                    const uint64_t ff[2] = {pack2(__float_as_uint(f0), __float_as_uint(f0)), pack2(__float_as_uint(f1), __float_as_uint(f1))};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t u[32];
+                        tmem_ld32_nowait(lanes + b * kCols + column(i), u);
+                        add32(acc[i], u, ff[i & 1]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(tempty(b));
+                    mbar_arrive(fempty(s));
+                }
+            }
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            if (GLU) {
+                uint32_t *amax = reinterpret_cast<uint32_t *>(smem + oMax) + (turn++ & 1) * 2 * kRows + row;
+                float big = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; i += 2)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float x0, y0, x1, y1;
+                        unpack2(acc[i][j], x0, y0);
+                        unpack2(acc[i + 1][j], x1, y1);
+                        x0 = gated(x0, x1, a.limit);
+                        y0 = gated(y0, y1, a.limit);
+                        big = amax3(big, x0, y0);
+                        acc[i][j] = pack2(__float_as_uint(x0), __float_as_uint(y0));
+                    }
+                amax[g * kRows] = __float_as_uint(big);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(together);
+                if (!(ok = wait(together, turn - 1))) break;   // the next tile's go to the other half
+                const uint32_t byte = block_scale_byte(max(amax[0], amax[kRows]));
+                const float inv = byte == 255u ? 0.f : inv_scale(byte);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int at = w.m0 + 64 * g + 32 * i;
+                    if (to < 0 || at >= a.N) continue;
+                    uint32_t c[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float x0, y0, x1, y1;
+                        unpack2(acc[2 * i][2 * j], x0, y0);
+                        unpack2(acc[2 * i][2 * j + 1], x1, y1);
+                        c[j] = byte == 255u ? 0u : e4m3x4(x0 * inv, y0 * inv, x1 * inv, y1 * inv);
+                    }
+                    uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.out) + (int64_t)to * a.N + at);
+                    o[0] = make_uint4(c[0], c[1], c[2], c[3]);
+                    if (at + 16 < a.N) o[1] = make_uint4(c[4], c[5], c[6], c[7]);
+                }
+                if (g == 0 && to >= 0) {
+                    const int64_t i = (int64_t)to * p.NB + w.m0 / kM;
+                    if (a.out_type == ENGRAM_FMT_FP8_E8M0)
+                        static_cast<uint8_t *>(a.out_scales)[i] = (uint8_t)byte;
+                    else
+                        static_cast<float *>(a.out_scales)[i] = e8m0_to_f32(byte);
+                }
+            } else if (to >= 0) {
+                const int at = w.m0 + kM * g, left = a.N - at;
+                const int64_t o = (int64_t)to * a.out_stride + at;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (a.out_type == ENGRAM_T_BF16)
+                        store32<__nv_bfloat16>(a.out, o + 32 * i, acc[i], left - 32 * i, p.wide);
+                    else if (a.out_type == ENGRAM_T_F16)
+                        store32<__half>(a.out, o + 32 * i, acc[i], left - 32 * i, p.wide);
+                    else
+                        store32<float>(a.out, o + 32 * i, acc[i], left - 32 * i, p.wide);
+                }
+            }
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+template <bool GLU>
+cudaError_t launch(Params &p, cudaStream_t s) {
+    const ProductArgs &a = p.a;
+    static bool attr[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(product_rows_kernel<GLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)smem_bytes(kMaxExperts));
+        if (e != cudaSuccess) return e;
+        attr[dev] = true;
+    }
+    const uint64_t xd[2] = {(uint64_t)a.K, (uint64_t)a.rows}, xst[1] = {(uint64_t)a.x_stride};
+    const uint32_t box[2] = {128, kRows};
+    if (!make_map_u8(&p.mx, a.x, 2, xd, xst, box)) return cudaErrorInvalidValue;
+    p.m_tiles = (a.N + (GLU ? kM : kCols) - 1) / (GLU ? kM : kCols);
+    const int64_t tiles = (int64_t)product_row_tiles(a, kRows) * p.m_tiles;
+    if (tiles > 0x3FFFFFFF) return cudaErrorInvalidConfiguration;
+    p.split = 1;
+    // row tiles side by side whose rows stay in L2
+    const int64_t rows_l2 = (int64_t(48) << 20) / a.K / kRows;
+    p.group = (int)(rows_l2 < 8 ? 8 : rows_l2 > 0x3FFFFFFF ? 0x3FFFFFFF : rows_l2);
+    product_rows_kernel<GLU><<<(unsigned)(tiles < a.sms ? tiles : a.sms), kThreads, smem_bytes(a.E), s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_product_rows(product::Params &p, cudaStream_t s) { return p.a.glu ? launch<true>(p, s) : launch<false>(p, s); }
+
+}  // namespace engram
