@@ -49,7 +49,7 @@ template <int NT> struct Cfg {
     static constexpr uint32_t oStage = oRows + kRowSlots * NT * 4;        // outputs: 512 bytes a warp (glu: [16][128] codes a group)
     static constexpr uint32_t oMax = oStage + kEpiWarps * 512;            // [groups][16][4] f32 bits
     static constexpr uint32_t oBar = oMax + kGroups * 16 * 4 * 4;
-    static constexpr uint32_t oFlag = oBar + 8 * (2 * kStages + 2 * kFactors + 4 + 1 + kGroups);
+    static constexpr uint32_t oFlag = oBar + 8 * (2 * kStages + 2 * kFactors + 2 + 1 + kGroups);
     static constexpr uint32_t oLists = oFlag + 16;                        // first [E], rows [E], tiles before [E + 1]
     static size_t bytes(int E) { return 1024 + oLists + (3 * (size_t)E + 1) * 4; }
 };
@@ -64,12 +64,11 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (base - raw);
     auto full = [&](int s) { return base + C::oBar + 8u * s; };
-    auto empty = [&](int s) { return base + C::oBar + 8u * (ST + s); };
+    auto done = [&](int s) { return base + C::oBar + 8u * (ST + s); };
     auto ffull = [&](int s) { return base + C::oBar + 8u * (2 * ST + s); };
     auto fempty = [&](int s) { return base + C::oBar + 8u * (2 * ST + FS + s); };
-    auto tfull = [&](int b) { return base + C::oBar + 8u * (2 * ST + 2 * FS + b); };
-    auto tempty = [&](int b) { return base + C::oBar + 8u * (2 * ST + 2 * FS + 2 + b); };
-    const uint32_t drain = base + C::oBar + 8u * (2 * ST + 2 * FS + 4);
+    auto tempty = [&](int b) { return base + C::oBar + 8u * (2 * ST + 2 * FS + b); };
+    const uint32_t drain = base + C::oBar + 8u * (2 * ST + 2 * FS + 2);
     auto together = [&](int g) { return drain + 8u * (1 + g); };
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + C::oFlag);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::oFlag + 4);
@@ -80,14 +79,13 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
             mbar_init(full(s), GLU && a.pairs ? 2 : 1);
-            mbar_init(empty(s), 1);
+            mbar_init(done(s), 1);
         }
         for (int s = 0; s < FS; ++s) {
             mbar_init(ffull(s), 1);
             mbar_init(fempty(s), C::kEpiWarps);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(tfull(b), 1);
             mbar_init(tempty(b), C::kEpiWarps);
         }
         mbar_init(drain, 1);
@@ -115,10 +113,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
     auto tile_at = [&](int t) { return tile_of(p, first, count, before, t, GLU ? kM : 2 * kM); };
     // whether the tile has a second block of weight rows
     auto two = [&](const TileAt &t) { return GLU || t.m0 + kM < a.N; };
-    auto wait_one = [&](uint32_t bar, uint32_t parity) {
-        return mbar_try(bar, parity & 1) || mbar_wait(bar, parity & 1, abort_flag, a.err);
-    };
-    auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait_one(bar, parity)) != 0; };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, warp_wait(bar, parity & 1, abort_flag, a.err)) != 0; };
     const bool gather = GLU && a.pairs;
 
     // 640 threads launch with 96 registers each: 128 x 64 + 512 x 104 are as many
@@ -133,7 +128,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
             const uint32_t bytes = 2 * kTileA + (gather ? 0u : few ? 16u * 128u : NT * 128u);
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = it % ST;
-                if (!(ok = wait(empty(s), it / ST ^ 1))) break;
+                if (!(ok = wait(done(s), it / ST ^ 1))) break;
                 if (elect()) {
                     const uint32_t at = base + s * C::kStage, bar = full(s);
                     mbar_expect_tx(bar, bytes);
@@ -172,8 +167,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
 #pragma unroll
                         for (int k = 0; k < 4; ++k) mma_f8(d + NT, d1 + 2u * k, db + 2u * k, idesc, k != 0);
                     }
-                    commit(empty(s));
-                    commit(tfull(b));
+                    commit(done(s));
                 }
                 __syncwarp();
             }
@@ -263,7 +257,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
             const int n8 = (w.n + 7) / 8;
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = it % ST;
-                if (!(ok = wait(empty(s), it / ST ^ 1))) break;
+                if (!(ok = wait(done(s), it / ST ^ 1))) break;
                 const bool real = kb * 128 + chunk * 16 < a.K;
                 const uint8_t *src = a.x + (real ? kb * 128 + chunk * 16 : 0);
                 // rows r0 and r0 + 4 of each 8: a chunk's place is turned by the row's last three bits
@@ -391,7 +385,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
                 for (int j = 0; j < 8; ++j) acc0[i][j] = acc1[i][j] = 0;
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int b = it & 1, s = it % FS;
-                if (!(ok = wait(ffull(s), it / FS) && wait(tfull(b), it >> 1))) break;
+                if (!(ok = wait(ffull(s), it / FS) && wait(done(it % ST), it / ST))) break;
                 tc_fence_after();
                 const float *f = reinterpret_cast<const float *>(smem + C::oFactor) + s * 2 * NT;
                 const uint32_t d = lanes + b * 2 * NT;

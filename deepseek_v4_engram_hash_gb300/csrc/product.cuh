@@ -29,6 +29,30 @@ struct TileAt {
     int e, row, n, m0;                               // expert, first row, rows, first weight row
 };
 
+// Bounded wait as common.cuh's mbar_wait, for a whole warp; the timer, whose reading takes longer than most waits here, is looked at
+// every 64 tests only.  (One lane that waits for its warp is slow: 1245 clocks for a hand-over that takes all lanes 513.)
+// Once the flag is up a wait ends after 64 tests, so that loops may vote on the outcome at their end alone.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err) {
+    bool ok = true;
+    uint64_t began = 0;
+    for (uint32_t i = 1; !mbar_try(bar, parity); ++i) {
+        if (i & 63) continue;
+        if (*abort_flag) {
+            ok = false;
+            break;
+        }
+        const uint64_t now = now_ns();
+        if (!began) began = now;
+        if (now - began > kWaitNs) {
+            *abort_flag = 1;
+            set_err(err, ENGRAM_E_TIMEOUT);
+            ok = false;
+            break;
+        }
+    }
+    __syncwarp();
+    return ok;                                       // of this lane
+}
 // One lane of a converged warp.  (Issued by "lane == 0" instead, a block's four MMAs and two commits took the warp 700 clocks.)
 __device__ __forceinline__ bool elect() {
     uint32_t ok;

@@ -10,7 +10,8 @@
 // Roles (16 warps):
 //   warp 0       TMA: a block's 256 weight rows and, unless they are gathered, its 128 rows of x;
 //   warp 1       issues the MMAs, two 256-column buffers in tensor memory;
-//   warps 2, 3   scales of a block's rows and weights, to shared memory;
+//   warps 2, 3   scales of a block's rows and weights, to shared memory (a load of theirs takes the better part of
+//                two blocks beside the copies);
 //   warps 4..7   rows of x that the lists gather, by 16-byte asynchronous copies (a block of 128 rows
 //                takes four warps 290 clocks, one warp 690; as tile::gather4 2200 to 2900);
 //   warps 8..15  take a block's sums into their f32 accumulators (thread: a row, 128 columns,
@@ -29,37 +30,23 @@ using namespace product;
 constexpr int kRows = 128, kCols = 256;
 constexpr int kScaleWarp = 2, kCopyWarp = 4, kCopyWarps = 4, kEpiWarp = 8, kEpiWarps = 8, kThreads = 32 * (kEpiWarp + kEpiWarps);
 constexpr uint32_t kStage = 3 * kTileA;              // x, then the weights
-constexpr int kStages = 4, kSlots = kStages + 2;     // of scales: [128] of rows, 2 of weights
+constexpr int kStages = 4;
+// Scales of four blocks at a time (the last of a tile: what is left), [4][128] of rows and [4][2] of weights.
+constexpr int kSlots = 3;
+constexpr uint32_t kSlotBytes = 4 * kRows * 4 + 4 * 2 * 4;
 constexpr uint32_t oScale = kStages * kStage;
-constexpr uint32_t kSlotBytes = kRows * 4 + 16;
 constexpr uint32_t oMax = oScale + kSlots * kSlotBytes;   // glu: [2][2 groups][128] f32 bits
 constexpr uint32_t oBar = oMax + 2 * 2 * kRows * 4;
-constexpr uint32_t oFlag = oBar + 8 * (2 * kStages + 2 * kSlots + 4 + 2);
+constexpr uint32_t oFlag = oBar + 8 * (2 * kStages + 2 + 2 + 2 * kSlots);
 constexpr uint32_t oLists = oFlag + 16;
 constexpr size_t smem_bytes(int E) { return 1024 + oLists + (3 * (size_t)E + 1) * 4; }
 
-__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-}
 // acc += u f, with f in both halves of a register pair.
-__device__ __forceinline__ void add32(uint64_t (&acc)[16], uint32_t (&u)[32], uint64_t f) {
-    tmem_wait_ld();
-    asm volatile(""
-                 : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]), "+r"(u[6]), "+r"(u[7]),
-                   "+r"(u[8]), "+r"(u[9]), "+r"(u[10]), "+r"(u[11]), "+r"(u[12]), "+r"(u[13]), "+r"(u[14]), "+r"(u[15]),
-                   "+r"(u[16]), "+r"(u[17]), "+r"(u[18]), "+r"(u[19]), "+r"(u[20]), "+r"(u[21]), "+r"(u[22]), "+r"(u[23]),
-                   "+r"(u[24]), "+r"(u[25]), "+r"(u[26]), "+r"(u[27]), "+r"(u[28]), "+r"(u[29]), "+r"(u[30]), "+r"(u[31]));
+__device__ __forceinline__ void add16(uint64_t *acc, const uint32_t (&u)[16], uint64_t f) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) acc[j] = fma2(pack2(u[2 * j], u[2 * j + 1]), f, acc[j]);
+    for (int j = 0; j < 8; ++j) acc[j] = fma2(pack2(u[2 * j], u[2 * j + 1]), f, acc[j]);
 }
+
 // 32 outputs of one row from column `col` on, of which `left` exist.
 template <class T>
 __device__ __forceinline__ void store32(void *out, int64_t at, const uint64_t (&acc)[16], int left, bool wide) {
@@ -94,20 +81,19 @@ __device__ __forceinline__ void store32(void *out, int64_t at, const uint64_t (&
 
 template <bool GLU>
 __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_constant__ Params p) {
-    constexpr int ST = kStages, FS = kSlots;
+    constexpr int ST = kStages;
     extern __shared__ uint8_t smem_raw[];
     const ProductArgs &a = p.a;
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (base - raw);
     auto full = [&](int s) { return base + oBar + 8u * s; };
-    auto empty = [&](int s) { return base + oBar + 8u * (ST + s); };
-    auto ffull = [&](int s) { return base + oBar + 8u * (2 * ST + s); };
-    auto fempty = [&](int s) { return base + oBar + 8u * (2 * ST + FS + s); };
-    auto tfull = [&](int b) { return base + oBar + 8u * (2 * ST + 2 * FS + b); };
-    auto tempty = [&](int b) { return base + oBar + 8u * (2 * ST + 2 * FS + 2 + b); };
-    const uint32_t drain = base + oBar + 8u * (2 * ST + 2 * FS + 4);
+    auto done = [&](int s) { return base + oBar + 8u * (ST + s); };
+    auto tempty = [&](int b) { return base + oBar + 8u * (2 * ST + b); };
+    const uint32_t drain = base + oBar + 8u * (2 * ST + 2);
     const uint32_t together = drain + 8;
+    auto sfull = [&](int i) { return together + 8u * (1 + i); };
+    auto sempty = [&](int i) { return together + 8u * (1 + kSlots + i); };
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + oFlag);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + oFlag + 4);
     int *first = reinterpret_cast<int *>(smem + oLists), *count = first + a.E, *before = count + a.E;
@@ -117,18 +103,17 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
             mbar_init(full(s), gather ? 1 + kCopyWarps : 1);
-            mbar_init(empty(s), 1);
-        }
-        for (int s = 0; s < FS; ++s) {
-            mbar_init(ffull(s), 2);
-            mbar_init(fempty(s), kEpiWarps);
+            mbar_init(done(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(tfull(b), 1);
             mbar_init(tempty(b), kEpiWarps);
         }
         mbar_init(drain, 1);
         mbar_init(together, kEpiWarps);
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(sfull(i), 2);
+            mbar_init(sempty(i), kEpiWarps);
+        }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -148,13 +133,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
     auto tile_at = [&](int t) { return tile_of(p, first, count, before, t, GLU ? kM : kCols); };
     // whether the tile has weight rows for its second 128 columns
     auto two = [&](const TileAt &t) { return GLU || t.m0 + kM < a.N; };
-    auto wait_one = [&](uint32_t bar, uint32_t parity) {
-        return mbar_try(bar, parity & 1) || mbar_wait(bar, parity & 1, abort_flag, a.err);
-    };
-    auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait_one(bar, parity)) != 0; };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, warp_wait(bar, parity & 1, abort_flag, a.err)) != 0; };
+    auto lane_wait = [&](uint32_t bar, uint32_t parity) { return warp_wait(bar, parity & 1, abort_flag, a.err); };
 
-    // 512 threads launch with 128 registers each: 256 x 56 + 256 x 200 are as many
-    if (warp < kEpiWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    // 512 threads launch with 128 registers each: 256 x 80 + 256 x 176 are as many
+    if (warp < kEpiWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == 0) {
         // ---- weights, and rows that stand together ----
         uint32_t it = 0;
@@ -163,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
             const TileAt w = tile_at(t);
             for (int kb = 0; kb < KB; ++kb, ++it) {
                 const int s = it % ST;
-                if (!(ok = wait(empty(s), it / ST ^ 1))) break;
+                if (!(ok = wait(done(s), it / ST ^ 1))) break;
                 if (elect()) {
                     const uint32_t at = base + s * kStage, bar = full(s);
                     mbar_expect_tx(bar, gather ? 2 * kTileA : 3 * kTileA);
@@ -183,25 +166,27 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
         __syncwarp();
     } else if (warp == 1) {
         // ---- MMA ----
+        // (After a wait that ran out, what it issues reads anything and goes to sums that nobody writes.)
         uint32_t it = 0;
         bool ok = true;
+        const uint64_t desc = sdesc(base);
         for (int t = t0; t < tiles && ok; t += t_step) {
-            const TileAt w = tile_at(t);
-            const uint32_t idesc = idesc_f8(two(w) ? kCols : kM);
+            const uint32_t idesc = idesc_f8(two(tile_at(t)) ? kCols : kM);
             for (int kb = 0; kb < KB; ++kb, ++it) {
-                const int s = it % ST, b = it & 1;
-                if (!(ok = wait(tempty(b), it >> 1 ^ 1) && wait(full(s), it / ST))) break;
+                const int s = it % ST;
+                const uint32_t d = tmem + (it & 1) * kCols;
+                const uint64_t da = desc + s * (kStage >> 4), db = da + (kTileA >> 4);
+                if (!lane_wait(tempty(it & 1), it >> 1 ^ 1)) ok = false;
+                if (!lane_wait(full(s), it / ST)) ok = false;
                 tc_fence_after();
-                const uint32_t at = base + s * kStage, d = tmem + b * kCols;
-                const uint64_t da = sdesc(at), db = sdesc(at + kTileA);
                 if (elect()) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) mma_f8(d, da + 2u * k, db + 2u * k, idesc, k != 0);
-                    commit(empty(s));
-                    commit(tfull(b));
+                    commit(done(s));
                 }
                 __syncwarp();
             }
+            ok = __all_sync(0xFFFFFFFFu, ok);
         }
         // every MMA issued has finished before tensor memory can be freed
         if (elect()) commit(drain);
@@ -237,25 +222,20 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
                 if (both) next_w[1] = load_scales(a.w_scales, a.w_fmt, vec_w, w1 + kb4, left);
             };
             fetch(0);
-            for (int kb4 = 0; kb4 < KB && ok; kb4 += 4) {
-                uint4 x[2];
-#pragma unroll
-                for (int v = 0; v < 2; ++v) x[v] = next_x[v];
-                const uint4 s0 = next_w[0], s1 = both ? next_w[1] : s0;
+            for (int kb4 = 0; kb4 < KB; kb4 += 4, ++it) {
+                const uint4 x[2] = {next_x[0], next_x[1]}, s0 = next_w[0], s1 = both ? next_w[1] : s0;
                 if (kb4 + 4 < KB) fetch(kb4 + 4);
+                const int slot = it % kSlots;
+                float *f = reinterpret_cast<float *>(smem + oScale + slot * kSlotBytes);
+                if (!(ok = wait(sempty(slot), it / kSlots ^ 1))) break;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (kb4 + j >= KB || !ok) continue;
-                    const int s = it % FS;
-                    if (!(ok = wait(fempty(s), it / FS ^ 1))) continue;
-                    float *f = reinterpret_cast<float *>(smem + oScale + s * kSlotBytes);
+                for (int j = 0; j < 4; ++j)          // blocks behind the last: anything
 #pragma unroll
-                    for (int v = 0; v < 2; ++v) f[c0 + v * 32] = xi[v] >= 0 ? scale_at(x[v], a.x_fmt, vec_x, j) : 0.f;
-                    if (warp == kScaleWarp && lane < 2) f[kRows + lane] = scale_at(lane ? s1 : s0, a.w_fmt, vec_w, j);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(ffull(s));
-                    ++it;
-                }
+                    for (int v = 0; v < 2; ++v) f[j * kRows + c0 + v * 32] = xi[v] >= 0 ? scale_at(x[v], a.x_fmt, vec_x, j) : 0.f;
+                if (warp == kScaleWarp && lane < 8)
+                    f[4 * kRows + lane] = scale_at(lane & 1 ? s1 : s0, a.w_fmt, vec_w, lane >> 1);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sfull(slot));
             }
         }
     } else if (warp < kEpiWarp) {
@@ -280,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
             }
             for (int kb = 0; kb < KB; ++kb, ++it) {
                 const int s = it % ST;
-                if (!(ok = wait(empty(s), it / ST ^ 1))) break;
+                if (!(ok = wait(done(s), it / ST ^ 1))) break;
                 const bool real = kb * 128 + chunk * 16 < a.K;
                 const uint8_t *src = a.x + (real ? kb * 128 + chunk * 16 : 0);
                 // rows 16 apart have the same place in the swizzle
@@ -300,44 +280,59 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
         __syncwarp();
     } else {
         // ---- sums and output ----
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         const int g = (warp - kEpiWarp) >> 2, q = warp & 3, row = 32 * q + lane;
         // this thread's columns: 128 g .. + 127 in quarters, or 64 g .. + 63 of both parts in halves (parts in turn)
         auto column = [&](int i) { return GLU ? (i & 1) * kM + 64 * g + (i >> 1) * 32 : kM * g + 32 * i; };
         const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
-        uint32_t it = 0, turn = 0;
+        uint32_t it = 0, turn = 0, group = 0;        // blocks, tiles, groups of scales
         bool ok = true;
         for (int t = t0; t < tiles && ok; t += t_step) {
             const TileAt w = tile_at(t);
             int to = row < w.n ? w.row + row : -1;
             if (!GLU && a.pairs && to >= 0) to = out_row_of(a, to);
-            const bool mine = GLU || w.m0 + kM * g < a.N;     // columns that exist
             uint64_t acc[4][16];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 16; ++j) acc[i][j] = 0;
-            for (int kb = 0; kb < KB; ++kb, ++it) {
-                const int b = it & 1, s = it % FS;
-                if (!(ok = wait(ffull(s), it / FS))) break;
-                const float *f = reinterpret_cast<const float *>(smem + oScale + s * kSlotBytes);
-                const float sx = f[row], f0 = sx * f[kRows + (GLU ? 0 : g)], f1 = GLU ? sx * f[kRows + 1] : f0;
-                if (!(ok = wait(tfull(b), it >> 1))) break;
-                tc_fence_after();
-                if (mine) {
-                    const uint64_t ff[2] = {pack2(__float_as_uint(f0), __float_as_uint(f0)), pack2(__float_as_uint(f1), __float_as_uint(f1))};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t u[32];
-                        tmem_ld32_nowait(lanes + b * kCols + column(i), u);
-                        add32(acc[i], u, ff[i & 1]);
-                    }
+            // Steps of 16 columns: while one is added up the next is on its way from tensor memory, over the end of a block, too.
+            // Columns without weight rows are added up as well, nobody writes their sums: a test of them for every step
+            // took a block to 1100 clocks.
+            auto step_at = [&](int j) { return lanes + (it & 1) * kCols + column(j >> 1) + 16 * (j & 1); };
+            uint32_t u[2][16];
+            ok = lane_wait(done(it % ST), it / ST) && ok;
+            tc_fence_after();
+            tmem_ld16(step_at(0), u[0]);
+            for (int kb = 0; kb < KB; ++kb) {
+                const uint32_t slot = group % kSlots, four = kb & 3;
+                if (!four) ok = lane_wait(sfull(slot), group / kSlots) && ok;
+                const float *f = reinterpret_cast<const float *>(smem + oScale + slot * kSlotBytes), *fw = f + 4 * kRows + 2 * four;
+                const float sx = f[four * kRows + row], f0 = sx * fw[GLU ? 0 : g], f1 = GLU ? sx * fw[1] : f0;
+                if (four == 3 || kb + 1 == KB) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sempty(slot));
+                    ++group;
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(tempty(b));
-                    mbar_arrive(fempty(s));
+                const uint64_t ff[2] = {pack2(__float_as_uint(f0), __float_as_uint(f0)), pack2(__float_as_uint(f1), __float_as_uint(f1))};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    tmem_wait_ld();
+                    pin16(u[j & 1]);
+                    if (j < 7) {
+                        tmem_ld16(step_at(j + 1), u[(j + 1) & 1]);
+                    } else {
+                        tc_fence_before();           // the buffer is free: it is in registers
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(tempty(it & 1));
+                        ++it;
+                        if (kb + 1 < KB) {
+                            ok = lane_wait(done(it % ST), it / ST) && ok;
+                            tc_fence_after();
+                            tmem_ld16(step_at(0), u[0]);
+                        }
+                    }
+                    add16(&acc[j >> 1][8 * (j & 1)], u[j & 1], ff[j >> 1 & 1]);
                 }
             }
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
