@@ -528,7 +528,9 @@ cudaError_t launch_product(const ProductArgs &a, cudaStream_t s) {
     const uint64_t wd[4] = {K, N, parts, (uint64_t)a.E}, wst[3] = {K, N * K, parts * N * K};
     const uint32_t wbox[4] = {128, a.glu ? 128u : 256u, a.glu ? 2u : 1u, 1};
     if (!make_map_u8(&p.mw, a.w, 4, wd, wst, wbox)) return cudaErrorInvalidValue;
-    p.wide = a.out_stride % 8 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0;
+    const uint64_t row = (uint64_t)a.out_stride * (a.glu ? 1 : a.out_type == ENGRAM_T_F32 ? 4 : 2);
+    const uint64_t either = row | reinterpret_cast<uintptr_t>(a.out);
+    p.wide = either % 32 == 0 ? 2 : either % 16 == 0 ? 1 : 0;
     // Many rows: tiles of 128 rows and 256 weight rows, where they are enough for the SMs (shared memory bounds this kernel
     // at three times the MMA's time a block: 8192 x 4096 -> 6144 took 324 us with it).  Few rows an expert: a tile of few
     // rows leaves shared memory to the weights on their way.

@@ -22,7 +22,7 @@ struct Params {
     int m_tiles;                                     // of an expert
     int split;                                       // CTAs that share a tile
     int group;                                       // row tiles side by side
-    int wide;                                        // outputs may be written 16 bytes at a time
+    int wide;                                        // outputs may be written 16 (1) or 32 (2) bytes at a time
 };
 
 struct TileAt {
@@ -147,6 +147,11 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// 32 bytes, 32-byte aligned: a whole sector of L2.
+__device__ __forceinline__ void st32(void *p, const uint32_t (&u)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]) : "memory");
+}
 // Four scales from index i on, of which `left` exist, as they lie in memory: f32 bits, or bytes (packed in .x if vec).
 __device__ __forceinline__ uint4 load_scales(const void *p, int fmt, bool vec, int64_t i, int left) {
     uint4 r = make_uint4(0u, 0u, 0u, 0u);

@@ -49,7 +49,7 @@ __device__ __forceinline__ void add16(uint64_t *acc, const uint32_t (&u)[16], ui
 
 // 32 outputs of one row from column `col` on, of which `left` exist.
 template <class T>
-__device__ __forceinline__ void store32(void *out, int64_t at, const uint64_t (&acc)[16], int left, bool wide) {
+__device__ __forceinline__ void store32(void *out, int64_t at, const uint64_t (&acc)[16], int left, int wide) {
     if (left <= 0) return;
     T *o = static_cast<T *>(out) + at;
     if (wide && left >= 32) {
@@ -65,9 +65,17 @@ __device__ __forceinline__ void store32(void *out, int64_t at, const uint64_t (&
                 w[j] = sizeof(T) == 2 && std::is_same<T, __half>::value ? pack_f16x2(x, y) : pack_bf16x2(x, y);
             }
         }
+        if (wide == 2) {
 #pragma unroll
-        for (int j = 0; j < kWords; j += 4)
-            reinterpret_cast<uint4 *>(o)[j / 4] = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+            for (int j = 0; j < kWords; j += 8) {
+                const uint32_t u[8] = {w[j], w[j + 1], w[j + 2], w[j + 3], w[j + 4], w[j + 5], w[j + 6], w[j + 7]};
+                st32(reinterpret_cast<uint32_t *>(o) + j, u);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kWords; j += 4)
+                reinterpret_cast<uint4 *>(o)[j / 4] = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+        }
         return;
     }
 #pragma unroll
@@ -370,8 +378,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
                         c[j] = byte == 255u ? 0u : e4m3x4(x0 * inv, y0 * inv, x1 * inv, y1 * inv);
                     }
                     uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.out) + (int64_t)to * a.N + at);
-                    o[0] = make_uint4(c[0], c[1], c[2], c[3]);
-                    if (at + 16 < a.N) o[1] = make_uint4(c[4], c[5], c[6], c[7]);
+                    if (p.wide == 2) {               // n is a multiple of 32
+                        st32(o, c);
+                    } else {
+                        o[0] = make_uint4(c[0], c[1], c[2], c[3]);
+                        if (at + 16 < a.N) o[1] = make_uint4(c[4], c[5], c[6], c[7]);
+                    }
                 }
                 if (g == 0 && to >= 0) {
                     const int64_t i = (int64_t)to * p.NB + w.m0 / kM;
