@@ -1,35 +1,37 @@
 // route.cu -- tokens to experts (engram_route): scores, groups, the top_k, their
 // weights, and the lists of pairs by expert.
 //
-// A warp takes a token; lane l holds the experts l, l + 32, ...  A choice is the
-// largest key (a float's bits, ordered as integers) by one warp-wide maximum of
-// integers and the lowest index that has it by one minimum.  Scores are formed in 32 bits; where two that a choice
-// depends on lie closer than their error (kTol, about one row in a thousand of 256
-// sigmoid scores), the row is chosen again on scores in 64 bits.
+// A warp takes a token; lane l holds c = ceil(n_experts / 32) consecutive experts from l c on.  A
+// lane sorts its experts (up to eight) by their keys, a float's bits ordered as integers; a choice is the largest first key by one
+// warp-wide maximum of integers, the lowest lane that has it by a vote, and a step of that lane's list.  Groups that are a power of two
+// of lanes (8 groups of 256 experts: four) find their two largest all at once by exchanges.  Scores are formed in 32 bits;
+// where two that a choice depends on lie closer than their error (kTol, about one row in a thousand of 256
+// sigmoid scores), those in question are formed again in 64 bits, one a lane (all of a row's took its warp 15 us).
 //
 // Lists: counts of a block's experts, then positions from the counts of the blocks
 // before it (two kernels; one where a block takes all tokens).  A warp's tokens are consecutive and walked in order,
 // and a token's choices are different experts, so a counter an expert and warp needs no atomics and the lists
 // are in rising order.
 //
-// Bound by latency: one token is a chain of load, exponential and top_k + 1 maxima.
+// Bound by latency and instructions: one token is a chain of load, exponential and top_k + 1 maxima.
 #include "experts.cuh"
 
 namespace engram {
 
 namespace {
 
-constexpr int kWarps = 16, kThreads = kWarps * 32;
-constexpr int kOneBlock = 64;                        // tokens up to which one block does all
+constexpr int kOneBlock = 32;                        // tokens up to which one block does all
 constexpr int kBlocks = 152;                         // blocks at most of the others
 constexpr unsigned kAll = 0xFFFFFFFFu;
-// A 32-bit score is within 3e-7 max(1, |c|) of the 64-bit one: exp and the quotient are off by 2^-22 of s <= 1 at most,
-// the sum with the bias by 2^-24 |c|; a softmax adds 2^-24 |l - max| e^(l - max) <= 2^-25.  Two of them, and sums of two, differ by twice that.
+// A 32-bit score is within 4e-7 max(1, |c|) of the 64-bit one: exp and the quotient (2 ulp each, an addition) are off by
+// 5 x 2^-24 of s <= 1 at most, the sum with the bias by 2^-24 |c|; a softmax adds 2^-24 |l - max| e^(l - max) <= 2^-25.  Two of them, and sums of two, differ by twice that.
 constexpr float kTol = 1e-6f;
 
-int route_blocks(int tokens) {
+// Warps a block: 32 with 64 registers; rows of many experts take 16 with 128.
+int route_warps(int n_experts) { return n_experts <= 256 ? 32 : 16; }
+int route_blocks(int n_experts, int tokens) {
     if (tokens <= kOneBlock) return 1;
-    const int b = (tokens + kWarps - 1) / kWarps;
+    const int w = route_warps(n_experts) / 4, b = (tokens + w - 1) / w;   // a few tokens do not wait for each other in a warp
     return b < kBlocks ? b : kBlocks;
 }
 
@@ -65,105 +67,237 @@ template <class Key> struct Real;
 template <> struct Real<uint32_t> { using type = float; };
 template <> struct Real<uint64_t> { using type = double; };
 
-// Largest key of the warp and the lowest expert that has it (key 0: none left).
-template <class Key, int NV>
-__device__ __forceinline__ Key best_of(const Key (&key)[NV], int lane, int &e) {
-    Key m = 0;
-    int at = 0;
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-        if (key[v] > m) m = key[v], at = v;          // the lowest of equal ones
-    const Key top = warp_max(m);
-    e = (int)__reduce_min_sync(kAll, m == top ? (unsigned)(at * 32 + lane) : 0xFFFFFFFFu);
-    return top;
-}
-
 // Whether two scores that order experts e and f by their 32-bit values are too near to do so: not if they are equal for being
 // formed of the same numbers.
 __device__ __forceinline__ bool unsure(const RouteArgs &a, int64_t row, float x, float y, int e, int f) {
-    if (x - y > kTol * fmaxf(1.f, fabsf(x))) return false;
     return !(load_logit(a, row * a.stride + e) == load_logit(a, row * a.stride + f) && a.bias[e] == a.bias[f]);
 }
 
-// The row's choices from `key` (consumed), with `group` the values that order groups (without a bias and of two: the scores).
-// Lane j gets id j (-1: none).  CHECK: false where 32 bits leave a doubt.
-template <bool CHECK, class Key, int NV>
-__device__ __forceinline__ bool choose(const RouteArgs &a, int64_t row, Key (&key)[NV], const Key (&group)[NV], bool exact,
-                                       int lane, int &id) {
-    using T = typename Real<Key>::type;
-    const engram_router &r = a.r;
-    bool sure = true;
-    if (r.top_groups < r.n_groups) {
-        const int size = r.n_experts / r.n_groups;
-        Key mine = 0;                                // lane g: group g's sum
-        for (int g = 0; g < r.n_groups; ++g) {
-            const int lo = g * size, hi = lo + size;
-            Key in[NV];
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int e = v * 32 + lane;
-                in[v] = e >= lo && e < hi ? group[v] : Key(0);
-            }
-            int e;
-            const Key first = best_of(in, lane, e);
-            Key sum = first;
-            if (r.group_best == 2 && first) {
-#pragma unroll
-                for (int v = 0; v < NV; ++v)
-                    if (v * 32 + lane == e) in[v] = 0;
-                const Key second = best_of(in, lane, e);
-                if (second) sum = key_of(of_key(first) + of_key(second));
-            }
-            if (lane == g) mine = sum;
-        }
-        unsigned kept = 0;
-        T last = 0;
-        for (int i = 0; i <= r.top_groups; ++i) {
-            const Key top = warp_max(mine);
-            const int g = (int)__reduce_min_sync(kAll, mine == top ? (unsigned)lane : 0xFFFFFFFFu);
-            if (i == r.top_groups) {
-                // single logits and equal infinities need no care
-                if (CHECK && top && !(exact && r.group_best == 1) && last - of_key(top) <= (T)(2 * kTol) * fmax((T)1, fabs(last)))
-                    sure = false;
-                break;
-            }
-            if (!top) break;                         // masked groups alone are left
-            last = of_key(top);
-            kept |= 1u << g;
-            if (lane == g) mine = 0;
-        }
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if (!(kept >> min(31, (v * 32 + lane) / size) & 1)) key[v] = 0;
+// How lanes hold a row's experts, and groups their lanes.
+struct Shape {
+    int c;                              // experts a lane
+    int size;                           // experts a group
+    int lanes;                          // lanes a group where that is a power of two, else 0
+};
+__device__ __forceinline__ Shape shape_of(const engram_router &r) {
+    Shape s;
+    s.c = (r.n_experts + 31) / 32;
+    s.size = r.n_experts / r.n_groups;
+    s.lanes = s.size / s.c;
+    if (s.lanes * s.c != s.size || (s.lanes & (s.lanes - 1))) s.lanes = 0;
+    return s;
+}
+
+template <class Key>
+__device__ __forceinline__ void two_best(Key &first, Key &second, Key x, Key y) {   // of (first, second) and (x, y), both ordered
+    const Key low = first < x ? first : x;
+    first = first < x ? x : first;
+    second = second < y ? y : second;
+    second = second < low ? low : second;
+}
+
+template <class Key>
+__device__ __forceinline__ Key sum_of(int best, Key first, Key second) {
+    return best == 2 && second ? key_of(of_key(first) + of_key(second)) : first;
+}
+// The two largest of this warp's (first, second)s.
+template <class Key>
+__device__ __forceinline__ void two_best_of_lanes(Key &first, Key &second, int lanes) {
+    for (int o = 1; o < lanes; o <<= 1) {
+        const Key x = __shfl_xor_sync(kAll, first, o), y = __shfl_xor_sync(kAll, second, o);
+        two_best(first, second, x, y);
     }
+}
+// Groups that are no whole lanes: lane g gets group g's sum.
+template <class Key, int NV>
+__device__ __forceinline__ Key group_sums(const RouteArgs &a, const Shape &sh, const Key (&group)[NV], int lane) {
+    Key mine = 0;
+    for (int g = 0; g < a.r.n_groups; ++g) {
+        const int lo = g * sh.size - lane * sh.c, hi = lo + sh.size;   // of this lane's experts
+        Key first = 0, second = 0;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) two_best(first, second, v >= lo && v < hi ? group[v] : Key(0), Key(0));
+        two_best_of_lanes(first, second, 32);
+        if (lane == g) mine = sum_of(a.r.group_best, first, second);
+    }
+    return mine;
+}
+// The top_groups of the groups' sums `mine` (lane g: group g's).  CHECK: false in `sure` where 32 bits leave a doubt.
+template <bool CHECK, class Key>
+__device__ __forceinline__ unsigned keep_groups(const RouteArgs &a, Key mine, bool exact, int lane, bool &sure) {
+    using T = typename Real<Key>::type;
+    unsigned kept = 0;
+    T last = 0;
+    for (int i = 0; i <= a.r.top_groups; ++i) {
+        const Key top = warp_max(mine);
+        if (!top) break;                             // masked groups alone are left
+        if (i == a.r.top_groups) {
+            // logits alone are ordered exactly
+            if (CHECK && !(exact && a.r.group_best == 1) && last - of_key(top) <= (T)(2 * kTol) * fmax((T)1, fabs(last))) sure = false;
+            break;
+        }
+        const int g = __ffs(__ballot_sync(kAll, mine == top)) - 1;
+        last = of_key(top);
+        kept |= 1u << g;
+        mine = lane == g ? Key(0) : mine;
+    }
+    return kept;
+}
+template <class Key, int NV>
+__device__ __forceinline__ void mask_groups(const Shape &sh, unsigned kept, int lane, Key (&key)[NV]) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+        if (!(kept >> min(31, (lane * sh.c + v) / sh.size) & 1)) key[v] = 0;
+}
+
+// The top_k of the keys of which a lane's largest that is left is `m`, of its expert `at`; next(): the lane takes it out.  Lane j gets
+// id j (-1: none).  CHECK: false where 32 bits leave a doubt; `least` is the key behind the last choice.
+template <bool CHECK, class Key, class Next>
+__device__ __forceinline__ bool choose(const RouteArgs &a, const Shape &sh, int64_t row, Key &m, int &at, Next next, bool exact,
+                                       int lane, int &id, Key &least) {
+    using T = typename Real<Key>::type;
+    bool sure = true;
     id = -1;
     int before = -1;
     T last = 0;
-    for (int j = 0; j <= r.top_k; ++j) {
-        int e;
-        const Key top = best_of(key, lane, e);
+    for (int j = 0; j <= a.r.top_k; ++j) {
+        const Key top = warp_max(m);
         if (!top) break;
-        if (CHECK && !exact && before >= 0 && unsure(a, row, (float)last, (float)of_key(top), before, e)) sure = false;
-        if (j == r.top_k) break;
-        last = of_key(top);
+        least = top;
+        const T x = of_key(top);
+        const int from = __ffs(__ballot_sync(kAll, m == top)) - 1;   // lower lanes hold lower experts
+        const int e = __shfl_sync(kAll, lane * sh.c + at, from);
+        if (CHECK && !exact && before >= 0 && last - x <= (T)kTol * fmax((T)1, fabs(last)))
+            if (unsure(a, row, (float)last, (float)x, before, e)) sure = false;
+        if (j == a.r.top_k) break;
+        last = x;
         before = e;
-        if (lane == j) id = e;
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if (v * 32 + lane == e) key[v] = 0;
+        id = lane == j ? e : id;
+        next(lane == from);
     }
     return sure;
 }
+// The same on keys in registers, unsorted.
+template <bool CHECK, class Key, int NV>
+__device__ __forceinline__ bool choose_of(const RouteArgs &a, const Shape &sh, int64_t row, const Key (&key)[NV], bool exact, int lane,
+                                          int &id, Key &least) {
+    unsigned taken = 0;
+    int at = 0;
+    Key m = 0;
+    auto next = [&](bool mine) {
+        if (!mine) return;
+        taken |= 1u << at;
+        m = 0;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const Key x = taken >> v & 1 ? Key(0) : key[v];
+            if (x > m) m = x, at = v;                // the lowest of equal ones
+        }
+    };
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+        if (key[v] > m) m = key[v], at = v;
+    return choose<CHECK>(a, sh, row, m, at, next, exact, lane, id, least);
+}
 
-// The same on scores in 64 bits.
+// Up to 32 experts, marked in `want` bit by bit of a lane, to one a lane in rising order; -1 behind the last.  False: more.
+__device__ __forceinline__ bool one_a_lane(const Shape &sh, unsigned want, int lane, int &e) {
+    int upto = __popc(want);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kAll, upto, o);
+        if (lane >= o) upto += x;
+    }
+    const int total = __shfl_sync(kAll, upto, 31);
+    e = -1;
+    if (total > 32) return false;
+    for (int i = 0; i < total; ++i) {
+        // the lane whose marks reach past i
+        const int from = __ffs(__ballot_sync(kAll, upto > i)) - 1;
+        const int x = __shfl_sync(kAll, lane * sh.c + __ffs(want) - 1, from);
+        if (lane == i) e = x;
+        if (lane == from) want &= want - 1;
+    }
+    return true;
+}
+// c of expert e in 64 bits (p without a bias), softmax without its divisor: for rows whose order it does not change.
+__device__ __forceinline__ double score64(const RouteArgs &a, int64_t row, int e, float top) {
+    const double x = (double)load_logit(a, row * a.stride + e);
+    const double p = a.r.score == ENGRAM_SCORE_SOFTMAX ? exp(x - (double)top) : 1. / (1. + exp(-x));
+    return a.bias ? p + (double)a.bias[e] : p;
+}
+
+// Logits of token `row` as a lane holds them; -inf where there is no expert.  wide: NV of them lie side by side in aligned 16 bytes.
 template <int NV>
-__device__ __noinline__ void choose_again(const RouteArgs &a, int64_t row, int lane, int &id) {
-    uint64_t key[NV], group[NV];
+__device__ __forceinline__ void load_row(const RouteArgs &a, int c, bool wide, int64_t row, int lane, float (&l)[NV]) {
+    const int64_t at = row * a.stride + lane * c;
+    if (NV >= 4 && wide && a.type == ENGRAM_T_F32) {
+#pragma unroll
+        for (int v = 0; v + 3 < NV; v += 4) {
+            const float4 x = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(a.logits) + at + v));
+            l[v] = x.x, l[v + 1] = x.y, l[v + 2] = x.z, l[v + 3] = x.w;
+        }
+    } else if (NV >= 8 && wide) {
+#pragma unroll
+        for (int v = 0; v + 7 < NV; v += 8) {
+            float x[8];
+            const uint4 raw = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.logits) + at + v));
+            if (a.type == ENGRAM_T_BF16)
+                load8<ENGRAM_T_BF16>(&raw, 0, x);
+            else
+                load8<ENGRAM_T_F16>(&raw, 0, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) l[v + i] = x[i];
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            l[v] = v < c && lane * c + v < a.r.n_experts ? load_logit(a, at + v) : -INFINITY;
+    }
+}
+template <int NV>
+__device__ __forceinline__ bool wide_rows(const RouteArgs &a) {
+    const int size = a.type == ENGRAM_T_F32 ? 4 : 2;
+    return a.r.n_experts == 32 * NV && NV * size % 16 == 0 && a.stride * size % 16 == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0;
+}
+
+// s of a logit; top and sum: a softmax's.
+__device__ __forceinline__ float score32(bool soft, float x, float top, float sum) {
+    return soft ? __fdividef(expf(x - top), sum) : __fdividef(1.f, 1.f + expf(-x));
+}
+// The key of a logit (0 for a masked one), and of the value that orders groups.
+__device__ __forceinline__ uint32_t key32(const RouteArgs &a, bool soft, float l, float bias, float top, float sum) {
+    if (l == -INFINITY) return 0u;
+    return key_of(a.bias ? score32(soft, l, top, sum) + bias : l);
+}
+__device__ __forceinline__ uint32_t group_key32(const RouteArgs &a, bool soft, uint32_t key, float top, float sum) {
+    return !key || a.bias || a.r.group_best == 1 ? key : key_of(score32(soft, of_key(key), top, sum));
+}
+
+// What follows is called for about one row in a thousand; it forms the row's numbers anew, so that they stay in registers elsewhere.
+// The 32-bit keys of row `row`.
+template <int NV>
+__device__ __forceinline__ void keys_again(const RouteArgs &a, const Shape &sh, int64_t row, int lane, float top, float sum,
+                                           uint32_t (&key)[NV]) {
+    const bool soft = a.r.score == ENGRAM_SCORE_SOFTMAX;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int e = lane * sh.c + v;
+        const bool real = v < sh.c && e < a.r.n_experts;
+        const float l = real ? load_logit(a, row * a.stride + e) : -INFINITY;
+        key[v] = l == l ? key32(a, soft, l, real && a.bias ? a.bias[e] : 0.f, top, sum) : 0u;
+    }
+}
+// The row's choices on all its scores in 64 bits.
+template <int NV>
+__device__ __noinline__ int choose_all(const RouteArgs &a, int64_t row, int lane) {
+    const Shape sh = shape_of(a.r);
+    uint64_t key[NV], group[NV], least = 0;
     double s[NV], top = -INFINITY, sum = 0;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        const int e = v * 32 + lane;
-        s[v] = e < a.r.n_experts ? (double)load_logit(a, row * a.stride + e) : -INFINITY;
+        const int e = lane * sh.c + v;
+        s[v] = v < sh.c && e < a.r.n_experts ? (double)load_logit(a, row * a.stride + e) : -INFINITY;
         if (s[v] != s[v]) s[v] = -INFINITY;
         top = fmax(top, s[v]);
     }
@@ -178,60 +312,177 @@ __device__ __noinline__ void choose_again(const RouteArgs &a, int64_t row, int l
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        const int e = v * 32 + lane;
         const bool masked = s[v] == -INFINITY;
         const double p = soft ? exp(s[v] - top) / sum : 1. / (1. + exp(-s[v]));
-        key[v] = masked ? 0 : key_of(a.bias ? p + (double)a.bias[e] : s[v]);
+        key[v] = masked ? 0 : key_of(a.bias ? p + (double)a.bias[lane * sh.c + v] : s[v]);
         group[v] = masked ? 0 : a.bias || a.r.group_best == 1 ? key[v] : key_of(p);
     }
-    choose<false>(a, row, key, group, true, lane, id);
+    bool sure = true;
+    int id;
+    if (a.r.top_groups < a.r.n_groups)
+        mask_groups(sh, keep_groups<false>(a, group_sums(a, sh, group, lane), true, lane, sure), lane, key);
+    choose_of<false>(a, sh, row, key, true, lane, id, least);
+    return id;
+}
+// The groups that stay, by 64-bit scores of each group's experts that may be among its two largest.  0: too many of them.
+template <int NV>
+__device__ __noinline__ unsigned groups_again(const RouteArgs &a, int64_t row, int lane, float top, float sum) {
+    const Shape sh = shape_of(a.r);
+    const engram_router &r = a.r;
+    uint32_t key[NV];
+    keys_again(a, sh, row, lane, top, sum, key);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) key[v] = group_key32(a, r.score == ENGRAM_SCORE_SOFTMAX, key[v], top, sum);
+    unsigned want = 0;
+    for (int g = 0; g < r.n_groups; ++g) {
+        const int lo = g * sh.size - lane * sh.c, hi = lo + sh.size;
+        uint32_t first = 0, second = 0;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) two_best(first, second, v >= lo && v < hi ? key[v] : 0u, 0u);
+        two_best_of_lanes(first, second, 32);
+        const uint32_t low = second && r.group_best == 2 ? second : first;
+        if (!low) continue;
+        const float x = of_key(low), from = x - kTol * fmaxf(1.f, fabsf(x));
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            if (v >= lo && v < hi && key[v] && of_key(key[v]) >= from) want |= 1u << v;
+    }
+    int e;
+    if (!one_a_lane(sh, want, lane, e)) return 0;
+    const uint64_t mine = e >= 0 ? key_of(score64(a, row, e, top)) : 0;
+    uint64_t sums = 0;                               // lane g: group g's
+    for (int g = 0; g < r.n_groups; ++g) {
+        uint64_t x = e >= 0 && e / sh.size == g ? mine : 0;
+        const uint64_t first = warp_max(x);
+        if (lane == __ffs(__ballot_sync(kAll, x == first)) - 1) x = 0;
+        const uint64_t second = warp_max(x);
+        if (lane == g) sums = sum_of(r.group_best, first, second);
+    }
+    bool sure = true;
+    return keep_groups<false>(a, sums, true, lane, sure);
+}
+// The choices among the groups `kept`, by 64-bit scores of the experts that may be among them: from `least`, the 32-bit key behind the
+// last choice, on.  -2: too many.
+template <int NV>
+__device__ __noinline__ int experts_again(const RouteArgs &a, int64_t row, int lane, float top, float sum, unsigned kept, uint32_t least) {
+    const Shape sh = shape_of(a.r);
+    uint32_t key[NV];
+    keys_again(a, sh, row, lane, top, sum, key);
+    if (a.r.top_groups < a.r.n_groups) mask_groups(sh, kept, lane, key);
+    const float x = of_key(least), from = x - kTol * fmaxf(1.f, fabsf(x));
+    unsigned want = 0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+        if (key[v] && of_key(key[v]) >= from) want |= 1u << v;
+    int e, id = -1;
+    if (!one_a_lane(sh, want, lane, e)) return -2;
+    uint64_t mine = e >= 0 ? key_of(score64(a, row, e, top)) : 0;
+    for (int j = 0; j < a.r.top_k; ++j) {
+        const uint64_t most = warp_max(mine);
+        if (!most) break;
+        const int g = __ffs(__ballot_sync(kAll, mine == most)) - 1, f = __shfl_sync(kAll, e, g);
+        if (lane == j) id = f;
+        if (lane == g) mine = 0;
+    }
+    return id;
 }
 
-// Token `row`: its ids and weights, one choice a lane.
+// A lane's keys with their places (the lower the larger), in falling order: an odd-even merge of powers of two.
 template <int NV>
-__device__ __forceinline__ int route_row(const RouteArgs &a, int64_t row, int lane) {
-    const engram_router &r = a.r;
-    const bool soft = r.score == ENGRAM_SCORE_SOFTMAX;
-    float l[NV], top = -INFINITY, sum = 0.f;
-    bool nan = false;
+__device__ __forceinline__ void sort_falling(uint64_t (&s)[NV]) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int e = v * 32 + lane;
-        l[v] = e < r.n_experts ? load_logit(a, row * a.stride + e) : -INFINITY;
-    }
+    for (int p = 1; p < NV; p <<= 1)
+#pragma unroll
+        for (int k = p; k > 0; k >>= 1)
+#pragma unroll
+            for (int j = k % p; j + k < NV; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < NV && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const uint64_t x = s[i + j], y = s[i + j + k];
+                        const bool swap = x < y;
+                        s[i + j] = swap ? y : x;
+                        s[i + j + k] = swap ? x : y;
+                    }
+}
+
+// Token `row` with the logits l: its ids and weights, one choice a lane.
+template <int NV>
+__device__ __forceinline__ int route_row(const RouteArgs &a, const Shape &sh, const float (&bias)[NV], float (&l)[NV], int64_t row,
+                                         int lane) {
+    const engram_router &r = a.r;
+    const bool soft = r.score == ENGRAM_SCORE_SOFTMAX, grouped = r.top_groups < r.n_groups, exact = !a.bias;
+    float top = -INFINITY, sum = 0.f;
+    bool nan = false;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         nan |= l[v] != l[v] || (soft && l[v] == INFINITY);
         if (l[v] != l[v]) l[v] = -INFINITY;
-        top = fmaxf(top, l[v]);
     }
     nan = __any_sync(kAll, nan);
     if (soft) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) top = fmaxf(top, l[v]);
         top = of_key(__reduce_max_sync(kAll, key_of(top)));
 #pragma unroll
         for (int v = 0; v < NV; ++v) sum += l[v] == -INFINITY ? 0.f : expf(l[v] - top);
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
     }
-    const bool scores = a.bias || (r.top_groups < r.n_groups && r.group_best == 2);
-    uint32_t key[NV], group[NV];
+    uint32_t key[NV], least = 0;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int e = v * 32 + lane;
-        const bool masked = l[v] == -INFINITY;
-        float p = 0.f;
-        if (scores && !masked) p = soft ? expf(l[v] - top) / sum : 1.f / (1.f + expf(-l[v]));
-        key[v] = masked ? 0u : key_of(a.bias ? p + __ldg(a.bias + e) : l[v]);
-        group[v] = masked ? 0u : a.bias || r.group_best == 1 ? key[v] : key_of(p);
+    for (int v = 0; v < NV; ++v) key[v] = key32(a, soft, l[v], bias[v], top, sum);
+    // a softmax beside a bias needs its divisor in 64 bits, too: all scores
+    bool all = false, sure = true;
+    unsigned kept = 0xFFFFFFFFu;
+    auto settle_groups = [&](uint32_t mine) {
+        kept = keep_groups<true>(a, mine, exact, lane, sure);
+        if (!sure) all = (soft && a.bias) || !(kept = groups_again<NV>(a, row, lane, top, sum));
+    };
+    if (grouped && (!sh.lanes || NV > 8)) {
+        uint32_t group[NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) group[v] = group_key32(a, soft, key[v], top, sum);
+        settle_groups(group_sums(a, sh, group, lane));
+        mask_groups(sh, kept, lane, key);
     }
     int id;
-    // a row with infinite scores that are equal is as sure as another (a NaN of inf - inf)
-    if (!choose<true>(a, row, key, group, !a.bias, lane, id)) choose_again<NV>(a, row, lane, id);
-    float s = 0.f;
-    if (id >= 0) {
-        const float x = load_logit(a, row * a.stride + id);
-        s = soft ? expf(x - top) / sum : 1.f / (1.f + expf(-x));
+    bool chosen;
+    if (NV <= 8) {
+        uint64_t s[NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) s[v] = (uint64_t)key[v] << 32 | (uint32_t)(NV - 1 - v);
+        sort_falling(s);
+        if (grouped && sh.lanes) {
+            uint32_t first = group_key32(a, soft, (uint32_t)(s[0] >> 32), top, sum);
+            uint32_t second = NV > 1 ? group_key32(a, soft, (uint32_t)(s[NV > 1] >> 32), top, sum) : 0u;
+            two_best_of_lanes(first, second, sh.lanes);
+            const uint32_t mine = __shfl_sync(kAll, sum_of(r.group_best, first, second), lane * sh.lanes & 31);
+            settle_groups(lane < r.n_groups ? mine : 0u);
+            const bool out = !(kept >> min(31, lane / sh.lanes) & 1);
+#pragma unroll
+            for (int v = 0; v < NV; ++v) s[v] = out ? 0 : s[v];
+        }
+        uint32_t m = (uint32_t)(s[0] >> 32);
+        int at = NV - 1 - (int)(uint32_t)s[0];
+        auto next = [&](bool mine) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) s[v] = mine ? v + 1 < NV ? s[(v + 1) % NV] : 0 : s[v];
+            m = (uint32_t)(s[0] >> 32);
+            at = NV - 1 - (int)(uint32_t)s[0];
+        };
+        chosen = choose<true>(a, sh, row, m, at, next, exact, lane, id, least);
+    } else {
+        chosen = choose_of<true>(a, sh, row, key, exact, lane, id, least);
     }
+    if (!chosen && !all) {
+        if (soft)
+            all = true;
+        else
+            all = (id = experts_again<NV>(a, row, lane, top, sum, kept, least)) == -2;
+    }
+    if (all) id = choose_all<NV>(a, row, lane);
+    float s = id >= 0 ? score32(soft, load_logit(a, row * a.stride + id), top, sum) : 0.f;
     if (r.renormalise) {
         float t = s;
 #pragma unroll
@@ -247,16 +498,17 @@ __device__ __forceinline__ int route_row(const RouteArgs &a, int64_t row, int la
 
 // Tokens of warp `w` of block b.
 __device__ __forceinline__ void warp_tokens(const RouteArgs &a, int b, int blocks, int w, int64_t &lo, int64_t &hi) {
-    const int64_t n = (int64_t)blocks * kWarps, i = (int64_t)b * kWarps + w;
+    const int warps = blockDim.x >> 5;
+    const int64_t n = (int64_t)blocks * warps, i = (int64_t)b * warps + w;
     lo = a.tokens * i / n;
     hi = a.tokens * (i + 1) / n;
 }
 
 // Exclusive sums over `n` values of v[], all threads of the block; v[n] gets the total.  part: 32 ints.
 __device__ __forceinline__ void block_scan(int *v, int n, int *part) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     int carry = 0;
-    for (int i0 = 0; i0 < n; i0 += kThreads) {
+    for (int i0 = 0; i0 < n; i0 += (int)blockDim.x) {
         const int i = i0 + tid, x = i < n ? v[i] : 0;
         int s = x;
 #pragma unroll
@@ -267,7 +519,7 @@ __device__ __forceinline__ void block_scan(int *v, int n, int *part) {
         if (lane == 31) part[warp] = s;
         __syncthreads();
         int before = carry, total = carry;
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < warps; ++w) {
             if (w < warp) before += part[w];
             total += part[w];
         }
@@ -285,13 +537,13 @@ __device__ __forceinline__ void count_row(const RouteArgs &a, int *mine, int id,
     __syncwarp();
 }
 
-// counts: [kWarps][E] of the block's warps, turned into the first position of each; first: position of the block's first pair
+// counts: [warps][E] of the block's warps, turned into the first position of each; first: position of the block's first pair
 // of each expert.  Then the warp's pairs to their places.
 __device__ __forceinline__ void place_pairs(const RouteArgs &a, int *counts, const int *first, int64_t lo, int64_t hi) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.r.n_experts, k = a.r.top_k;
-    for (int e = tid; e < E; e += kThreads) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, E = a.r.n_experts, k = a.r.top_k;
+    for (int e = tid; e < E; e += blockDim.x) {
         int at = first[e];
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < warps; ++w) {
             const int n = counts[w * E + e];
             counts[w * E + e] = at;
             at += n;
@@ -308,73 +560,89 @@ __device__ __forceinline__ void place_pairs(const RouteArgs &a, int *counts, con
 
 // One block: everything.  Several: ids, weights and the block's counts (ws).
 template <int NV>
-__global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(NV <= 8 ? 1024 : 512) route_kernel(const __grid_constant__ RouteArgs a) {
     extern __shared__ int smem[];
     __shared__ int part[32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.r.n_experts;
-    int *counts = smem, *mine = counts + warp * E, *first = counts + kWarps * E;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, E = a.r.n_experts;
+    int *counts = smem, *mine = counts + warp * E, *first = counts + warps * E;
     int64_t lo, hi;
     warp_tokens(a, blockIdx.x, gridDim.x, warp, lo, hi);
     if (a.offsets)
         for (int e = lane; e < E; e += 32) mine[e] = 0;
     __syncwarp();
+    const Shape sh = shape_of(a.r);
+    const bool wide = wide_rows<NV>(a);
+    float bias[NV], next[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+        bias[v] = a.bias && v < sh.c && lane * sh.c + v < E ? __ldg(a.bias + lane * sh.c + v) : 0.f;
+    if (lo < hi) load_row<NV>(a, sh.c, wide, lo, lane, next);
     for (int64_t t = lo; t < hi; ++t) {
-        const int id = route_row<NV>(a, t, lane);
+        float l[NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) l[v] = next[v];
+        if (t + 1 < hi) load_row<NV>(a, sh.c, wide, t + 1, lane, next);
+        const int id = route_row<NV>(a, sh, bias, l, t, lane);
         if (a.offsets) count_row(a, mine, id, lane);
     }
     if (!a.offsets) return;
     __syncthreads();
     if (gridDim.x > 1) {
-        for (int e = tid; e < E; e += kThreads) {
+        for (int e = tid; e < E; e += blockDim.x) {
             int n = 0;
-            for (int w = 0; w < kWarps; ++w) n += counts[w * E + e];
+            for (int w = 0; w < warps; ++w) n += counts[w * E + e];
             a.ws[(int64_t)blockIdx.x * E + e] = n;
         }
         return;
     }
-    for (int e = tid; e < E; e += kThreads) {
+    for (int e = tid; e < E; e += blockDim.x) {
         int n = 0;
-        for (int w = 0; w < kWarps; ++w) n += counts[w * E + e];
+        for (int w = 0; w < warps; ++w) n += counts[w * E + e];
         first[e] = n;
     }
     __syncthreads();
     block_scan(first, E, part);
-    for (int e = tid; e <= E; e += kThreads) a.offsets[e] = first[e];
+    for (int e = tid; e <= E; e += blockDim.x) a.offsets[e] = first[e];
     place_pairs(a, counts, first, lo, hi);
 }
 
-__global__ void __launch_bounds__(kThreads) route_lists_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(1024) route_lists_kernel(const RouteArgs a) {
     extern __shared__ int smem[];
     __shared__ int part[32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = a.r.n_experts, k = a.r.top_k;
-    int *counts = smem, *mine = counts + warp * E, *first = counts + kWarps * E, *before = first + E + 1;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, E = a.r.n_experts, k = a.r.top_k;
+    int *counts = smem, *mine = counts + warp * E, *first = counts + warps * E, *before = first + E + 1;
     int64_t lo, hi;
     warp_tokens(a, blockIdx.x, gridDim.x, warp, lo, hi);
     for (int e = lane; e < E; e += 32) mine[e] = 0;
-    __syncwarp();
-    for (int64_t t = lo; t < hi; ++t) count_row(a, mine, lane < k ? a.ids[t * k + lane] : -1, lane);
-    for (int e = tid; e < E; e += kThreads) {
+    for (int e = tid; e < E; e += blockDim.x) first[e] = before[e] = 0;
+    __syncthreads();
+    griddep_wait();
+    // the blocks' counts of an expert, by as many threads as there are for each
+    const int parts = max(1, (int)blockDim.x / E), blocks = gridDim.x;
+    for (int i = tid; i < parts * E; i += blockDim.x) {
+        const int e = i % E, part_no = i / E;
         int n = 0, sum = 0;
 #pragma unroll 8
-        for (int b = 0; b < (int)gridDim.x; ++b) {
+        for (int b = blocks * part_no / parts; b < blocks * (part_no + 1) / parts; ++b) {
             const int c = a.ws[(int64_t)b * E + e];
             n += b < (int)blockIdx.x ? c : 0;
             sum += c;
         }
-        first[e] = sum;
-        before[e] = n;
+        atomicAdd(first + e, sum);                   // whole numbers: in any order
+        atomicAdd(before + e, n);
     }
+    for (int64_t t = lo; t < hi; ++t) count_row(a, mine, lane < k ? a.ids[t * k + lane] : -1, lane);
     __syncthreads();
     block_scan(first, E, part);
     if (blockIdx.x == 0)
-        for (int e = tid; e <= E; e += kThreads) a.offsets[e] = first[e];
+        for (int e = tid; e <= E; e += blockDim.x) a.offsets[e] = first[e];
     __syncthreads();
-    for (int e = tid; e < E; e += kThreads) first[e] += before[e];
+    for (int e = tid; e < E; e += blockDim.x) first[e] += before[e];
     __syncthreads();
     place_pairs(a, counts, first, lo, hi);
 }
 
-constexpr size_t smem_bytes(int E) { return ((size_t)(kWarps + 2) * E + 2) * sizeof(int); }
+size_t smem_bytes(int E, int warps) { return ((size_t)(warps + 2) * E + 2) * sizeof(int); }
 
 // Once a device: dynamic shared memory for the most experts.
 cudaError_t allow_smem(void (*kernel)(const RouteArgs), bool (&done)[64]) {
@@ -382,49 +650,59 @@ cudaError_t allow_smem(void (*kernel)(const RouteArgs), bool (&done)[64]) {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (done[dev]) return cudaSuccess;
     const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(kMaxExperts));
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(kMaxExperts, 32));
     done[dev] = e == cudaSuccess;
     return e;
 }
 
 template <int NV>
-cudaError_t launch_rows(const RouteArgs &a, int blocks, size_t smem, cudaStream_t s) {
+cudaError_t launch_rows(const RouteArgs &a, int blocks, int warps, cudaStream_t s) {
     static bool wide[64] = {};
     const cudaError_t e = allow_smem(route_kernel<NV>, wide);
     if (e != cudaSuccess) return e;
-    route_kernel<NV><<<blocks, kThreads, smem, s>>>(a);
+    route_kernel<NV><<<blocks, 32 * warps, a.offsets ? smem_bytes(a.r.n_experts, warps) : 0, s>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t route_workspace_ints(int n_experts, int tokens) {
-    const int b = route_blocks(tokens);
+    const int b = route_blocks(n_experts, tokens);
     return b > 1 ? (size_t)b * n_experts : 0;
 }
 
 cudaError_t launch_route(const RouteArgs &a, cudaStream_t s) {
-    const int blocks = route_blocks(a.tokens), E = a.r.n_experts;
-    const size_t smem = smem_bytes(E);
+    const int E = a.r.n_experts, blocks = route_blocks(E, a.tokens);
+    // no more warps than tokens, but the eight that make short work of the lists
+    const int most = route_warps(E), each = (a.tokens + blocks - 1) / blocks, warps = each > most ? most : each < 8 ? 8 : each;
     cudaError_t e;
     if (E <= 32)
-        e = launch_rows<1>(a, blocks, smem, s);
+        e = launch_rows<1>(a, blocks, warps, s);
     else if (E <= 64)
-        e = launch_rows<2>(a, blocks, smem, s);
+        e = launch_rows<2>(a, blocks, warps, s);
     else if (E <= 128)
-        e = launch_rows<4>(a, blocks, smem, s);
+        e = launch_rows<4>(a, blocks, warps, s);
     else if (E <= 256)
-        e = launch_rows<8>(a, blocks, smem, s);
+        e = launch_rows<8>(a, blocks, warps, s);
     else if (E <= 512)
-        e = launch_rows<16>(a, blocks, smem, s);
+        e = launch_rows<16>(a, blocks, warps, s);
     else
-        e = launch_rows<32>(a, blocks, smem, s);
+        e = launch_rows<32>(a, blocks, warps, s);
     if (e != cudaSuccess || blocks == 1 || !a.offsets) return e;
     static bool wide[64] = {};
     e = allow_smem(route_lists_kernel, wide);
     if (e != cudaSuccess) return e;
-    route_lists_kernel<<<blocks, kThreads, smem, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(32 * warps);
+    cfg.dynamicSmemBytes = smem_bytes(E, warps);
+    cfg.stream = s;
+    cudaLaunchAttribute la[1];
+    la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    la[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = la;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, route_lists_kernel, a);
 }
 
 }  // namespace engram
