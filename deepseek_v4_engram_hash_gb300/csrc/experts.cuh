@@ -51,7 +51,8 @@ struct CombineArgs {
     void *out;
     int64_t y_stride, add_stride, out_stride;
     int32_t y_type, add_type, out_type, tokens, top_k, dim;
+    uint32_t blocks;                    // set by the launcher
 };
-cudaError_t launch_combine(const CombineArgs &a, cudaStream_t s);
+cudaError_t launch_combine(CombineArgs a, cudaStream_t s);
 
 }  // namespace engram
