@@ -16,6 +16,9 @@
 //                takes four warps 290 clocks, one warp 690; as tile::gather4 2200 to 2900);
 //   warps 8..15  take a block's sums into their f32 accumulators (thread: a row, 128 columns,
 //                for glu 64 of each part; 128 KB of them in about 300 clocks); at the end of a tile they write it.
+// Where both scales are powers of two (e8m0 bytes) the tensor cores apply them: tcgen05.mma kind::mxf8f6f4 with a
+// block's bytes in tensor memory (four blocks to a 32-bit column; an MMA names its byte).  Sums then stay in tensor memory over
+// all of K, in one 256-column buffer, and the last warps take them once a tile.
 // Waits are bounded as in product.cu.
 #include "product.cuh"
 
@@ -33,11 +36,15 @@ constexpr uint32_t kStage = 3 * kTileA;              // x, then the weights
 constexpr int kStages = 4;
 // Scales of four blocks at a time (the last of a tile: what is left), [4][128] of rows and [4][2] of weights.
 constexpr int kSlots = 3;
-constexpr uint32_t kSlotBytes = 4 * kRows * 4 + 4 * 2 * 4;
-constexpr uint32_t oScale = kStages * kStage;
+constexpr uint32_t kSlotBytes = 4 * kRows * 4 + 128;
+// For the tensor cores: a 32-bit word (a byte a block) for each row of x and weight row, 32 x 4 of them an image of 512 bytes.
+constexpr uint32_t kImage = 512, kScaleCols = 16;         // tensor-memory columns of a group of four blocks: 4 of rows, 8 of weights
+constexpr uint32_t kScaleTmem = kCols;                    // behind the sums
+static_assert(3 * kImage <= kSlotBytes, "images in a slot of scales");
+constexpr uint32_t oScale = kStages * kStage;             // a multiple of 16
 constexpr uint32_t oMax = oScale + kSlots * kSlotBytes;   // glu: [2][2 groups][128] f32 bits
 constexpr uint32_t oBar = oMax + 2 * 2 * kRows * 4;
-constexpr uint32_t oFlag = oBar + 8 * (2 * kStages + 2 + 2 + 2 * kSlots);
+constexpr uint32_t oFlag = oBar + 8 * (2 * kStages + 2 + 2 + 2 * kSlots + 1);
 constexpr uint32_t oLists = oFlag + 16;
 constexpr size_t smem_bytes(int E) { return 1024 + oLists + (3 * (size_t)E + 1) * 4; }
 
@@ -87,7 +94,35 @@ __device__ __forceinline__ void store32(void *out, int64_t at, const uint64_t (&
     }
 }
 
-template <bool GLU>
+// kind::mxf8f6f4: scales of A and B in tensor memory, power-of-two bytes (bit 23); which byte of a column's four in bits 29.. and 4...
+__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t sa, uint32_t sb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d), "l"(da), "l"(db), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t idesc_mx(int N, uint32_t byte) {
+    return (byte << 4) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | (1u << 27) | (byte << 29);
+}
+// An image of 32 rows of 16 bytes to 4 columns of all lanes.  Its descriptor: no swizzle, groups of 8 rows 128 bytes apart.
+__device__ __forceinline__ void copy_image(uint32_t taddr, uint32_t saddr) {
+    const uint64_t desc = (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)1u << 16 | (uint64_t)(128u >> 4) << 32 | (uint64_t)1u << 46;
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// Four bytes of scales from index i on, of which `left` exist (others: 1).
+__device__ __forceinline__ uint32_t four_bytes(const void *p, bool vec, int64_t i, int left) {
+    const uint8_t *b = static_cast<const uint8_t *>(p) + i;
+    if (vec) return __ldg(reinterpret_cast<const uint32_t *>(b));
+    uint32_t r = 0x7F7F7F00u | __ldg(b);
+    if (left > 1) r = (r & 0xFFFF00FFu) | (uint32_t)__ldg(b + 1) << 8;
+    if (left > 2) r = (r & 0xFF00FFFFu) | (uint32_t)__ldg(b + 2) << 16;
+    if (left > 3) r = (r & 0x00FFFFFFu) | (uint32_t)__ldg(b + 3) << 24;
+    return r;
+}
+
+template <bool GLU, bool MX>
 __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_constant__ Params p) {
     constexpr int ST = kStages;
     extern __shared__ uint8_t smem_raw[];
@@ -102,6 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
     const uint32_t together = drain + 8;
     auto sfull = [&](int i) { return together + 8u * (1 + i); };
     auto sempty = [&](int i) { return together + 8u * (1 + kSlots + i); };
+    const uint32_t sums_ready = together + 8u * (1 + 2 * kSlots);
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + oFlag);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + oFlag + 4);
     int *first = reinterpret_cast<int *>(smem + oLists), *count = first + a.E, *before = count + a.E;
@@ -120,8 +156,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
         mbar_init(together, kEpiWarps);
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(sfull(i), 2);
-            mbar_init(sempty(i), kEpiWarps);
+            mbar_init(sempty(i), MX ? 1 : kEpiWarps);
         }
+        mbar_init(sums_ready, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -175,10 +212,44 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
     } else if (warp == 1) {
         // ---- MMA ----
         // (After a wait that ran out, what it issues reads anything and goes to sums that nobody writes.)
-        uint32_t it = 0;
+        uint32_t it = 0, group = 0, turn = 0;
         bool ok = true;
         const uint64_t desc = sdesc(base);
-        for (int t = t0; t < tiles && ok; t += t_step) {
+        for (int t = t0; MX && t < tiles && ok; t += t_step, ++turn) {
+            const int N = two(tile_at(t)) ? kCols : kM;
+            if (!lane_wait(tempty(0), turn ^ 1)) ok = false;
+            for (int kb = 0; kb < KB; ++kb, ++it) {
+                const int s = it % ST, slot = group % kSlots, byte = kb & 3;
+                const uint32_t sa = tmem + kScaleTmem + (group & 1) * kScaleCols, sb = sa + 4;
+                const uint64_t da = desc + s * (kStage >> 4), db = da + (kTileA >> 4);
+                if (!byte) {
+                    if (!lane_wait(sfull(slot), group / kSlots)) ok = false;
+                    tc_fence_after();
+                    if (elect()) {
+                        const uint32_t image = base + oScale + slot * kSlotBytes;
+                        copy_image(sa, image);
+                        copy_image(sb, image + kImage);
+                        copy_image(sb + 4, image + 2 * kImage);
+                        commit(sempty(slot));
+                    }
+                    __syncwarp();
+                }
+                if (byte == 3) ++group;
+                const uint32_t idesc = idesc_mx(N, byte);
+                if (!lane_wait(full(s), it / ST)) ok = false;
+                tc_fence_after();
+                if (elect()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mma_mx(tmem, da + 2u * k, db + 2u * k, idesc, sa, sb, kb | k);
+                    commit(done(s));
+                    if (kb + 1 == KB) commit(sums_ready);
+                }
+                __syncwarp();
+            }
+            if (KB & 3) ++group;
+            ok = __all_sync(0xFFFFFFFFu, ok);
+        }
+        for (int t = t0; !MX && t < tiles && ok; t += t_step) {
             const uint32_t idesc = idesc_f8(two(tile_at(t)) ? kCols : kM);
             for (int kb = 0; kb < KB; ++kb, ++it) {
                 const int s = it % ST;
@@ -219,6 +290,41 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
                 xi[v] = c < w.n ? gather ? token_of(a, w.row + c) : w.row + c : -1;
             }
             const int64_t w0 = ((int64_t)w.e * (GLU ? 2 : 1) * p.NB + w.m0 / kM) * KB, w1 = w0 + (int64_t)(GLU ? p.NB : 1) * KB;
+            if (MX) {
+                // this warp's images: rows of x (0 is 2^-127: rows behind the last have 1), or the two blocks of weight rows
+                int r4[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = i * 32 + lane;
+                    r4[i] = warp == kScaleWarp && c < w.n ? gather ? token_of(a, w.row + c) : w.row + c : -1;
+                }
+                for (int kb4 = 0; kb4 < KB; kb4 += 4, ++it) {
+                    const int left = KB - kb4, slot = it % kSlots;
+                    uint4 u = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                    uint32_t b0 = 0, b1 = 0;
+                    if (warp == kScaleWarp) {
+                        if (r4[0] >= 0) u.x = four_bytes(a.x_scales, vec_x, (int64_t)r4[0] * KB + kb4, left);
+                        if (r4[1] >= 0) u.y = four_bytes(a.x_scales, vec_x, (int64_t)r4[1] * KB + kb4, left);
+                        if (r4[2] >= 0) u.z = four_bytes(a.x_scales, vec_x, (int64_t)r4[2] * KB + kb4, left);
+                        if (r4[3] >= 0) u.w = four_bytes(a.x_scales, vec_x, (int64_t)r4[3] * KB + kb4, left);
+                    } else {
+                        b0 = four_bytes(a.w_scales, vec_w, w0 + kb4, left);
+                        b1 = both ? four_bytes(a.w_scales, vec_w, w1 + kb4, left) : b0;
+                    }
+                    if (!(ok = wait(sempty(slot), it / kSlots ^ 1))) break;
+                    uint4 *image = reinterpret_cast<uint4 *>(smem + oScale + slot * kSlotBytes) + lane;
+                    if (warp == kScaleWarp) {
+                        image[0] = u;
+                    } else {
+                        image[kImage / 16] = make_uint4(b0, b0, b0, b0);
+                        image[2 * kImage / 16] = make_uint4(b1, b1, b1, b1);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sfull(slot));
+                }
+                continue;
+            }
             // the next four blocks' scales are on their way while these are written
             uint4 next_x[2], next_w[2];
             auto fetch = [&](int kb4) {
@@ -304,6 +410,20 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 16; ++j) acc[i][j] = 0;
+            if (MX) {
+                ok = lane_wait(sums_ready, turn) && ok;
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t u[32];
+                    tmem_ld32(lanes + column(i), u);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) acc[i][j] = pack2(u[2 * j], u[2 * j + 1]);
+                }
+                tc_fence_before();                   // the buffer is free: it is in registers
+                __syncwarp();
+                if (lane == 0) mbar_arrive(tempty(0));
+            } else {
             // Steps of 16 columns: while one is added up the next is on its way from tensor memory, over the end of a block, too.
             // Columns without weight rows are added up as well, nobody writes their sums: a test of them for every step
             // took a block to 1100 clocks.
@@ -343,9 +463,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
                     add16(&acc[j >> 1][8 * (j & 1)], u[j & 1], ff[j >> 1 & 1]);
                 }
             }
+            }
+            ++turn;
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             if (GLU) {
-                uint32_t *amax = reinterpret_cast<uint32_t *>(smem + oMax) + (turn++ & 1) * 2 * kRows + row;
+                uint32_t *amax = reinterpret_cast<uint32_t *>(smem + oMax) + (turn & 1) * 2 * kRows + row;
                 float big = 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; i += 2)
@@ -415,14 +537,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-template <bool GLU>
+template <bool GLU, bool MX>
 cudaError_t launch(Params &p, cudaStream_t s) {
     const ProductArgs &a = p.a;
     static bool attr[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!attr[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(product_rows_kernel<GLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t e = cudaFuncSetAttribute(product_rows_kernel<GLU, MX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    (int)smem_bytes(kMaxExperts));
         if (e != cudaSuccess) return e;
         attr[dev] = true;
@@ -437,12 +559,16 @@ cudaError_t launch(Params &p, cudaStream_t s) {
     // row tiles side by side whose rows stay in L2
     const int64_t rows_l2 = (int64_t(48) << 20) / a.K / kRows;
     p.group = (int)(rows_l2 < 8 ? 8 : rows_l2 > 0x3FFFFFFF ? 0x3FFFFFFF : rows_l2);
-    product_rows_kernel<GLU><<<(unsigned)(tiles < a.sms ? tiles : a.sms), kThreads, smem_bytes(a.E), s>>>(p);
+    product_rows_kernel<GLU, MX><<<(unsigned)(tiles < a.sms ? tiles : a.sms), kThreads, smem_bytes(a.E), s>>>(p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_product_rows(product::Params &p, cudaStream_t s) { return p.a.glu ? launch<true>(p, s) : launch<false>(p, s); }
+cudaError_t launch_product_rows(product::Params &p, cudaStream_t s) {
+    const bool mx = p.a.x_fmt == ENGRAM_FMT_FP8_E8M0 && p.a.w_fmt == ENGRAM_FMT_FP8_E8M0;
+    if (p.a.glu) return mx ? launch<true, true>(p, s) : launch<true, false>(p, s);
+    return mx ? launch<false, true>(p, s) : launch<false, false>(p, s);
+}
 
 }  // namespace engram

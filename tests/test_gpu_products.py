@@ -119,6 +119,66 @@ def test_project_experts(E, i, shape):
             _near(y[pairs[mine].long()], *X.product(x64[mine], X.weight64(w[e], ws[e])), K, out)
 
 
+FORMATS = [("e8m0", "e8m0"), ("e8m0", "fp8"), ("fp8", "e8m0"), ("fp8", "fp8")]
+# enough rows for tiles of 128 rows and 256 weight rows: K of 1 to 33 blocks, whole and cut off, N with tails of both halves
+MANY = [(1300, 1040, 2000, "bf16"), (700, 128, 7000, "f32"), (2500, 528, 1100, "f16"), (1153, 4112, 2177, "f32"), (9000, 16, 300, "bf16"),
+        (640, 1664, 4097, "f16")]
+
+
+@pytest.mark.parametrize("formats", FORMATS)
+@pytest.mark.parametrize("i,shape", list(enumerate(MANY)))
+def test_project_many_rows(E, i, shape, formats):
+    rows, K, N, out = shape
+    g = rng(400 + i)
+    x, xs = _rows(g, rows, K, formats[0], stride=K + 16 * (i % 2))
+    w, ws, weight = _weight(E, g, 1, N, K, formats[1])
+    y = _project(E, x, xs, formats[0], weight, None, out, rows, N, stride=(0, N + 3, (N + 31) // 16 * 16)[i % 3])
+    _near(y, *X.product(X.rows64(x, xs), X.weight64(w[0], ws[0])), K, out)
+
+
+def test_many_rows_with_scales_at_the_ends(E):
+    """NaN scales of rows and of weights, the least and large ones, powers of two for the tensor cores and in 32 bits alike."""
+    rows, K, N = 1500, 640, 2000
+    g = rng(21)
+    x, xs = _rows(g, rows, K, "e8m0")
+    w, ws, _ = _weight(E, g, 1, N, K, "e8m0")
+    xs[3, 1], xs[4, 0], xs[5, 2], xs[1400, 4], xs[77] = 255, 1, 247, 255, 0
+    ws[0, 2, 1], ws[0, 3, 4], ws[0, 5, 0] = 255, 0, 130
+    nan_rows = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    nan_rows[[3, 1400]] = True
+    nan_cols = torch.zeros(N, dtype=torch.bool, device="cuda")
+    nan_cols[256:384] = True
+    want, mass = X.product(X.rows64(x, xs.clone()), X.weight64(w[0], ws[0]))
+    f32 = [torch.where(s == 255, math.nan, X.scale_values(s)).float() for s in (xs, ws)]
+    for xk, wk, a, b in (("e8m0", "e8m0", xs, ws), ("e8m0", "fp8", xs, f32[1]), ("fp8", "fp8", f32[0], f32[1])):
+        y = _project(E, x, a, xk, E.Fp8Weight(w, b, fmt(E, wk), 1, N, K), None, "f32", rows, N)
+        assert torch.equal(torch.isnan(y), nan_rows[:, None] | nan_cols[None])
+        # row 5 reaches 2^120 2^3 448^2 128: beyond f32 where |want| >= 2^128, and anywhere on the way where the sizes' sum is
+        ok = ~nan_rows[:, None] & ~nan_cols[None] & (mass < 2.0 ** 127)
+        _near(y[ok], want[ok], mass[ok], K, "f32")
+        beyond = ~nan_cols[None] & (want.abs().nan_to_num() >= 2.0 ** 128)
+        assert not torch.isfinite(y[beyond]).any() and ok[~nan_rows][:, ~nan_cols].float().mean() > 0.99
+
+
+MANY_EXPERTS = [(2000, 2, 7, 656, 1200, 1.0), (1500, 4, 9, 144, 2000, 0), (700, 3, 6, 1536, 1792, 3.0)]
+
+
+@pytest.mark.parametrize("formats", FORMATS)
+@pytest.mark.parametrize("i,shape", list(enumerate(MANY_EXPERTS)))
+def test_many_rows_of_experts(E, i, shape, formats):
+    tokens, k, n, K, N, skew = shape
+    g = rng(500 + i)
+    ids, offsets, pairs, lists = random_lists(E, g, tokens, k, n, skew)
+    x, xs = _rows(g, tokens * k, K, formats[0])
+    w, ws, weight = _weight(E, g, n, N, K, formats[1])
+    y = _project(E, x, xs, formats[0], weight, lists, "f32", tokens * k, N)
+    x64 = X.rows64(x, xs)
+    for e in range(n):
+        mine = slice(int(offsets[e]), int(offsets[e + 1]))
+        if mine.start < mine.stop:
+            _near(y[pairs[mine].long()], *X.product(x64[mine], X.weight64(w[e], ws[e])), K, "f32")
+
+
 def _glu_want(x64, w, ws, e, limit):
     (g, mg), (u, mu) = (X.product(x64, X.weight64(w[2 * e + i], ws[2 * e + i])) for i in (0, 1))
     K = x64.shape[1]
@@ -176,20 +236,55 @@ def test_glu_experts(E, i, shape):
     assert (c[total:] == 0x55).all()
 
 
-def test_glu_of_values_that_are_not_finite(E):
-    rows, K, N = 20, 256, 256
+@pytest.mark.parametrize("formats", FORMATS)
+@pytest.mark.parametrize("i,shape", [(0, (1500, 272, 1200)), (1, (2600, 1296, 640)), (2, (700, 128, 2064))])
+def test_glu_many_rows(E, i, shape, formats):
+    rows, K, N = shape
+    g, out, limit = rng(600 + i), ("e8m0", "fp8")[i % 2], (0.0, 0.75)[i % 2]
+    x, xs = _rows(g, rows, K, formats[0], stride=K + 32)
+    w, ws, weight = _weight(E, g, 2, N, K, formats[1], True)
+    c, s = _glu(E, x, xs, formats[0], weight, None, limit, out, rows, N)
+    check_codes(c[:rows], s[:rows], *_glu_want(X.rows64(x, xs), w, ws, 0, limit))
+    assert (c[rows:] == 0x55).all() and (s[rows:] == 9).all()
+
+
+@pytest.mark.parametrize("formats", FORMATS)
+@pytest.mark.parametrize("i,shape", list(enumerate(MANY_EXPERTS)))
+def test_glu_many_rows_of_experts(E, i, shape, formats):
+    tokens, k, n, K, N, skew = shape
+    g = rng(700 + i)
+    ids, offsets, pairs, lists = random_lists(E, g, tokens, k, n, skew)
+    x, xs = _rows(g, tokens, K, formats[0], stride=K + 48)
+    w, ws, weight = _weight(E, g, 2 * n, N, K, formats[1], True)
+    total = tokens * k
+    c, s = _glu(E, x, xs, formats[0], weight, lists, 0.0, ("fp8", "e8m0")[i % 2], total, N)
+    x64 = X.rows64(x, xs)
+    want, err = (torch.empty((total, N), dtype=torch.float64, device="cuda") for _ in "ab")
+    for e in range(n):
+        mine = slice(int(offsets[e]), int(offsets[e + 1]))
+        if mine.start < mine.stop:
+            want[mine], err[mine] = _glu_want(x64[pairs[mine].long() // k], w, ws, e, 0.0)
+    check_codes(c[:total], s[:total], want, err)
+    assert (c[total:] == 0x55).all()
+
+
+@pytest.mark.parametrize("rows,formats", [(20, "fp8"), (2500, "fp8"), (2500, "e8m0")])
+def test_glu_of_values_that_are_not_finite(E, rows, formats):
+    K, N = 256, 640
     g = rng(9)
     x, xs = _rows(g, rows, K, "e8m0")
-    w, ws, weight = _weight(E, g, 2, N, K, "fp8", True)
+    w, ws, weight = _weight(E, g, 2, N, K, formats, True)
     xs[2] = 255                                              # a NaN row
-    ws[1, 1] = math.inf                                      # infinite values in the second block of all rows
+    ws[1, 1] = math.inf if formats == "fp8" else 255         # infinite or NaN values in the second block of all rows
     c, s = _glu(E, x, xs, "e8m0", weight, None, 0.0, "e8m0", rows, N)
     assert (s[2] == 255).all() and (c[2] == 0).all()
-    assert (s[:rows, 1] == 255).all() and (c[:rows, 128:] == 0).all()
+    assert (s[:rows, 1] == 255).all() and (c[:rows, 128:256] == 0).all()
     keep = torch.arange(rows, device="cuda") != 2
-    ws[1, 1] = 1.0
+    ws[1, 1] = 1 if formats == "fp8" else 127
     want, err = _glu_want(X.rows64(x, xs)[keep], w, ws, 0, 0.0)
-    check_codes(c[:rows][keep][:, :128].contiguous(), s[:rows][keep][:, :1].contiguous(), want[:, :128], err[:, :128])
+    for b in (0, 2, 4):
+        at = slice(128 * b, 128 * b + 128)
+        check_codes(c[:rows][keep][:, at].contiguous(), s[:rows][keep][:, b: b + 1].contiguous(), want[:, at], err[:, at])
 
 
 def test_rows_in_no_list_stay_as_they_were(E):
