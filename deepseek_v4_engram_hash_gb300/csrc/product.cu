@@ -482,14 +482,12 @@ template <bool GLU, int NT>
 cudaError_t launch_tile(Params &p, cudaStream_t s) {
     using C = Cfg<NT>;
     const ProductArgs &a = p.a;
-    static bool attr[64] = {};
+    static Fit fit[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!attr[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(product_kernel<GLU, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)C::bytes(kMaxExperts));
+    if (!fit[dev].ready) {
+        const cudaError_t e = make_fit(&fit[dev], product_kernel<GLU, NT>, C::kThreads, C::bytes(kMaxExperts));
         if (e != cudaSuccess) return e;
-        attr[dev] = true;
     }
     const uint64_t xd[2] = {(uint64_t)a.K, (uint64_t)a.rows}, xst[1] = {(uint64_t)a.x_stride};
     const uint32_t box[2] = {128, NT}, box16[2] = {128, 16};
@@ -497,24 +495,11 @@ cudaError_t launch_tile(Params &p, cudaStream_t s) {
     p.m_tiles = (a.N + (GLU ? kM : 2 * kM) - 1) / (GLU ? kM : 2 * kM);
     const int64_t tiles = (int64_t)product_row_tiles(a, NT) * p.m_tiles;
     if (tiles > 0x3FFFFFFF) return cudaErrorInvalidConfiguration;
-    // a cluster shares a tile while that leaves SMs idle otherwise, with two K blocks a CTA at least
-    p.split = 1;
-    while (p.split < 8 && tiles * p.split * 2 <= a.sms && p.KB >= p.split * 4) p.split *= 2;
+    p.split = fitting_split(fit[dev], tiles, p.KB / 2, false);
     // row tiles of a dense product side by side whose rows stay in L2
     const int64_t rows_l2 = (int64_t(48) << 20) / a.K / NT;
     p.group = (int)(rows_l2 < 8 ? 8 : rows_l2 > 0x3FFFFFFF ? 0x3FFFFFFF : rows_l2);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.split > 1 ? tiles * p.split : tiles < a.sms ? tiles : a.sms));
-    cfg.blockDim = dim3(C::kThreads);
-    cfg.dynamicSmemBytes = C::bytes(a.E);
-    cfg.stream = s;
-    cudaLaunchAttribute la[1];
-    la[0].id = cudaLaunchAttributeClusterDimension;
-    la[0].val.clusterDim.x = (unsigned)p.split;
-    la[0].val.clusterDim.y = la[0].val.clusterDim.z = 1;
-    cfg.attrs = la;
-    cfg.numAttrs = p.split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, product_kernel<GLU, NT>, p);
+    return launch_split(product_kernel<GLU, NT>, p, tiles, C::kThreads, C::bytes(a.E), s);
 }
 
 }  // namespace
@@ -531,12 +516,11 @@ cudaError_t launch_product(const ProductArgs &a, cudaStream_t s) {
     const uint64_t row = (uint64_t)a.out_stride * (a.glu ? 1 : a.out_type == ENGRAM_T_F32 ? 4 : 2);
     const uint64_t either = row | reinterpret_cast<uintptr_t>(a.out);
     p.wide = either % 32 == 0 ? 2 : either % 16 == 0 ? 1 : 0;
-    // Many rows: tiles of 128 rows and 256 weight rows, where they are enough for the SMs (shared memory bounds this kernel
-    // at three times the MMA's time a block: 8192 x 4096 -> 6144 took 324 us with it).  Few rows an expert: a tile of few
-    // rows leaves shared memory to the weights on their way.
+    // Many rows: tiles of 128 rows and 256 weight rows (shared memory bounds this kernel at three times the MMA's time a
+    // block: 8192 x 4096 -> 6144 took 324 us with it).  Few rows an expert: a tile of few rows leaves shared memory to the
+    // weights on their way.
     const int rows = a.offsets ? (a.n_pairs + a.E - 1) / a.E : a.n_pairs;
-    if (rows > 64 && (int64_t)product_row_tiles(a, 128) * ((a.N + (a.glu ? 127 : 255)) / (a.glu ? 128 : 256)) * 2 > a.sms)
-        return launch_product_rows(p, s);
+    if (rows > 64) return launch_product_rows(p, s);
     if (a.glu) return rows <= 24 ? launch_tile<true, 32>(p, s) : launch_tile<true, 64>(p, s);
     return rows <= 24 ? launch_tile<false, 32>(p, s) : launch_tile<false, 64>(p, s);
 }

@@ -269,6 +269,53 @@ __device__ __forceinline__ bool four_at_once(const void *scales, int fmt, int KB
     return KB % 4 == 0 && reinterpret_cast<uintptr_t>(scales) % (fmt == ENGRAM_FMT_FP8 ? 16 : 4) == 0;
 }
 
+using Kernel = void (*)(const Params);
+
+// Of one kernel on one device: whether its shared memory is allowed, and how many clusters of each size run at once.
+struct Fit {
+    bool ready;
+    int clusters[9];
+};
+// smem: what the most experts need.
+inline cudaError_t make_fit(Fit *fit, Kernel kernel, int threads, size_t smem) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    for (int s = 2; s <= 8 && e == cudaSuccess; ++s) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)s);
+        cfg.blockDim = dim3((unsigned)threads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute la[1];
+        la[0].id = cudaLaunchAttributeClusterDimension;
+        la[0].val.clusterDim.x = (unsigned)s;
+        la[0].val.clusterDim.y = la[0].val.clusterDim.z = 1;
+        cfg.attrs = la;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&fit->clusters[s], kernel, &cfg);
+    }
+    fit->ready = e == cudaSuccess;
+    return e;
+}
+// How many CTAs share a tile (at most `most`): the most of 2..8 (powers of two) for which all clusters run at once, or 1.
+inline int fitting_split(const Fit &fit, int64_t tiles, int most, bool powers) {
+    for (int s = 8; s > 1; s = powers ? s / 2 : s - 1)
+        if (s <= most && tiles <= fit.clusters[s]) return s;
+    return 1;
+}
+inline cudaError_t launch_split(Kernel kernel, const Params &p, int64_t tiles, int threads, size_t smem, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.split > 1 ? tiles * p.split : tiles < p.a.sms ? tiles : p.a.sms));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute la[1];
+    la[0].id = cudaLaunchAttributeClusterDimension;
+    la[0].val.clusterDim.x = (unsigned)p.split;
+    la[0].val.clusterDim.y = la[0].val.clusterDim.z = 1;
+    cfg.attrs = la;
+    cfg.numAttrs = p.split > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 }  // namespace product
 
 cudaError_t launch_product_rows(product::Params &p, cudaStream_t s);   // product_rows.cu

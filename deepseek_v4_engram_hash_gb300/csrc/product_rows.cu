@@ -19,6 +19,7 @@
 // Where both scales are powers of two (e8m0 bytes) the tensor cores apply them: tcgen05.mma kind::mxf8f6f4 with a
 // block's bytes in tensor memory (four blocks to a 32-bit column; an MMA names its byte).  Sums then stay in tensor memory over
 // all of K, in one 256-column buffer, and the last warps take them once a tile.
+// Where there are fewer tiles than SMs a cluster shares a tile as in product.cu, K cut at groups of four blocks.
 // Waits are bounded as in product.cu.
 #include "product.cuh"
 
@@ -122,6 +123,82 @@ __device__ __forceinline__ uint32_t four_bytes(const void *p, bool vec, int64_t 
     return r;
 }
 
+// The part of CTA `rank` of a cluster that shares tile w: 128 / split of its rows, from all CTAs' sums, added in CTA order.  Thread i of
+// 256: a row, and a slice of the columns.
+template <bool GLU, class Sync>
+__device__ __forceinline__ void share_of_tile(const Params &p, const TileAt &w, uint32_t base, uint8_t *smem, int rank, int i, Sync together) {
+    const ProductArgs &a = p.a;
+    const int rows = kRows / p.split, row = rank * rows + i % rows, slice = i / rows;
+    const int per = (GLU ? kM : kCols) / (2 * p.split), c0 = slice * per;   // columns of a slice: 8 to 64
+    int to = row < w.n ? w.row + row : -1;
+    if (!GLU && a.pairs && to >= 0) to = out_row_of(a, to);
+    auto sum8 = [&](int c, float (&v)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+        for (int r = 0; r < p.split; ++r) {
+            const uint32_t at = mapa(base, (uint32_t)r) + (uint32_t)(c * kRows + row) * 4;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += lds_cluster(at + j * kRows * 4);
+        }
+    };
+    if (!GLU) {
+        if (to < 0) return;
+        for (int c = c0; c < c0 + per && w.m0 + c < a.N; c += 8) {
+            float v[8];
+            sum8(c, v);
+            const int64_t at = (int64_t)to * a.out_stride + w.m0 + c;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (w.m0 + c + j >= a.N) break;
+                if (a.out_type == ENGRAM_T_BF16)
+                    static_cast<__nv_bfloat16 *>(a.out)[at + j] = __float2bfloat16_rn(v[j]);
+                else if (a.out_type == ENGRAM_T_F16)
+                    static_cast<__half *>(a.out)[at + j] = __float2half_rn(v[j]);
+                else
+                    static_cast<float *>(a.out)[at + j] = v[j];
+            }
+        }
+        return;
+    }
+    // gated values of the slice (32 at most, [value][thread] behind the parts), then the row's largest over its slices
+    float *mine = reinterpret_cast<float *>(smem + kCols * kRows * 4) + i;
+    uint32_t *amax = reinterpret_cast<uint32_t *>(smem + oMax);       // [slices][rows], 256 in all
+    float big = 0.f;
+    for (int c = c0; c < c0 + per; c += 8) {
+        float g[8], u[8];
+        sum8(c, g);
+        sum8(kM + c, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            g[j] = gated(g[j], u[j], a.limit);
+            big = amax3(big, g[j], 0.f);
+            mine[(c - c0 + j) * 256] = g[j];
+        }
+    }
+    amax[i] = __float_as_uint(big);
+    if (!together() || to < 0) return;
+    uint32_t most = 0;
+    for (int s = 0; s < 2 * p.split; ++s) most = max(most, amax[s * rows + i % rows]);
+    const uint32_t byte = block_scale_byte(most);
+    const float inv = byte == 255u ? 0.f : inv_scale(byte);
+    for (int c = c0; c < c0 + per && w.m0 + c < a.N; c += 8) {
+        uint2 code = make_uint2(0u, 0u);
+        if (byte != 255u) {
+            const float *v = mine + (c - c0) * 256;
+            code.x = e4m3x4(v[0] * inv, v[256] * inv, v[512] * inv, v[768] * inv);
+            code.y = e4m3x4(v[1024] * inv, v[1280] * inv, v[1536] * inv, v[1792] * inv);
+        }
+        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + (int64_t)to * a.N + w.m0 + c) = code;
+    }
+    if (slice == 0) {
+        const int64_t at = (int64_t)to * p.NB + w.m0 / kM;
+        if (a.out_type == ENGRAM_FMT_FP8_E8M0)
+            static_cast<uint8_t *>(a.out_scales)[at] = (uint8_t)byte;
+        else
+            static_cast<float *>(a.out_scales)[at] = e8m0_to_f32(byte);
+    }
+}
+
 template <bool GLU, bool MX>
 __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_constant__ Params p) {
     constexpr int ST = kStages;
@@ -171,10 +248,13 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
     set_lists(a, first, count, before, kRows, kThreads);
     tc_fence_before();
     __syncthreads();
+    if (p.split > 1) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    const int t0 = blockIdx.x, t_step = gridDim.x, tiles = before[a.E] * p.m_tiles, KB = p.KB;
+    const int rank = p.split > 1 ? (int)cluster_rank() : 0;
+    const int t0 = blockIdx.x / p.split, t_step = gridDim.x / p.split, tiles = before[a.E] * p.m_tiles, KB = p.KB;
+    const int fours = (KB + 3) / 4, kb0 = fours * rank / p.split * 4, kb1 = min(KB, fours * (rank + 1) / p.split * 4);
     auto tile_at = [&](int t) { return tile_of(p, first, count, before, t, GLU ? kM : kCols); };
     // whether the tile has weight rows for its second 128 columns
     auto two = [&](const TileAt &t) { return GLU || t.m0 + kM < a.N; };
@@ -189,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
         bool ok = true;
         for (int t = t0; t < tiles && ok; t += t_step) {
             const TileAt w = tile_at(t);
-            for (int kb = 0; kb < KB; ++kb, ++it) {
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = it % ST;
                 if (!(ok = wait(done(s), it / ST ^ 1))) break;
                 if (elect()) {
@@ -218,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
         for (int t = t0; MX && t < tiles && ok; t += t_step, ++turn) {
             const int N = two(tile_at(t)) ? kCols : kM;
             if (!lane_wait(tempty(0), turn ^ 1)) ok = false;
-            for (int kb = 0; kb < KB; ++kb, ++it) {
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = it % ST, slot = group % kSlots, byte = kb & 3;
                 const uint32_t sa = tmem + kScaleTmem + (group & 1) * kScaleCols, sb = sa + 4;
                 const uint64_t da = desc + s * (kStage >> 4), db = da + (kTileA >> 4);
@@ -240,23 +320,23 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
                 tc_fence_after();
                 if (elect()) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mma_mx(tmem, da + 2u * k, db + 2u * k, idesc, sa, sb, kb | k);
+                    for (int k = 0; k < 4; ++k) mma_mx(tmem, da + 2u * k, db + 2u * k, idesc, sa, sb, (kb - kb0) | k);
                     commit(done(s));
-                    if (kb + 1 == KB) commit(sums_ready);
+                    if (kb + 1 == kb1) commit(sums_ready);
                 }
                 __syncwarp();
             }
-            if (KB & 3) ++group;
+            if (kb1 & 3) ++group;
             ok = __all_sync(0xFFFFFFFFu, ok);
         }
         for (int t = t0; !MX && t < tiles && ok; t += t_step) {
             const uint32_t idesc = idesc_f8(two(tile_at(t)) ? kCols : kM);
-            for (int kb = 0; kb < KB; ++kb, ++it) {
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = it % ST;
                 const uint32_t d = tmem + (it & 1) * kCols;
                 const uint64_t da = desc + s * (kStage >> 4), db = da + (kTileA >> 4);
-                if (!lane_wait(tempty(it & 1), it >> 1 ^ 1)) ok = false;
                 if (!lane_wait(full(s), it / ST)) ok = false;
+                if (!lane_wait(tempty(it & 1), it >> 1 ^ 1)) ok = false;
                 tc_fence_after();
                 if (elect()) {
 #pragma unroll
@@ -298,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
                     const int c = i * 32 + lane;
                     r4[i] = warp == kScaleWarp && c < w.n ? gather ? token_of(a, w.row + c) : w.row + c : -1;
                 }
-                for (int kb4 = 0; kb4 < KB; kb4 += 4, ++it) {
+                for (int kb4 = kb0; kb4 < kb1; kb4 += 4, ++it) {
                     const int left = KB - kb4, slot = it % kSlots;
                     uint4 u = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
                     uint32_t b0 = 0, b1 = 0;
@@ -335,10 +415,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
                 next_w[0] = load_scales(a.w_scales, a.w_fmt, vec_w, w0 + kb4, left);
                 if (both) next_w[1] = load_scales(a.w_scales, a.w_fmt, vec_w, w1 + kb4, left);
             };
-            fetch(0);
-            for (int kb4 = 0; kb4 < KB; kb4 += 4, ++it) {
+            fetch(kb0);
+            for (int kb4 = kb0; kb4 < kb1; kb4 += 4, ++it) {
                 const uint4 x[2] = {next_x[0], next_x[1]}, s0 = next_w[0], s1 = both ? next_w[1] : s0;
-                if (kb4 + 4 < KB) fetch(kb4 + 4);
+                if (kb4 + 4 < kb1) fetch(kb4 + 4);
                 const int slot = it % kSlots;
                 float *f = reinterpret_cast<float *>(smem + oScale + slot * kSlotBytes);
                 if (!(ok = wait(sempty(slot), it / kSlots ^ 1))) break;
@@ -372,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
                 const int r = r0 + i * 4 * kCopyWarps;
                 from[i] = r < w.n ? (uint32_t)(token_of(a, w.row + r) * (a.x_stride >> 4)) : 0u;
             }
-            for (int kb = 0; kb < KB; ++kb, ++it) {
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int s = it % ST;
                 if (!(ok = wait(done(s), it / ST ^ 1))) break;
                 const bool real = kb * 128 + chunk * 16 < a.K;
@@ -432,12 +512,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
             ok = lane_wait(done(it % ST), it / ST) && ok;
             tc_fence_after();
             tmem_ld16(step_at(0), u[0]);
-            for (int kb = 0; kb < KB; ++kb) {
+            for (int kb = kb0; kb < kb1; ++kb) {
                 const uint32_t slot = group % kSlots, four = kb & 3;
                 if (!four) ok = lane_wait(sfull(slot), group / kSlots) && ok;
                 const float *f = reinterpret_cast<const float *>(smem + oScale + slot * kSlotBytes), *fw = f + 4 * kRows + 2 * four;
                 const float sx = f[four * kRows + row], f0 = sx * fw[GLU ? 0 : g], f1 = GLU ? sx * fw[1] : f0;
-                if (four == 3 || kb + 1 == KB) {
+                if (four == 3 || kb + 1 == kb1) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(sempty(slot));
                     ++group;
@@ -454,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
                         __syncwarp();
                         if (lane == 0) mbar_arrive(tempty(it & 1));
                         ++it;
-                        if (kb + 1 < KB) {
+                        if (kb + 1 < kb1) {
                             ok = lane_wait(done(it % ST), it / ST) && ok;
                             tc_fence_after();
                             tmem_ld16(step_at(0), u[0]);
@@ -466,6 +546,20 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
             }
             ++turn;
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            if (p.split > 1) {
+                // this part's sums as [column][row]; the ring they overwrite is drained: a cluster has one tile
+                float *part = reinterpret_cast<float *>(smem) + row;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        float x, y;
+                        unpack2(acc[i][j], x, y);
+                        part[(column(i) + 2 * j) * kRows] = x;
+                        part[(column(i) + 2 * j + 1) * kRows] = y;
+                    }
+                break;
+            }
             if (GLU) {
                 uint32_t *amax = reinterpret_cast<uint32_t *>(smem + oMax) + (turn & 1) * 2 * kRows + row;
                 float big = 0.f;
@@ -529,6 +623,20 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
             }
         }
         __syncwarp();
+        if (p.split > 1) {
+            cluster_sync();
+            if (t0 < tiles && ok) share_of_tile<GLU>(p, tile_at(t0), base, smem, rank, threadIdx.x - 32 * kEpiWarp, [&]() {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(together);
+                return wait(together, 0);
+            });
+            cluster_sync();
+        }
+    }
+    if (p.split > 1 && warp < kEpiWarp) {
+        __syncwarp();
+        cluster_sync();
+        cluster_sync();
     }
     tc_fence_before();
     __syncthreads();
@@ -540,14 +648,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
 template <bool GLU, bool MX>
 cudaError_t launch(Params &p, cudaStream_t s) {
     const ProductArgs &a = p.a;
-    static bool attr[64] = {};
+    static Fit fit[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!attr[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(product_rows_kernel<GLU, MX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)smem_bytes(kMaxExperts));
+    if (!fit[dev].ready) {
+        const cudaError_t e = make_fit(&fit[dev], product_rows_kernel<GLU, MX>, kThreads, smem_bytes(kMaxExperts));
         if (e != cudaSuccess) return e;
-        attr[dev] = true;
     }
     const uint64_t xd[2] = {(uint64_t)a.K, (uint64_t)a.rows}, xst[1] = {(uint64_t)a.x_stride};
     const uint32_t box[2] = {128, kRows};
@@ -555,12 +661,11 @@ cudaError_t launch(Params &p, cudaStream_t s) {
     p.m_tiles = (a.N + (GLU ? kM : kCols) - 1) / (GLU ? kM : kCols);
     const int64_t tiles = (int64_t)product_row_tiles(a, kRows) * p.m_tiles;
     if (tiles > 0x3FFFFFFF) return cudaErrorInvalidConfiguration;
-    p.split = 1;
+    p.split = fitting_split(fit[dev], tiles, (p.KB + 3) / 4, true);
     // row tiles side by side whose rows stay in L2
     const int64_t rows_l2 = (int64_t(48) << 20) / a.K / kRows;
     p.group = (int)(rows_l2 < 8 ? 8 : rows_l2 > 0x3FFFFFFF ? 0x3FFFFFFF : rows_l2);
-    product_rows_kernel<GLU, MX><<<(unsigned)(tiles < a.sms ? tiles : a.sms), kThreads, smem_bytes(a.E), s>>>(p);
-    return cudaGetLastError();
+    return launch_split(product_rows_kernel<GLU, MX>, p, tiles, kThreads, smem_bytes(a.E), s);
 }
 
 }  // namespace

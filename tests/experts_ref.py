@@ -35,9 +35,10 @@ def product(x, w):
 
 
 def sum_error(K):
-    """The relative bound (of the products' sizes) on a sum of K exact products that is added up in f32: blocks of 128 in any
-    order, each addition cut off or rounded (2^-23 of a partial sum), the factor sx sw (2^-24) and one FMA a block (2^-24)."""
-    return (B + 1 + (K + B - 1) // B) * 2.0 ** -23
+    """The relative bound (of the products' sizes) on a sum of K exact products that is added up in f32, each addition cut off or
+    rounded (2^-23 of a partial sum): blocks of 128 in any order, the factor sx sw (2^-24) and one FMA a block (2^-24); or 32 products
+    in any order at a time onto the running sum (power-of-two factors are exact).  Up to 8 partial sums are then added."""
+    return (max(B + 1 + (K + B - 1) // B, 32 + (K + 31) // 32) + 8) * 2.0 ** -23
 
 
 def glu(g, u, limit):

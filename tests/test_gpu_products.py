@@ -121,7 +121,7 @@ def test_project_experts(E, i, shape):
 
 FORMATS = [("e8m0", "e8m0"), ("e8m0", "fp8"), ("fp8", "e8m0"), ("fp8", "fp8")]
 # enough rows for tiles of 128 rows and 256 weight rows: K of 1 to 33 blocks, whole and cut off, N with tails of both halves
-MANY = [(1300, 1040, 2000, "bf16"), (700, 128, 7000, "f32"), (2500, 528, 1100, "f16"), (1153, 4112, 2177, "f32"), (9000, 16, 300, "bf16"),
+MANY = [(65, 4096, 300, "f32"), (100, 1568, 1000, "bf16"), (777, 640, 515, "f16"), (128, 8192, 256, "bf16"), (300, 2064, 2100, "f32"), (1300, 1040, 2000, "bf16"), (700, 128, 7000, "f32"), (2500, 528, 1100, "f16"), (1153, 4112, 2177, "f32"), (9000, 16, 300, "bf16"),
         (640, 1664, 4097, "f16")]
 
 
@@ -160,7 +160,7 @@ def test_many_rows_with_scales_at_the_ends(E):
         assert not torch.isfinite(y[beyond]).any() and ok[~nan_rows][:, ~nan_cols].float().mean() > 0.99
 
 
-MANY_EXPERTS = [(2000, 2, 7, 656, 1200, 1.0), (1500, 4, 9, 144, 2000, 0), (700, 3, 6, 1536, 1792, 3.0)]
+MANY_EXPERTS = [(150, 1, 2, 2064, 272, 0), (200, 2, 3, 1040, 640, 1.0), (2000, 2, 7, 656, 1200, 1.0), (1500, 4, 9, 144, 2000, 0), (700, 3, 6, 1536, 1792, 3.0)]
 
 
 @pytest.mark.parametrize("formats", FORMATS)
@@ -237,7 +237,8 @@ def test_glu_experts(E, i, shape):
 
 
 @pytest.mark.parametrize("formats", FORMATS)
-@pytest.mark.parametrize("i,shape", [(0, (1500, 272, 1200)), (1, (2600, 1296, 640)), (2, (700, 128, 2064))])
+@pytest.mark.parametrize("i,shape", [(0, (1500, 272, 1200)), (1, (2600, 1296, 640)), (2, (700, 128, 2064)),
+                                     (3, (70, 4096, 80)), (4, (333, 1088, 272)), (5, (128, 2048, 1040))])
 def test_glu_many_rows(E, i, shape, formats):
     rows, K, N = shape
     g, out, limit = rng(600 + i), ("e8m0", "fp8")[i % 2], (0.0, 0.75)[i % 2]
