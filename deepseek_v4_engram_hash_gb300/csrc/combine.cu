@@ -13,6 +13,7 @@ namespace {
 
 constexpr int kThreads = 128, kBlocks = 8;             // blocks an SM at least
 
+// Waits for the kernel before it (a programmatic dependent launch) where it first reads.
 template <int YT>
 __global__ void __launch_bounds__(kThreads, kBlocks) combine_kernel(const CombineArgs a) {
     const unsigned token = blockIdx.x / a.blocks;    // blocks: of a token
@@ -21,6 +22,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) combine_kernel(const Combin
     if (c >= a.dim) return;
     const float *w = a.w + t * a.top_k;
     float s[8] = {};
+    griddep_wait();
     constexpr int kRows = YT == ENGRAM_T_F32 ? 4 : 8;
     for (int j0 = 0; j0 < a.top_k; j0 += kRows) {
         Raw8<YT> raw[kRows];
@@ -67,12 +69,20 @@ cudaError_t launch_combine(CombineArgs a, cudaStream_t s) {
     a.blocks = (chunks + threads - 1) / threads;
     const int64_t blocks = (int64_t)a.tokens * a.blocks;
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = s;
+    cudaLaunchAttribute la[1];
+    la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    la[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = la;
+    cfg.numAttrs = 1;
     switch (a.y_type) {
-        case ENGRAM_T_BF16: combine_kernel<ENGRAM_T_BF16><<<(unsigned)blocks, threads, 0, s>>>(a); break;
-        case ENGRAM_T_F16: combine_kernel<ENGRAM_T_F16><<<(unsigned)blocks, threads, 0, s>>>(a); break;
-        default: combine_kernel<ENGRAM_T_F32><<<(unsigned)blocks, threads, 0, s>>>(a);
+        case ENGRAM_T_BF16: return cudaLaunchKernelEx(&cfg, combine_kernel<ENGRAM_T_BF16>, a);
+        case ENGRAM_T_F16: return cudaLaunchKernelEx(&cfg, combine_kernel<ENGRAM_T_F16>, a);
+        default: return cudaLaunchKernelEx(&cfg, combine_kernel<ENGRAM_T_F32>, a);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace engram

@@ -99,6 +99,8 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
                      ::"r"(smem_u32((const void *)tmem_slot)), "r"(kCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    griddep_wait();
+    griddep_launch();
     set_lists(a, first, count, before, NT, C::kThreads);
     tc_fence_before();
     __syncthreads();
@@ -450,15 +452,14 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
                     float v0[16], v1[16];
                     const int n = min(16, hi - c0);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v0[j] = v1[j] = 0.f;
-                    for (int r = 0; r < p.split; ++r) {
-                        const uint32_t part = mapa(base, (uint32_t)r) + (uint32_t)(c0 * 2 * kM + m) * 4;
+                    for (int j0 = 0; j0 < 16; j0 += 4) {
+                        uint32_t at[8];
+                        float v[8];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            if (j >= n) break;
-                            v0[j] += lds_cluster(part + j * 2 * kM * 4);
-                            v1[j] += lds_cluster(part + j * 2 * kM * 4 + kM * 4);
-                        }
+                        for (int j = 0; j < 8; ++j) at[j] = (uint32_t)((c0 + j0 + (j >> 1)) * 2 * kM + (j & 1) * kM + m) * 4;
+                        if (j0 < n) sum_of_cluster(base, p.split, at, 2 * (n - j0), v);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v0[j0 + j] = j0 < n ? v[2 * j] : 0.f, v1[j0 + j] = j0 < n ? v[2 * j + 1] : 0.f;
                     }
                     ok = finish(w, v0, v1, c0, n);
                 }

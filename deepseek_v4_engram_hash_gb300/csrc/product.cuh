@@ -138,6 +138,23 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
+// The sums of all CTAs' f32 values at base + at[j], j < n <= N, in CTA order; their loads are all under way at once.
+template <int N>
+__device__ __forceinline__ void sum_of_cluster(uint32_t base, int split, const uint32_t (&at)[N], int n, float (&sum)[N]) {
+    float x[8][N];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        const uint32_t of = mapa(base, (uint32_t)min(r, split - 1));
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[r][j] = r < split && j < n ? lds_cluster(of + at[j]) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        sum[j] = x[0][j];
+#pragma unroll
+        for (int r = 1; r < 8; ++r) sum[j] += x[r][j];
+    }
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -185,7 +202,7 @@ __device__ __forceinline__ float scale_at(const uint4 &r, int fmt, bool vec, int
 }
 
 
-// The experts' rows and how many tiles of up to `rows` rows come before each: shared memory, by all threads.
+// The experts' rows (global memory: after griddep_wait) and how many tiles of up to `rows` rows come before each: shared memory, by all threads.
 __device__ __forceinline__ void set_lists(const ProductArgs &a, int *first, int *count, int *before, int rows, int threads) {
     for (int e = threadIdx.x; e < a.E; e += threads) {
         int lo = 0, n = a.n_pairs;
@@ -307,12 +324,14 @@ inline cudaError_t launch_split(Kernel kernel, const Params &p, int64_t tiles, i
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute la[1];
-    la[0].id = cudaLaunchAttributeClusterDimension;
-    la[0].val.clusterDim.x = (unsigned)p.split;
-    la[0].val.clusterDim.y = la[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute la[2];
+    la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // the set-up runs beside the end of the kernel before
+    la[0].val.programmaticStreamSerializationAllowed = 1;
+    la[1].id = cudaLaunchAttributeClusterDimension;
+    la[1].val.clusterDim.x = (unsigned)p.split;
+    la[1].val.clusterDim.y = la[1].val.clusterDim.z = 1;
     cfg.attrs = la;
-    cfg.numAttrs = p.split > 1 ? 1 : 0;
+    cfg.numAttrs = p.split > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 

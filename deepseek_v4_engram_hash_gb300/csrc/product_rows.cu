@@ -133,13 +133,10 @@ __device__ __forceinline__ void share_of_tile(const Params &p, const TileAt &w, 
     int to = row < w.n ? w.row + row : -1;
     if (!GLU && a.pairs && to >= 0) to = out_row_of(a, to);
     auto sum8 = [&](int c, float (&v)[8]) {
+        uint32_t at[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.f;
-        for (int r = 0; r < p.split; ++r) {
-            const uint32_t at = mapa(base, (uint32_t)r) + (uint32_t)(c * kRows + row) * 4;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += lds_cluster(at + j * kRows * 4);
-        }
+        for (int j = 0; j < 8; ++j) at[j] = (uint32_t)((c + j) * kRows + row) * 4;
+        sum_of_cluster(base, p.split, at, 8, v);
     };
     if (!GLU) {
         if (to < 0) return;
@@ -147,15 +144,24 @@ __device__ __forceinline__ void share_of_tile(const Params &p, const TileAt &w, 
             float v[8];
             sum8(c, v);
             const int64_t at = (int64_t)to * a.out_stride + w.m0 + c;
+            const bool whole = p.wide && w.m0 + c + 8 <= a.N;
+            if (whole && a.out_type == ENGRAM_T_BF16) {
+                store8<ENGRAM_T_BF16>(a.out, at, v);
+            } else if (whole && a.out_type == ENGRAM_T_F16) {
+                store8<ENGRAM_T_F16>(a.out, at, v);
+            } else if (whole) {
+                store8<ENGRAM_T_F32>(a.out, at, v);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (w.m0 + c + j >= a.N) break;
-                if (a.out_type == ENGRAM_T_BF16)
-                    static_cast<__nv_bfloat16 *>(a.out)[at + j] = __float2bfloat16_rn(v[j]);
-                else if (a.out_type == ENGRAM_T_F16)
-                    static_cast<__half *>(a.out)[at + j] = __float2half_rn(v[j]);
-                else
-                    static_cast<float *>(a.out)[at + j] = v[j];
+                for (int j = 0; j < 8; ++j) {
+                    if (w.m0 + c + j >= a.N) break;
+                    if (a.out_type == ENGRAM_T_BF16)
+                        static_cast<__nv_bfloat16 *>(a.out)[at + j] = __float2bfloat16_rn(v[j]);
+                    else if (a.out_type == ENGRAM_T_F16)
+                        static_cast<__half *>(a.out)[at + j] = __float2half_rn(v[j]);
+                    else
+                        static_cast<float *>(a.out)[at + j] = v[j];
+                }
             }
         }
         return;
@@ -245,6 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
                      ::"r"(smem_u32((const void *)tmem_slot)), "r"(512u) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    griddep_wait();
+    griddep_launch();
     set_lists(a, first, count, before, kRows, kThreads);
     tc_fence_before();
     __syncthreads();
