@@ -64,6 +64,7 @@ int check_product(const uint8_t *d_x, int64_t x_stride, const void *d_x_scales, 
     if (!aligned(d_x, 16) || !aligned(w->codes, 16) || (x_fmt == ENGRAM_FMT_FP8 && !aligned(d_x_scales, 4)) ||
         (w->fmt == ENGRAM_FMT_FP8 && !aligned(w->scales, 4)))
         return ENGRAM_E_ALIGN;
+    if (lists && glu && (int64_t)rows * (x_stride / 16) >= int64_t(1) << 32) return ENGRAM_E_UNSUPPORTED;   // gathered rows
     if (lists) {
         const int rc = check_list_pointers(lists, true);
         if (rc) return rc;

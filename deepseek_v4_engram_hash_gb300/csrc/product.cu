@@ -1,23 +1,27 @@
 // product.cu -- products of e4m3 rows with e4m3 weights that have a scale for each
 // block of 128 (engram_project_fp8), and the gated pair of them with an 8-bit
-// output (engram_glu_fp8), dense or with a matrix an expert.
+// output (engram_glu_fp8), dense or with a matrix an expert: up to 24 rows (an expert, on
+// average) here, more in product_rows.cu.
 //
 // out[r, n] = sum_b sx[r, b] sw[n / 128, b] sum_{k in block b} x[r, k] W[n, k].  The inner sum
 // of 128 products is tcgen05.mma kind::f8f6f4 (products exact, f32 sums in tensor memory); the
 // outer one is f32 FMAs in registers.  Weights are the M side of the MMA (two blocks of
-// 128 rows: neighbours, or the gate's and the other's), rows of x the N side, so that one token
-// costs the tensor cores N = 16 and a prompt N = 128 by the same code, and a thread that holds
-// weight row m for all tokens writes neighbouring addresses beside its warp's others.
+// 128 rows: neighbours, or the gate's and the other's), up to 32 rows of x the N side, so that one token
+// costs the tensor cores N = 16.
 //
-// Roles (20 warps, 12 for tiles of few rows):
+// Bound by the weights on their way from DRAM (five stages of 32 KB a CTA): 64 tokens, 8 of 256 experts, 4096 -> 2 x 2048:
+// 403 us for 2.87 GB; the second product 212 us for 1.44 GB: the measured copy rate.  One token's eight experts, 134 MB, take 28 us (0.70 of it:
+// 128 tiles on 152 SMs, 4 us of start and end); 4096 -> 6144 for one token, 25 MB, 9.5 us: 4.3 us is what one block of a
+// single CTA takes, 2.2 more the exchange in a cluster.
+//
+// Roles (12 warps):
 //   warp 0       TMA: a block's two 128 x 128 weight tiles, and its rows of x unless they are gathered
 //                (one instruction each: issuing one takes a warp about 100 clocks);
 //   warp 1       issues the MMAs;
 //   warp 2       the factors sx sw of a block's rows, and where the tile's rows go, to shared memory;
-//   warp 3       rows of x that the lists gather, by 16-byte asynchronous copies (tile::gather4 takes an
-//                instruction for each four rows: 2900 clocks a block of 128 rows);
-//   warps 4..    take a block's sums from tensor memory (two buffers) into their f32
-//                accumulators; at the end of a tile they write it.  A group of four warps has 32 or 16 of
+//   warp 3       rows of x that the lists gather, by 16-byte asynchronous copies;
+//   warps 4..11  take a block's sums from tensor memory (two buffers) into their f32
+//                accumulators; at the end of a tile they write it.  A group of four warps has 16 of
 //                the tile's rows.
 // A CTA an SM walks the list of (expert, weight rows, rows) tiles; an expert's row tiles stand side by side, so
 // that its weights are read from DRAM once.  Where there are fewer tiles than SMs, a cluster shares a tile: each CTA takes a part of K, and
@@ -35,44 +39,39 @@ using namespace product;
 
 constexpr int kEpiWarp = 4;                          // first of the warps that take sums
 
-template <int NT> struct Cfg {
-    static constexpr int kGroups = NT >= 64 ? 4 : 2;
-    static constexpr int kCols = NT / kGroups;       // rows of x a group
-    static constexpr int kEpiWarps = 4 * kGroups, kThreads = 32 * (kEpiWarp + kEpiWarps);
-    static constexpr uint32_t kStage = 2 * kTileA + NT * 128;
-    static constexpr int kStages = NT == 32 ? 5 : 4;
-    static constexpr int kFactors = kStages + 2;     // slots of [2][NT] f32
-    // tiles whose rows are known: factors may be kFactors + 1 tiles (of one block) ahead of the one that is written
-    static constexpr int kRowSlots = kFactors + 2;
-    static constexpr uint32_t oFactor = kStages * kStage;
-    static constexpr uint32_t oRows = oFactor + kFactors * 2 * NT * 4;    // [slots][NT] rows of the output
-    static constexpr uint32_t oStage = oRows + kRowSlots * NT * 4;        // outputs: 512 bytes a warp (glu: [16][128] codes a group)
-    static constexpr uint32_t oMax = oStage + kEpiWarps * 512;            // [groups][16][4] f32 bits
-    static constexpr uint32_t oBar = oMax + kGroups * 16 * 4 * 4;
-    static constexpr uint32_t oFlag = oBar + 8 * (2 * kStages + 2 * kFactors + 2 + 1 + kGroups);
-    static constexpr uint32_t oLists = oFlag + 16;                        // first [E], rows [E], tiles before [E + 1]
-    static size_t bytes(int E) { return 1024 + oLists + (3 * (size_t)E + 1) * 4; }
-};
+constexpr int NT = 32;                               // rows of x a tile
+constexpr int kGroups = 2, kEpiWarps = 4 * kGroups, kThreads = 32 * (kEpiWarp + kEpiWarps);
+constexpr uint32_t kStage = 2 * kTileA + NT * 128;
+constexpr int kStages = 5, kFactors = kStages + 2;   // slots of [2][NT] f32
+// Tiles whose rows are known: factors may be kFactors + 1 tiles (of one block) ahead of the one that is written.
+constexpr int kRowSlots = kFactors + 2;
+constexpr uint32_t oFactor = kStages * kStage;
+constexpr uint32_t oRows = oFactor + kFactors * 2 * NT * 4;    // [slots][NT] rows of the output
+constexpr uint32_t oStage = oRows + kRowSlots * NT * 4;        // outputs: 512 bytes a warp (glu: [16][128] codes a group)
+constexpr uint32_t oMax = oStage + kEpiWarps * 512;            // [groups][16][4] f32 bits
+constexpr uint32_t oBar = oMax + kGroups * 16 * 4 * 4;
+constexpr uint32_t oFlag = oBar + 8 * (2 * kStages + 2 * kFactors + 2 + 1 + kGroups);
+constexpr uint32_t oLists = oFlag + 16;                        // first [E], rows [E], tiles before [E + 1]
+constexpr size_t smem_bytes(int E) { return 1024 + oLists + (3 * (size_t)E + 1) * 4; }
 
-template <bool GLU, int NT>
-__global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __grid_constant__ Params p) {
-    using C = Cfg<NT>;
-    constexpr int ST = C::kStages, FS = C::kFactors, G = C::kGroups, NC = C::kCols / 16;
+template <bool GLU>
+__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ Params p) {
+    constexpr int ST = kStages, FS = kFactors, G = kGroups;
     extern __shared__ uint8_t smem_raw[];
     const ProductArgs &a = p.a;
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (base - raw);
-    auto full = [&](int s) { return base + C::oBar + 8u * s; };
-    auto done = [&](int s) { return base + C::oBar + 8u * (ST + s); };
-    auto ffull = [&](int s) { return base + C::oBar + 8u * (2 * ST + s); };
-    auto fempty = [&](int s) { return base + C::oBar + 8u * (2 * ST + FS + s); };
-    auto tempty = [&](int b) { return base + C::oBar + 8u * (2 * ST + 2 * FS + b); };
-    const uint32_t drain = base + C::oBar + 8u * (2 * ST + 2 * FS + 2);
+    auto full = [&](int s) { return base + oBar + 8u * s; };
+    auto done = [&](int s) { return base + oBar + 8u * (ST + s); };
+    auto ffull = [&](int s) { return base + oBar + 8u * (2 * ST + s); };
+    auto fempty = [&](int s) { return base + oBar + 8u * (2 * ST + FS + s); };
+    auto tempty = [&](int b) { return base + oBar + 8u * (2 * ST + 2 * FS + b); };
+    const uint32_t drain = base + oBar + 8u * (2 * ST + 2 * FS + 2);
     auto together = [&](int g) { return drain + 8u * (1 + g); };
-    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + C::oFlag);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::oFlag + 4);
-    int *first = reinterpret_cast<int *>(smem + C::oLists), *count = first + a.E, *before = count + a.E;
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + oFlag);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + oFlag + 4);
+    int *first = reinterpret_cast<int *>(smem + oLists), *count = first + a.E, *before = count + a.E;
     constexpr uint32_t kCols = 4 * NT;               // two buffers of two blocks
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -83,10 +82,10 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
         }
         for (int s = 0; s < FS; ++s) {
             mbar_init(ffull(s), 1);
-            mbar_init(fempty(s), C::kEpiWarps);
+            mbar_init(fempty(s), kEpiWarps);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(tempty(b), C::kEpiWarps);
+            mbar_init(tempty(b), kEpiWarps);
         }
         mbar_init(drain, 1);
         for (int g = 0; g < G; ++g) mbar_init(together(g), 4);
@@ -101,10 +100,9 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
     }
     griddep_wait();
     griddep_launch();
-    set_lists(a, first, count, before, NT, C::kThreads);
+    set_lists(a, first, count, before, NT, kThreads);
     tc_fence_before();
     __syncthreads();
-    if (p.split > 1) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
@@ -118,8 +116,6 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
     auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, warp_wait(bar, parity & 1, abort_flag, a.err)) != 0; };
     const bool gather = GLU && a.pairs;
 
-    // 640 threads launch with 96 registers each: 128 x 64 + 512 x 104 are as many
-    if (NT >= 64 && warp < kEpiWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 0) {
         // ---- weights, and rows that stand together ----
         uint32_t it = 0;
@@ -132,7 +128,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
                 const int s = it % ST;
                 if (!(ok = wait(done(s), it / ST ^ 1))) break;
                 if (elect()) {
-                    const uint32_t at = base + s * C::kStage, bar = full(s);
+                    const uint32_t at = base + s * kStage, bar = full(s);
                     mbar_expect_tx(bar, bytes);
                     tma_weights(at, &p.mw, kb * 128, w.m0, 0, w.e, bar);
                     if (!gather) tma_rows(at + 2 * kTileA, few ? &p.mx16 : &p.mx, kb * 128, w.row, bar);
@@ -160,7 +156,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
                 const int s = it % ST, b = it & 1;
                 if (!(ok = wait(tempty(b), it >> 1 ^ 1) && wait(full(s), it / ST))) break;
                 tc_fence_after();
-                const uint32_t at = base + s * C::kStage, d = tmem + b * 2 * NT;
+                const uint32_t at = base + s * kStage, d = tmem + b * 2 * NT;
                 const uint64_t d0 = sdesc(at), d1 = sdesc(at + kTileA), db = sdesc(at + 2 * kTileA);
                 if (elect()) {
 #pragma unroll
@@ -183,40 +179,28 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
         __syncwarp();
     } else if (warp == 2) {
         // ---- factors ----
-        constexpr int NV = NT / 32;
         const bool vec_x = four_at_once(a.x_scales, a.x_fmt, p.KB);
         const bool vec_w = four_at_once(a.w_scales, a.w_fmt, p.KB);
         uint32_t it = 0, slot = 0;
         bool ok = true;
-        for (int t = t0; t < tiles && ok; t += t_step, slot = slot + 1 == C::kRowSlots ? 0 : slot + 1) {
+        for (int t = t0; t < tiles && ok; t += t_step, slot = slot + 1 == kRowSlots ? 0 : slot + 1) {
             const TileAt w = tile_at(t);
             const bool both = two(w);
-            int *rows = reinterpret_cast<int *>(smem + C::oRows) + slot * NT;
-            int xi[NV];
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int c = v * 32 + lane;
-                xi[v] = c < w.n ? gather ? token_of(a, w.row + c) : w.row + c : -1;
-                const int r = c >= w.n ? -1 : GLU || !a.pairs ? w.row + c : out_row_of(a, w.row + c);
-                rows[c] = r;
-            }
+            int *rows = reinterpret_cast<int *>(smem + oRows) + slot * NT;
+            const int xi = lane < w.n ? gather ? token_of(a, w.row + lane) : w.row + lane : -1;
+            rows[lane] = lane >= w.n ? -1 : GLU || !a.pairs ? w.row + lane : out_row_of(a, w.row + lane);
             const int64_t w0 = ((int64_t)w.e * (GLU ? 2 : 1) * p.NB + w.m0 / kM) * p.KB, w1 = w0 + (int64_t)(GLU ? p.NB : 1) * p.KB;
             // the next four blocks' scales are on their way while these are written
-            uint4 next_x[NV], next_w[2];
+            uint4 next_x, next_w[2];
             auto fetch = [&](int kb4) {
                 const int left = p.KB - kb4;
-#pragma unroll
-                for (int v = 0; v < NV; ++v)
-                    if (xi[v] >= 0) next_x[v] = load_scales(a.x_scales, a.x_fmt, vec_x, (int64_t)xi[v] * p.KB + kb4, left);
+                if (xi >= 0) next_x = load_scales(a.x_scales, a.x_fmt, vec_x, (int64_t)xi * p.KB + kb4, left);
                 next_w[0] = load_scales(a.w_scales, a.w_fmt, vec_w, w0 + kb4, left);
                 if (both) next_w[1] = load_scales(a.w_scales, a.w_fmt, vec_w, w1 + kb4, left);
             };
             fetch(kb0 & ~3);
             for (int kb4 = kb0 & ~3; kb4 < kb1 && ok; kb4 += 4) {
-                uint4 x[NV];
-#pragma unroll
-                for (int v = 0; v < NV; ++v) x[v] = next_x[v];
-                const uint4 s0 = next_w[0], s1 = both ? next_w[1] : s0;
+                const uint4 x = next_x, s0 = next_w[0], s1 = both ? next_w[1] : s0;
                 if (kb4 + 4 < kb1) fetch(kb4 + 4);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -224,14 +208,11 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
                     if (kb < kb0 || kb >= kb1 || !ok) continue;
                     const int s = it % FS;
                     if (!(ok = wait(fempty(s), it / FS ^ 1))) continue;
-                    float *f = reinterpret_cast<float *>(smem + C::oFactor) + s * 2 * NT + lane;
+                    float *f = reinterpret_cast<float *>(smem + oFactor) + s * 2 * NT + lane;
                     const float g0 = scale_at(s0, a.w_fmt, vec_w, j), g1 = scale_at(s1, a.w_fmt, vec_w, j);
-#pragma unroll
-                    for (int v = 0; v < NV; ++v) {
-                        const float sx = xi[v] >= 0 ? scale_at(x[v], a.x_fmt, vec_x, j) : 0.f;
-                        f[v * 32] = sx * g0;
-                        f[NT + v * 32] = sx * g1;
-                    }
+                    const float sx = xi >= 0 ? scale_at(x, a.x_fmt, vec_x, j) : 0.f;
+                    f[0] = sx * g0;
+                    f[NT] = sx * g1;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(ffull(s));
                     ++it;
@@ -263,7 +244,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
                 const bool real = kb * 128 + chunk * 16 < a.K;
                 const uint8_t *src = a.x + (real ? kb * 128 + chunk * 16 : 0);
                 // rows r0 and r0 + 4 of each 8: a chunk's place is turned by the row's last three bits
-                const uint32_t at = base + s * C::kStage + 2 * kTileA + r0 * 128, lo = (chunk ^ r0) * 16, hi = (chunk ^ (r0 + 4)) * 16 + 512;
+                const uint32_t at = base + s * kStage + 2 * kTileA + r0 * 128, lo = (chunk ^ r0) * 16, hi = (chunk ^ (r0 + 4)) * 16 + 512;
 #pragma unroll
                 for (int i = 0; i < NT / 8; ++i) {
                     if (i >= n8) break;
@@ -282,7 +263,6 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
         __syncwarp();
     } else {
         // ---- sums and output ----
-        if (NT >= 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         const int g = (warp - kEpiWarp) >> 2, q = warp & 3, m = 32 * q + lane, tw = threadIdx.x & 127;
         const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
         uint32_t it = 0, slot = 0, syncs = 0;
@@ -295,8 +275,8 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
         // Writes rows c0 .. c0 + n - 1 of tile w, n <= 16: v0, v1 the sums of weight rows m of its two blocks.  False: a wait ran out.
         auto finish = [&](const TileAt &w, float (&v0)[16], float (&v1)[16], int c0, int n) {
             if (GLU) {
-                uint32_t *amax = reinterpret_cast<uint32_t *>(smem + C::oMax) + g * 64;
-                uint8_t *codes = smem + C::oStage + g * 2048;
+                uint32_t *amax = reinterpret_cast<uint32_t *>(smem + oMax) + g * 64;
+                uint8_t *codes = smem + oStage + g * 2048;
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     v0[j] = gated(v0[j], v1[j], a.limit);
@@ -329,7 +309,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
                 }
                 return group_sync();                                // before the next chunk's
             } else {
-                const int *rows = reinterpret_cast<const int *>(smem + C::oRows) + slot * NT + c0;
+                const int *rows = reinterpret_cast<const int *>(smem + oRows) + slot * NT + c0;
                 const int col = w.m0 + m;
                 if (a.out_type == ENGRAM_T_F32) {
 #pragma unroll
@@ -342,7 +322,7 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
                     return true;
                 }
                 // 16-bit: this warp's 32 weight rows of 8 rows of x through shared memory, 16 bytes a lane to global
-                uint16_t *stage = reinterpret_cast<uint16_t *>(smem + C::oStage + (warp - kEpiWarp) * 512);
+                uint16_t *stage = reinterpret_cast<uint16_t *>(smem + oStage + (warp - kEpiWarp) * 512);
                 const bool bf = a.out_type == ENGRAM_T_BF16;
                 auto put = [&](const float (&v)[16], int first_col) {
                     const int at = (lane & 3) * 8, left = a.N - first_col - at;   // of this lane's eight columns
@@ -377,37 +357,30 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
             }
         };
         bool ok = true;
-        for (int t = t0; t < tiles && ok; t += t_step, slot = slot + 1 == C::kRowSlots ? 0 : slot + 1) {
+        for (int t = t0; t < tiles && ok; t += t_step, slot = slot + 1 == kRowSlots ? 0 : slot + 1) {
             const TileAt w = tile_at(t);
             const bool both = two(w);
-            uint64_t acc0[NC][8], acc1[NC][8];
+            uint64_t acc0[8], acc1[8];
 #pragma unroll
-            for (int i = 0; i < NC; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) acc0[i][j] = acc1[i][j] = 0;
+            for (int j = 0; j < 8; ++j) acc0[j] = acc1[j] = 0;
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
                 const int b = it & 1, s = it % FS;
                 if (!(ok = wait(ffull(s), it / FS) && wait(done(it % ST), it / ST))) break;
                 tc_fence_after();
-                const float *f = reinterpret_cast<const float *>(smem + C::oFactor) + s * 2 * NT;
+                const float *f = reinterpret_cast<const float *>(smem + oFactor) + s * 2 * NT;
                 const uint32_t d = lanes + b * 2 * NT;
-                auto load = [&](uint32_t at, uint32_t (&u)[NC][16]) {
-#pragma unroll
-                    for (int i = 0; i < NC; ++i) tmem_ld16(at + 16 * i, u[i]);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < NC; ++i) pin16(u[i]);
-                };
                 // rows behind the tile's last are added up, too: nobody reads their sums
-                if (g * C::kCols < w.n) {
-                    uint32_t u[NC][16];
-                    load(d + g * C::kCols, u);
-#pragma unroll
-                    for (int i = 0; i < NC; ++i) add_chunk(acc0[i], u[i], f + g * C::kCols + 16 * i);
+                if (g * 16 < w.n) {
+                    uint32_t u[16];
+                    tmem_ld16(d + g * 16, u);
+                    tmem_wait_ld();
+                    pin16(u);
+                    add_chunk(acc0, u, f + g * 16);
                     if (both) {
-                        load(d + NT + g * C::kCols, u);
-#pragma unroll
-                        for (int i = 0; i < NC; ++i) add_chunk(acc1[i], u[i], f + NT + g * C::kCols + 16 * i);
+                        tmem_ld16(d + NT + g * 16, u);
+                        tmem_wait_ld();
+                        pin16(u);
+                        add_chunk(acc1, u, f + NT + g * 16);
                     }
                 }
                 tc_fence_before();
@@ -418,15 +391,13 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
                 }
             }
             if (!ok) break;
-#pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                const int c0 = g * C::kCols + 16 * i;
-                if (c0 >= w.n || !ok) break;
+            const int c0 = g * 16;
+            if (c0 < w.n) {
                 float v0[16], v1[16];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    unpack2(acc0[i][j], v0[2 * j], v0[2 * j + 1]);
-                    unpack2(acc1[i][j], v1[2 * j], v1[2 * j + 1]);
+                    unpack2(acc0[j], v0[2 * j], v0[2 * j + 1]);
+                    unpack2(acc1[j], v1[2 * j], v1[2 * j + 1]);
                 }
                 if (p.split == 1) {
                     ok = finish(w, v0, v1, c0, min(16, w.n - c0));
@@ -479,15 +450,14 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, 1) product_kernel(const __g
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols) : "memory");
 }
 
-template <bool GLU, int NT>
+template <bool GLU>
 cudaError_t launch_tile(Params &p, cudaStream_t s) {
-    using C = Cfg<NT>;
     const ProductArgs &a = p.a;
     static Fit fit[64] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!fit[dev].ready) {
-        const cudaError_t e = make_fit(&fit[dev], product_kernel<GLU, NT>, C::kThreads, C::bytes(kMaxExperts));
+        const cudaError_t e = make_fit(&fit[dev], product_kernel<GLU>, kThreads, smem_bytes(kMaxExperts));
         if (e != cudaSuccess) return e;
     }
     const uint64_t xd[2] = {(uint64_t)a.K, (uint64_t)a.rows}, xst[1] = {(uint64_t)a.x_stride};
@@ -500,7 +470,7 @@ cudaError_t launch_tile(Params &p, cudaStream_t s) {
     // row tiles of a dense product side by side whose rows stay in L2
     const int64_t rows_l2 = (int64_t(48) << 20) / a.K / NT;
     p.group = (int)(rows_l2 < 8 ? 8 : rows_l2 > 0x3FFFFFFF ? 0x3FFFFFFF : rows_l2);
-    return launch_split(product_kernel<GLU, NT>, p, tiles, C::kThreads, C::bytes(a.E), s);
+    return launch_split(product_kernel<GLU>, p, tiles, kThreads, smem_bytes(a.E), s);
 }
 
 }  // namespace
@@ -517,13 +487,11 @@ cudaError_t launch_product(const ProductArgs &a, cudaStream_t s) {
     const uint64_t row = (uint64_t)a.out_stride * (a.glu ? 1 : a.out_type == ENGRAM_T_F32 ? 4 : 2);
     const uint64_t either = row | reinterpret_cast<uintptr_t>(a.out);
     p.wide = either % 32 == 0 ? 2 : either % 16 == 0 ? 1 : 0;
-    // Many rows: tiles of 128 rows and 256 weight rows (shared memory bounds this kernel at three times the MMA's time a
-    // block: 8192 x 4096 -> 6144 took 324 us with it).  Few rows an expert: a tile of few rows leaves shared memory to the
-    // weights on their way.
+    // rows (an expert, on average).  8 of 64 experts, 4096 -> 2 x 1024: at 16 rows 92 us here, 103 (weights' scales in 32 bits) or 91 with
+    // tiles of 128 rows; at 32 rows 104 and 92; at 64, 125 (tiles of 64 rows here) and 103.
     const int rows = a.offsets ? (a.n_pairs + a.E - 1) / a.E : a.n_pairs;
-    if (rows > 64) return launch_product_rows(p, s);
-    if (a.glu) return rows <= 24 ? launch_tile<true, 32>(p, s) : launch_tile<true, 64>(p, s);
-    return rows <= 24 ? launch_tile<false, 32>(p, s) : launch_tile<false, 64>(p, s);
+    if (rows > 24) return launch_product_rows(p, s);
+    return a.glu ? launch_tile<true>(p, s) : launch_tile<false>(p, s);
 }
 
 int product_row_tiles(const ProductArgs &a, int rows) {

@@ -123,59 +123,76 @@ __device__ __forceinline__ uint32_t four_bytes(const void *p, bool vec, int64_t 
     return r;
 }
 
-// The part of CTA `rank` of a cluster that shares tile w: 128 / split of its rows, from all CTAs' sums, added in CTA order.  Thread i of
-// 256: a row, and a slice of the columns.
-template <bool GLU, class Sync>
+// The part of CTA `rank` of a cluster of S that shares tile w: 128 / S of its rows, from all CTAs' sums, added in CTA order.
+// Thread i of 256: a row, and a slice of the columns, half of it (64 loads from the others' shared memory) at a time.
+template <bool GLU, int S, class Sync>
 __device__ __forceinline__ void share_of_tile(const Params &p, const TileAt &w, uint32_t base, uint8_t *smem, int rank, int i, Sync together) {
+    constexpr int kPer = kRows / S, kSlices = 2 * S, kWidth = (GLU ? kM : kCols) / kSlices, kStep = kWidth / 2;
     const ProductArgs &a = p.a;
-    const int rows = kRows / p.split, row = rank * rows + i % rows, slice = i / rows;
-    const int per = (GLU ? kM : kCols) / (2 * p.split), c0 = slice * per;   // columns of a slice: 8 to 64
+    const int row = rank * kPer + i % kPer, slice = i / kPer, c0 = slice * kWidth;
     int to = row < w.n ? w.row + row : -1;
     if (!GLU && a.pairs && to >= 0) to = out_row_of(a, to);
-    auto sum8 = [&](int c, float (&v)[8]) {
-        uint32_t at[8];
+    auto sums = [&](int c, float (&v)[kStep]) {
+        float x[S][kStep];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) at[j] = (uint32_t)((c + j) * kRows + row) * 4;
-        sum_of_cluster(base, p.split, at, 8, v);
+        for (int r = 0; r < S; ++r) {
+            const uint32_t at = mapa(base, (uint32_t)r) + (uint32_t)(c * kRows + row) * 4;
+#pragma unroll
+            for (int j = 0; j < kStep; ++j) x[r][j] = lds_cluster(at + j * kRows * 4);
+        }
+#pragma unroll
+        for (int j = 0; j < kStep; ++j) {
+            v[j] = x[0][j];
+#pragma unroll
+            for (int r = 1; r < S; ++r) v[j] += x[r][j];
+        }
     };
     if (!GLU) {
         if (to < 0) return;
-        for (int c = c0; c < c0 + per && w.m0 + c < a.N; c += 8) {
-            float v[8];
-            sum8(c, v);
-            const int64_t at = (int64_t)to * a.out_stride + w.m0 + c;
-            const bool whole = p.wide && w.m0 + c + 8 <= a.N;
-            if (whole && a.out_type == ENGRAM_T_BF16) {
-                store8<ENGRAM_T_BF16>(a.out, at, v);
-            } else if (whole && a.out_type == ENGRAM_T_F16) {
-                store8<ENGRAM_T_F16>(a.out, at, v);
-            } else if (whole) {
-                store8<ENGRAM_T_F32>(a.out, at, v);
-            } else {
+#pragma unroll 1
+        for (int c = c0; c < c0 + kWidth && w.m0 + c < a.N; c += kStep) {
+            float v[kStep];
+            sums(c, v);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (w.m0 + c + j >= a.N) break;
-                    if (a.out_type == ENGRAM_T_BF16)
-                        static_cast<__nv_bfloat16 *>(a.out)[at + j] = __float2bfloat16_rn(v[j]);
-                    else if (a.out_type == ENGRAM_T_F16)
-                        static_cast<__half *>(a.out)[at + j] = __float2half_rn(v[j]);
-                    else
-                        static_cast<float *>(a.out)[at + j] = v[j];
+            for (int j = 0; j < kStep; j += 8) {
+                const int col = w.m0 + c + j;
+                const int64_t at = (int64_t)to * a.out_stride + col;
+                const float y[8] = {v[j % kStep], v[(j + 1) % kStep], v[(j + 2) % kStep], v[(j + 3) % kStep],
+                                    v[(j + 4) % kStep], v[(j + 5) % kStep], v[(j + 6) % kStep], v[(j + 7) % kStep]};
+                const bool whole = p.wide && col + 8 <= a.N;
+                if (whole && a.out_type == ENGRAM_T_BF16) {
+                    store8<ENGRAM_T_BF16>(a.out, at, y);
+                } else if (whole && a.out_type == ENGRAM_T_F16) {
+                    store8<ENGRAM_T_F16>(a.out, at, y);
+                } else if (whole) {
+                    store8<ENGRAM_T_F32>(a.out, at, y);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        if (col + k >= a.N) break;
+                        if (a.out_type == ENGRAM_T_BF16)
+                            static_cast<__nv_bfloat16 *>(a.out)[at + k] = __float2bfloat16_rn(y[k]);
+                        else if (a.out_type == ENGRAM_T_F16)
+                            static_cast<__half *>(a.out)[at + k] = __float2half_rn(y[k]);
+                        else
+                            static_cast<float *>(a.out)[at + k] = y[k];
+                    }
                 }
             }
         }
         return;
     }
-    // gated values of the slice (32 at most, [value][thread] behind the parts), then the row's largest over its slices
+    // gated values of the slice ([value][thread] behind the parts), then the row's largest over its slices
     float *mine = reinterpret_cast<float *>(smem + kCols * kRows * 4) + i;
     uint32_t *amax = reinterpret_cast<uint32_t *>(smem + oMax);       // [slices][rows], 256 in all
     float big = 0.f;
-    for (int c = c0; c < c0 + per; c += 8) {
-        float g[8], u[8];
-        sum8(c, g);
-        sum8(kM + c, u);
+#pragma unroll 1
+    for (int c = c0; c < c0 + kWidth; c += kStep) {
+        float g[kStep], u[kStep];
+        sums(c, g);
+        sums(kM + c, u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < kStep; ++j) {
             g[j] = gated(g[j], u[j], a.limit);
             big = amax3(big, g[j], 0.f);
             mine[(c - c0 + j) * 256] = g[j];
@@ -184,10 +201,11 @@ __device__ __forceinline__ void share_of_tile(const Params &p, const TileAt &w, 
     amax[i] = __float_as_uint(big);
     if (!together() || to < 0) return;
     uint32_t most = 0;
-    for (int s = 0; s < 2 * p.split; ++s) most = max(most, amax[s * rows + i % rows]);
+#pragma unroll
+    for (int s = 0; s < kSlices; ++s) most = max(most, amax[s * kPer + i % kPer]);
     const uint32_t byte = block_scale_byte(most);
     const float inv = byte == 255u ? 0.f : inv_scale(byte);
-    for (int c = c0; c < c0 + per && w.m0 + c < a.N; c += 8) {
+    for (int c = c0; c < c0 + kWidth && w.m0 + c < a.N; c += 8) {
         uint2 code = make_uint2(0u, 0u);
         if (byte != 255u) {
             const float *v = mine + (c - c0) * 256;
@@ -256,7 +274,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
     set_lists(a, first, count, before, kRows, kThreads);
     tc_fence_before();
     __syncthreads();
-    if (p.split > 1) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
@@ -633,11 +650,21 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
         __syncwarp();
         if (p.split > 1) {
             cluster_sync();
-            if (t0 < tiles && ok) share_of_tile<GLU>(p, tile_at(t0), base, smem, rank, threadIdx.x - 32 * kEpiWarp, [&]() {
+            auto all_meet = [&]() {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(together);
                 return wait(together, 0);
-            });
+            };
+            if (t0 < tiles && ok) {
+                const TileAt w = tile_at(t0);
+                const int i = threadIdx.x - 32 * kEpiWarp;
+                if (p.split == 2)
+                    share_of_tile<GLU, 2>(p, w, base, smem, rank, i, all_meet);
+                else if (p.split == 4)
+                    share_of_tile<GLU, 4>(p, w, base, smem, rank, i, all_meet);
+                else
+                    share_of_tile<GLU, 8>(p, w, base, smem, rank, i, all_meet);
+            }
             cluster_sync();
         }
     }

@@ -572,7 +572,8 @@ int engram_project_fp8(const uint8_t *d_x, int64_t x_stride, const void *d_x_sca
  * ceil(n / 128)], out_fmt ENGRAM_FMT_FP8 (f32) or ENGRAM_FMT_FP8_E8M0 (bytes).
  * lists NULL: output row r from x row r.  Otherwise rows == lists->tokens, and
  * output row p is that of pair pairs[p]: x row pairs[p] / top_k, expert p's matrices; rows behind
- * offsets[n_experts] are not written.  x: as above.  limit: 0 (none) or finite and > 0. */
+ * offsets[n_experts] are not written.  x: as above (gathered: under 2^36 bytes, else
+ * ENGRAM_E_UNSUPPORTED).  limit: 0 (none) or finite and > 0. */
 int engram_glu_fp8(const uint8_t *d_x, int64_t x_stride, const void *d_x_scales, int32_t x_fmt, int32_t rows,
                    const engram_fp8_weight *w, const engram_expert_lists *lists, float limit, int32_t out_fmt,
                    uint8_t *d_out, void *d_out_scales, uintptr_t stream);
