@@ -67,12 +67,6 @@ template <class Key> struct Real;
 template <> struct Real<uint32_t> { using type = float; };
 template <> struct Real<uint64_t> { using type = double; };
 
-// Whether two scores that order experts e and f by their 32-bit values are too near to do so: not if they are equal for being
-// formed of the same numbers.
-__device__ __forceinline__ bool unsure(const RouteArgs &a, int64_t row, float x, float y, int e, int f) {
-    return !(load_logit(a, row * a.stride + e) == load_logit(a, row * a.stride + f) && a.bias[e] == a.bias[f]);
-}
-
 // How lanes hold a row's experts, and groups their lanes.
 struct Shape {
     int c;                              // experts a lane
@@ -151,31 +145,44 @@ __device__ __forceinline__ void mask_groups(const Shape &sh, unsigned kept, int 
 }
 
 // The top_k of the keys of which a lane's largest that is left is `m`, of its expert `at`; next(): the lane takes it out.  Lane j gets
-// id j (-1: none).  CHECK: false where 32 bits leave a doubt; `least` is the key behind the last choice.
+// id j (-1: none).  CHECK: false where 32 bits leave a doubt about the order of two choices, or of the last and `least`, the key
+// behind it -- not where two are equal for being formed of the same numbers.
 template <bool CHECK, class Key, class Next>
 __device__ __forceinline__ bool choose(const RouteArgs &a, const Shape &sh, int64_t row, Key &m, int &at, Next next, bool exact,
                                        int lane, int &id, Key &least) {
-    using T = typename Real<Key>::type;
-    bool sure = true;
+    const int k = a.r.top_k;
     id = -1;
-    int before = -1;
-    T last = 0;
-    for (int j = 0; j <= a.r.top_k; ++j) {
+    Key mine = 0;
+    int behind = -1;
+    least = 0;
+    for (int j = 0;; ++j) {
         const Key top = warp_max(m);
         if (!top) break;
-        least = top;
-        const T x = of_key(top);
-        const int from = __ffs(__ballot_sync(kAll, m == top)) - 1;   // lower lanes hold lower experts
-        const int e = __shfl_sync(kAll, lane * sh.c + at, from);
-        if (CHECK && !exact && before >= 0 && last - x <= (T)kTol * fmax((T)1, fabs(last)))
-            if (unsure(a, row, (float)last, (float)x, before, e)) sure = false;
-        if (j == a.r.top_k) break;
-        last = x;
-        before = e;
+        const bool from = m == top;
+        const unsigned who = __ballot_sync(kAll, from);
+        const int first = __ffs(who) - 1;                // lower lanes hold lower experts
+        const int e = __shfl_sync(kAll, lane * sh.c + at, first);
+        if (j == k) {
+            least = top;
+            behind = e;
+            break;
+        }
         id = lane == j ? e : id;
-        next(lane == from);
+        mine = lane == j ? top : mine;
+        next(lane == first);
     }
-    return sure;
+    if (!CHECK || exact) return true;
+    Key after = __shfl_down_sync(kAll, mine, 1);
+    int other = __shfl_down_sync(kAll, id, 1);
+    after = lane == k - 1 ? least : after;
+    other = lane == k - 1 ? behind : other;
+    bool doubt = false;
+    if (lane < k && mine && after) {
+        const float x = (float)of_key(mine), y = (float)of_key(after);
+        doubt = x - y <= kTol * fmaxf(1.f, fabsf(x));
+        if (doubt) doubt = !(load_logit(a, row * a.stride + id) == load_logit(a, row * a.stride + other) && a.bias[id] == a.bias[other]);
+    }
+    return !__any_sync(kAll, doubt);
 }
 // The same on keys in registers, unsorted.
 template <bool CHECK, class Key, int NV>
@@ -211,6 +218,7 @@ __device__ __forceinline__ bool one_a_lane(const Shape &sh, unsigned want, int l
     const int total = __shfl_sync(kAll, upto, 31);
     e = -1;
     if (total > 32) return false;
+#pragma unroll 1
     for (int i = 0; i < total; ++i) {
         // the lane whose marks reach past i
         const int from = __ffs(__ballot_sync(kAll, upto > i)) - 1;
@@ -274,7 +282,8 @@ __device__ __forceinline__ uint32_t group_key32(const RouteArgs &a, bool soft, u
     return !key || a.bias || a.r.group_best == 1 ? key : key_of(score32(soft, of_key(key), top, sum));
 }
 
-// What follows is called for about one row in a thousand; it forms the row's numbers anew, so that they stay in registers elsewhere.
+// What follows is called for about one row in some thousands; it forms the row's numbers anew, so that they stay in registers
+// elsewhere.
 // The 32-bit keys of row `row`.
 template <int NV>
 __device__ __forceinline__ void keys_again(const RouteArgs &a, const Shape &sh, int64_t row, int lane, float top, float sum,
@@ -334,23 +343,37 @@ __device__ __noinline__ unsigned groups_again(const RouteArgs &a, int64_t row, i
 #pragma unroll
     for (int v = 0; v < NV; ++v) key[v] = group_key32(a, r.score == ENGRAM_SCORE_SOFTMAX, key[v], top, sum);
     unsigned want = 0;
-    for (int g = 0; g < r.n_groups; ++g) {
-        const int lo = g * sh.size - lane * sh.c, hi = lo + sh.size;
-        uint32_t first = 0, second = 0;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) two_best(first, second, v >= lo && v < hi ? key[v] : 0u, 0u);
-        two_best_of_lanes(first, second, 32);
+    // of keys at lo .. hi - 1 those that may be among the group's two largest, of which the 32-bit ones are first and second
+    auto mark = [&](int lo, int hi, uint32_t first, uint32_t second) {
         const uint32_t low = second && r.group_best == 2 ? second : first;
-        if (!low) continue;
+        if (!low) return;
         const float x = of_key(low), from = x - kTol * fmaxf(1.f, fabsf(x));
 #pragma unroll
         for (int v = 0; v < NV; ++v)
             if (v >= lo && v < hi && key[v] && of_key(key[v]) >= from) want |= 1u << v;
+    };
+    if (sh.lanes) {
+        uint32_t first = 0, second = 0;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) two_best(first, second, key[v], 0u);
+        two_best_of_lanes(first, second, sh.lanes);
+        mark(0, NV, first, second);
+    } else {
+#pragma unroll 1
+        for (int g = 0; g < r.n_groups; ++g) {
+            const int lo = g * sh.size - lane * sh.c, hi = lo + sh.size;
+            uint32_t first = 0, second = 0;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) two_best(first, second, v >= lo && v < hi ? key[v] : 0u, 0u);
+            two_best_of_lanes(first, second, 32);
+            mark(lo, hi, first, second);
+        }
     }
     int e;
     if (!one_a_lane(sh, want, lane, e)) return 0;
     const uint64_t mine = e >= 0 ? key_of(score64(a, row, e, top)) : 0;
     uint64_t sums = 0;                               // lane g: group g's
+#pragma unroll 1
     for (int g = 0; g < r.n_groups; ++g) {
         uint64_t x = e >= 0 && e / sh.size == g ? mine : 0;
         const uint64_t first = warp_max(x);
@@ -377,6 +400,7 @@ __device__ __noinline__ int experts_again(const RouteArgs &a, int64_t row, int l
     int e, id = -1;
     if (!one_a_lane(sh, want, lane, e)) return -2;
     uint64_t mine = e >= 0 ? key_of(score64(a, row, e, top)) : 0;
+#pragma unroll 1
     for (int j = 0; j < a.r.top_k; ++j) {
         const uint64_t most = warp_max(mine);
         if (!most) break;
@@ -461,15 +485,23 @@ __device__ __forceinline__ int route_row(const RouteArgs &a, const Shape &sh, co
             settle_groups(lane < r.n_groups ? mine : 0u);
             const bool out = !(kept >> min(31, lane / sh.lanes) & 1);
 #pragma unroll
-            for (int v = 0; v < NV; ++v) s[v] = out ? 0 : s[v];
+            for (int v = 0; v < NV; ++v) s[v] = out ? (uint32_t)s[v] : s[v];
         }
-        uint32_t m = (uint32_t)(s[0] >> 32);
-        int at = NV - 1 - (int)(uint32_t)s[0];
+        // keys in order, their places four bits each
+        uint32_t order = 0;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            key[v] = (uint32_t)(s[v] >> 32);
+            order |= (NV - 1 - (uint32_t)s[v]) << (4 * v);
+        }
+        uint32_t m = key[0];
+        int at = order & 15;
         auto next = [&](bool mine) {
 #pragma unroll
-            for (int v = 0; v < NV; ++v) s[v] = mine ? v + 1 < NV ? s[(v + 1) % NV] : 0 : s[v];
-            m = (uint32_t)(s[0] >> 32);
-            at = NV - 1 - (int)(uint32_t)s[0];
+            for (int v = 0; v < NV; ++v) key[v] = mine ? v + 1 < NV ? key[(v + 1) % NV] : 0 : key[v];
+            order = mine ? order >> 4 : order;
+            m = key[0];
+            at = order & 15;
         };
         chosen = choose<true>(a, sh, row, m, at, next, exact, lane, id, least);
     } else {
@@ -499,9 +531,9 @@ __device__ __forceinline__ int route_row(const RouteArgs &a, const Shape &sh, co
 // Tokens of warp `w` of block b.
 __device__ __forceinline__ void warp_tokens(const RouteArgs &a, int b, int blocks, int w, int64_t &lo, int64_t &hi) {
     const int warps = blockDim.x >> 5;
-    const int64_t n = (int64_t)blocks * warps, i = (int64_t)b * warps + w;
-    lo = a.tokens * i / n;
-    hi = a.tokens * (i + 1) / n;
+    const int64_t first = (int64_t)a.tokens * b / blocks, n = (int64_t)a.tokens * (b + 1) / blocks - first;
+    lo = first + n * w / warps;
+    hi = first + n * (w + 1) / warps;
 }
 
 // Exclusive sums over `n` values of v[], all threads of the block; v[n] gets the total.  part: 32 ints.
@@ -622,7 +654,7 @@ __global__ void __launch_bounds__(1024) route_lists_kernel(const RouteArgs a) {
     for (int i = tid; i < parts * E; i += blockDim.x) {
         const int e = i % E, part_no = i / E;
         int n = 0, sum = 0;
-#pragma unroll 8
+#pragma unroll 19
         for (int b = blocks * part_no / parts; b < blocks * (part_no + 1) / parts; ++b) {
             const int c = a.ws[(int64_t)b * E + e];
             n += b < (int)blockIdx.x ? c : 0;
@@ -694,8 +726,10 @@ cudaError_t launch_route(const RouteArgs &a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(32 * warps);
-    cfg.dynamicSmemBytes = smem_bytes(E, warps);
+    // a block's tokens do not depend on its warps; the more blocks, the more threads share their counts
+    const int list_warps = blocks > 32 ? 32 : warps;
+    cfg.blockDim = dim3(32 * list_warps);
+    cfg.dynamicSmemBytes = smem_bytes(E, list_warps);
     cfg.stream = s;
     cudaLaunchAttribute la[1];
     la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
