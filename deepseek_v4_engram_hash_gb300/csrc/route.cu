@@ -23,8 +23,10 @@ namespace {
 constexpr int kOneBlock = 32;                        // tokens up to which one block does all
 constexpr int kBlocks = 152;                         // blocks at most of the others
 constexpr unsigned kAll = 0xFFFFFFFFu;
-// A 32-bit score is within 4e-7 max(1, |c|) of the 64-bit one: exp and the quotient (2 ulp each, an addition) are off by
-// 5 x 2^-24 of s <= 1 at most, the sum with the bias by 2^-24 |c|; a softmax adds 2^-24 |l - max| e^(l - max) <= 2^-25.  Two of them, and sums of two, differ by twice that.
+// A 32-bit score that orders experts is within 4e-7 max(1, |c|) of the 64-bit one.  e = __expf(-l) is off by 2^-22 + 2^-23 |l| of itself, which moves
+// s = 1 / (1 + e) by s (1 - s) of that, under 2^-23; 1 + e and the reciprocal (1 ulp) by 2^-24 + 2^-23 of s; the sum with the
+// bias by 2^-24 |c|.  Softmax: e^(l - max) by 2^-22 + 2^-22 |l - max| of itself, under 2^-22 after all, and as much for the divisor.
+// Two of them, and sums of two, differ by twice that.
 constexpr float kTol = 1e-6f;
 
 // Warps a block: 32 with 64 registers; rows of many experts take 16 with 128.
@@ -44,7 +46,7 @@ __device__ __forceinline__ float load_logit(const RouteArgs &a, int64_t i) {
 // Keys ordered as the numbers are; 0, below all of them, means not to be chosen.  (+ 0 makes -0 the same as 0.)
 __device__ __forceinline__ uint32_t key_of(float x) {
     const uint32_t u = __float_as_uint(x + 0.f);
-    return u ^ ((int)u < 0 ? 0xFFFFFFFFu : 0x80000000u);
+    return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float of_key(uint32_t k) {
     return __uint_as_float((int)k < 0 ? k ^ 0x80000000u : ~k);
@@ -273,29 +275,52 @@ __device__ __forceinline__ bool wide_rows(const RouteArgs &a) {
 __device__ __forceinline__ float score32(bool soft, float x, float top, float sum) {
     return soft ? __fdividef(expf(x - top), sum) : __fdividef(1.f, 1.f + expf(-x));
 }
-// The key of a logit (0 for a masked one), and of the value that orders groups.
-__device__ __forceinline__ uint32_t key32(const RouteArgs &a, bool soft, float l, float bias, float top, float sum) {
-    if (l == -INFINITY) return 0u;
-    return key_of(a.bias ? score32(soft, l, top, sum) + bias : l);
+__device__ __forceinline__ float reciprocal(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
-__device__ __forceinline__ uint32_t group_key32(const RouteArgs &a, bool soft, uint32_t key, float top, float sum) {
-    return !key || a.bias || a.r.group_best == 1 ? key : key_of(score32(soft, of_key(key), top, sum));
+// The same, of few instructions, to order by (see kTol); of sum its reciprocal.
+__device__ __forceinline__ float quick_score(bool soft, float x, float top, float per_sum) {
+    return soft ? __expf(x - top) * per_sum : reciprocal(1.f + __expf(-x));
+}
+// The value that orders groups, of a key.
+__device__ __forceinline__ uint32_t group_key32(const RouteArgs &a, bool soft, uint32_t key, float top, float per_sum) {
+    return !key || a.bias || a.r.group_best == 1 ? key : key_of(quick_score(soft, of_key(key), top, per_sum));
+}
+// Keys of the logits l; 0 for masked ones (-inf, NaN).
+template <int NV>
+__device__ __forceinline__ void keys_of(const RouteArgs &a, bool soft, const float (&l)[NV], const float (&bias)[NV], float top, float per_sum,
+                                        uint32_t (&key)[NV]) {
+    if (!a.bias) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) key[v] = key_of(l[v]);
+    } else if (soft) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) key[v] = key_of(quick_score(true, l[v], top, per_sum) + bias[v]);
+    } else {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) key[v] = key_of(quick_score(false, l[v], top, per_sum) + bias[v]);
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) key[v] = l[v] > -INFINITY ? key[v] : 0u;
 }
 
 // What follows is called for about one row in some thousands; it forms the row's numbers anew, so that they stay in registers
 // elsewhere.
 // The 32-bit keys of row `row`.
 template <int NV>
-__device__ __forceinline__ void keys_again(const RouteArgs &a, const Shape &sh, int64_t row, int lane, float top, float sum,
+__device__ __forceinline__ void keys_again(const RouteArgs &a, const Shape &sh, int64_t row, int lane, float top, float per_sum,
                                            uint32_t (&key)[NV]) {
-    const bool soft = a.r.score == ENGRAM_SCORE_SOFTMAX;
+    float l[NV], bias[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int e = lane * sh.c + v;
         const bool real = v < sh.c && e < a.r.n_experts;
-        const float l = real ? load_logit(a, row * a.stride + e) : -INFINITY;
-        key[v] = l == l ? key32(a, soft, l, real && a.bias ? a.bias[e] : 0.f, top, sum) : 0u;
+        l[v] = real ? load_logit(a, row * a.stride + e) : -INFINITY;
+        bias[v] = real && a.bias ? a.bias[e] : 0.f;
     }
+    keys_of(a, a.r.score == ENGRAM_SCORE_SOFTMAX, l, bias, top, per_sum, key);
 }
 // The row's choices on all its scores in 64 bits.
 template <int NV>
@@ -335,13 +360,13 @@ __device__ __noinline__ int choose_all(const RouteArgs &a, int64_t row, int lane
 }
 // The groups that stay, by 64-bit scores of each group's experts that may be among its two largest.  0: too many of them.
 template <int NV>
-__device__ __noinline__ unsigned groups_again(const RouteArgs &a, int64_t row, int lane, float top, float sum) {
+__device__ __noinline__ unsigned groups_again(const RouteArgs &a, int64_t row, int lane, float top, float per_sum) {
     const Shape sh = shape_of(a.r);
     const engram_router &r = a.r;
     uint32_t key[NV];
-    keys_again(a, sh, row, lane, top, sum, key);
+    keys_again(a, sh, row, lane, top, per_sum, key);
 #pragma unroll
-    for (int v = 0; v < NV; ++v) key[v] = group_key32(a, r.score == ENGRAM_SCORE_SOFTMAX, key[v], top, sum);
+    for (int v = 0; v < NV; ++v) key[v] = group_key32(a, r.score == ENGRAM_SCORE_SOFTMAX, key[v], top, per_sum);
     unsigned want = 0;
     // of keys at lo .. hi - 1 those that may be among the group's two largest, of which the 32-bit ones are first and second
     auto mark = [&](int lo, int hi, uint32_t first, uint32_t second) {
@@ -387,10 +412,10 @@ __device__ __noinline__ unsigned groups_again(const RouteArgs &a, int64_t row, i
 // The choices among the groups `kept`, by 64-bit scores of the experts that may be among them: from `least`, the 32-bit key behind the
 // last choice, on.  -2: too many.
 template <int NV>
-__device__ __noinline__ int experts_again(const RouteArgs &a, int64_t row, int lane, float top, float sum, unsigned kept, uint32_t least) {
+__device__ __noinline__ int experts_again(const RouteArgs &a, int64_t row, int lane, float top, float per_sum, unsigned kept, uint32_t least) {
     const Shape sh = shape_of(a.r);
     uint32_t key[NV];
-    keys_again(a, sh, row, lane, top, sum, key);
+    keys_again(a, sh, row, lane, top, per_sum, key);
     if (a.r.top_groups < a.r.n_groups) mask_groups(sh, kept, lane, key);
     const float x = of_key(least), from = x - kTol * fmaxf(1.f, fabsf(x));
     unsigned want = 0;
@@ -436,37 +461,35 @@ __device__ __forceinline__ int route_row(const RouteArgs &a, const Shape &sh, co
                                          int lane) {
     const engram_router &r = a.r;
     const bool soft = r.score == ENGRAM_SCORE_SOFTMAX, grouped = r.top_groups < r.n_groups, exact = !a.bias;
-    float top = -INFINITY, sum = 0.f;
+    float top = -INFINITY, sum = 0.f, per_sum = 0.f;
     bool nan = false;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        nan |= l[v] != l[v] || (soft && l[v] == INFINITY);
-        if (l[v] != l[v]) l[v] = -INFINITY;
-    }
-    nan = __any_sync(kAll, nan);
+    for (int v = 0; v < NV; ++v) nan |= l[v] != l[v];
     if (soft) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v) top = fmaxf(top, l[v]);
+        for (int v = 0; v < NV; ++v) top = fmaxf(top, l[v]);     // NaN gives way
         top = of_key(__reduce_max_sync(kAll, key_of(top)));
+        nan |= top == INFINITY;
 #pragma unroll
-        for (int v = 0; v < NV; ++v) sum += l[v] == -INFINITY ? 0.f : expf(l[v] - top);
+        for (int v = 0; v < NV; ++v) sum += l[v] > -INFINITY ? expf(l[v] - top) : 0.f;
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+        per_sum = 1.f / sum;
     }
+    nan = __any_sync(kAll, nan);
     uint32_t key[NV], least = 0;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) key[v] = key32(a, soft, l[v], bias[v], top, sum);
+    keys_of(a, soft, l, bias, top, per_sum, key);
     // a softmax beside a bias needs its divisor in 64 bits, too: all scores
     bool all = false, sure = true;
     unsigned kept = 0xFFFFFFFFu;
     auto settle_groups = [&](uint32_t mine) {
         kept = keep_groups<true>(a, mine, exact, lane, sure);
-        if (!sure) all = (soft && a.bias) || !(kept = groups_again<NV>(a, row, lane, top, sum));
+        if (!sure) all = (soft && a.bias) || !(kept = groups_again<NV>(a, row, lane, top, per_sum));
     };
     if (grouped && (!sh.lanes || NV > 8)) {
         uint32_t group[NV];
 #pragma unroll
-        for (int v = 0; v < NV; ++v) group[v] = group_key32(a, soft, key[v], top, sum);
+        for (int v = 0; v < NV; ++v) group[v] = group_key32(a, soft, key[v], top, per_sum);
         settle_groups(group_sums(a, sh, group, lane));
         mask_groups(sh, kept, lane, key);
     }
@@ -478,8 +501,8 @@ __device__ __forceinline__ int route_row(const RouteArgs &a, const Shape &sh, co
         for (int v = 0; v < NV; ++v) s[v] = (uint64_t)key[v] << 32 | (uint32_t)(NV - 1 - v);
         sort_falling(s);
         if (grouped && sh.lanes) {
-            uint32_t first = group_key32(a, soft, (uint32_t)(s[0] >> 32), top, sum);
-            uint32_t second = NV > 1 ? group_key32(a, soft, (uint32_t)(s[NV > 1] >> 32), top, sum) : 0u;
+            uint32_t first = group_key32(a, soft, (uint32_t)(s[0] >> 32), top, per_sum);
+            uint32_t second = NV > 1 ? group_key32(a, soft, (uint32_t)(s[NV > 1] >> 32), top, per_sum) : 0u;
             two_best_of_lanes(first, second, sh.lanes);
             const uint32_t mine = __shfl_sync(kAll, sum_of(r.group_best, first, second), lane * sh.lanes & 31);
             settle_groups(lane < r.n_groups ? mine : 0u);
@@ -511,7 +534,7 @@ __device__ __forceinline__ int route_row(const RouteArgs &a, const Shape &sh, co
         if (soft)
             all = true;
         else
-            all = (id = experts_again<NV>(a, row, lane, top, sum, kept, least)) == -2;
+            all = (id = experts_again<NV>(a, row, lane, top, per_sum, kept, least)) == -2;
     }
     if (all) id = choose_all<NV>(a, row, lane);
     float s = id >= 0 ? score32(soft, load_logit(a, row * a.stride + id), top, sum) : 0.f;
