@@ -592,6 +592,12 @@ __device__ __forceinline__ void count_row(const RouteArgs &a, int *mine, int id,
     __syncwarp();
 }
 
+// Choices of four tokens from t on, one a lane.
+__device__ __forceinline__ void four_rows(const RouteArgs &a, int64_t t, int64_t hi, int lane, int (&id)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) id[i] = lane < a.r.top_k && t + i < hi ? a.ids[(t + i) * a.r.top_k + lane] : -1;
+}
+
 // counts: [warps][E] of the block's warps, turned into the first position of each; first: position of the block's first pair
 // of each expert.  Then the warp's pairs to their places.
 __device__ __forceinline__ void place_pairs(const RouteArgs &a, int *counts, const int *first, int64_t lo, int64_t hi) {
@@ -606,10 +612,14 @@ __device__ __forceinline__ void place_pairs(const RouteArgs &a, int *counts, con
     }
     __syncthreads();
     int *mine = counts + warp * E;
-    for (int64_t t = lo; t < hi; ++t) {
-        const int id = lane < k ? a.ids[t * k + lane] : -1;
-        if (id >= 0) a.pairs[mine[id]++] = (int)(t * k + lane);
-        __syncwarp();
+    for (int64_t t = lo; t < hi; t += 4) {
+        int id[4];
+        four_rows(a, t, hi, lane, id);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (id[i] >= 0) a.pairs[mine[id[i]]++] = (int)((t + i) * k + lane);
+            __syncwarp();
+        }
     }
 }
 
@@ -664,7 +674,7 @@ __global__ void __launch_bounds__(NV <= 8 ? 1024 : 512) route_kernel(const __gri
 __global__ void __launch_bounds__(1024) route_lists_kernel(const RouteArgs a) {
     extern __shared__ int smem[];
     __shared__ int part[32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, E = a.r.n_experts, k = a.r.top_k;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, E = a.r.n_experts;
     int *counts = smem, *mine = counts + warp * E, *first = counts + warps * E, *before = first + E + 1;
     int64_t lo, hi;
     warp_tokens(a, blockIdx.x, gridDim.x, warp, lo, hi);
@@ -672,6 +682,8 @@ __global__ void __launch_bounds__(1024) route_lists_kernel(const RouteArgs a) {
     for (int e = tid; e < E; e += blockDim.x) first[e] = before[e] = 0;
     __syncthreads();
     griddep_wait();
+    int id[4];
+    four_rows(a, lo, hi, lane, id);
     // the blocks' counts of an expert, by as many threads as there are for each
     const int parts = max(1, (int)blockDim.x / E), blocks = gridDim.x;
     for (int i = tid; i < parts * E; i += blockDim.x) {
@@ -686,7 +698,11 @@ __global__ void __launch_bounds__(1024) route_lists_kernel(const RouteArgs a) {
         atomicAdd(first + e, sum);                   // whole numbers: in any order
         atomicAdd(before + e, n);
     }
-    for (int64_t t = lo; t < hi; ++t) count_row(a, mine, lane < k ? a.ids[t * k + lane] : -1, lane);
+    for (int64_t t = lo; t < hi; t += 4) {
+        if (t > lo) four_rows(a, t, hi, lane, id);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) count_row(a, mine, id[i], lane);
+    }
     __syncthreads();
     block_scan(first, E, part);
     if (blockIdx.x == 0)
