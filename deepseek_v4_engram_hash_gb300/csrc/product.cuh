@@ -250,11 +250,16 @@ __device__ __forceinline__ TileAt tile_of(const Params &p, const int *first, con
     r.e = lo;
     const int nt = before[lo + 1] - before[lo];
     int i, m;
-    tile_coords(t - before[lo] * p.m_tiles, nt, p.m_tiles, min(p.group, nt), i, m);
-    const int n = count[lo];
-    const int r0 = (int)((int64_t)n * i / nt);
-    r.row = first[lo] + r0;
-    r.n = (int)((int64_t)n * (i + 1) / nt) - r0;
+    const int at = t - before[lo] * p.m_tiles;
+    if (p.group >= nt) {
+        m = (int)((unsigned)at / (unsigned)nt);
+        i = at - m * nt;
+    } else {
+        tile_coords(at, nt, p.m_tiles, p.group, i, m);
+    }
+    const int n = count[lo], each = (int)((unsigned)n / (unsigned)nt), more = n - each * nt;
+    r.row = first[lo] + i * each + min(i, more);
+    r.n = each + (i < more);
     r.m0 = m * m_rows;
     return r;
 }

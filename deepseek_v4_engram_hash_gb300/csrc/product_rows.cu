@@ -42,9 +42,14 @@ constexpr uint32_t kSlotBytes = 4 * kRows * 4 + 128;
 constexpr uint32_t kImage = 512, kScaleCols = 16;         // tensor-memory columns of a group of four blocks: 4 of rows, 8 of weights
 constexpr uint32_t kScaleTmem = kCols;                    // behind the sums
 static_assert(3 * kImage <= kSlotBytes, "images in a slot of scales");
+// What the last warps need to know of a tile: the first weight row, and where its 128 rows go (-1: nowhere).  The scales' warps, which
+// write it, are up to three groups of blocks ahead of the MMAs, and these a tile ahead of the last warps: with tiles of one group, five tiles.
+constexpr int kRecords = 6;
+constexpr uint32_t kRecordBytes = kRows * 4 + 16;
 constexpr uint32_t oScale = kStages * kStage;             // a multiple of 16
 constexpr uint32_t oMax = oScale + kSlots * kSlotBytes;   // glu: [2][2 groups][128] f32 bits
-constexpr uint32_t oBar = oMax + 2 * 2 * kRows * 4;
+constexpr uint32_t oRecord = oMax + 2 * 2 * kRows * 4;
+constexpr uint32_t oBar = oRecord + kRecords * kRecordBytes;
 constexpr uint32_t oFlag = oBar + 8 * (2 * kStages + 2 + 2 + 2 * kSlots + 1);
 constexpr uint32_t oLists = oFlag + 16;
 constexpr size_t smem_bytes(int E) { return 1024 + oLists + (3 * (size_t)E + 1) * 4; }
@@ -383,17 +388,20 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
         // ---- scales: 64 rows a warp ----
         const int c0 = (warp - kScaleWarp) * 64 + lane;
         const bool vec_x = four_at_once(a.x_scales, a.x_fmt, KB), vec_w = four_at_once(a.w_scales, a.w_fmt, KB);
-        uint32_t it = 0;
+        uint32_t it = 0, record = 0;
         bool ok = true;
-        for (int t = t0; t < tiles && ok; t += t_step) {
+        for (int t = t0; t < tiles && ok; t += t_step, record = record + 1 == kRecords ? 0 : record + 1) {
             const TileAt w = tile_at(t);
             const bool both = two(w);
+            int *to = reinterpret_cast<int *>(smem + oRecord + record * kRecordBytes);
             int xi[2];
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
                 const int c = c0 + v * 32;
                 xi[v] = c < w.n ? gather ? token_of(a, w.row + c) : w.row + c : -1;
+                to[c] = c >= w.n ? -1 : GLU || !a.pairs ? w.row + c : out_row_of(a, w.row + c);
             }
+            if (warp == kScaleWarp && lane == 0) to[kRows] = w.m0;
             const int64_t w0 = ((int64_t)w.e * (GLU ? 2 : 1) * p.NB + w.m0 / kM) * KB, w1 = w0 + (int64_t)(GLU ? p.NB : 1) * KB;
             if (MX) {
                 // this warp's images: rows of x (0 is 2^-127: rows behind the last have 1), or the two blocks of weight rows
@@ -459,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
         }
     } else if (warp < kEpiWarp) {
         // ---- gathered rows: eight lanes a row of 128 bytes, this warp's four of each 16 rows ----
-        constexpr int LAG = 2, NR = kRows / (4 * kCopyWarps);   // blocks in flight behind the newest; rows a lane
+        constexpr int LAG = 1, NR = kRows / (4 * kCopyWarps);   // blocks in flight behind the newest; rows a lane
         const int r0 = (warp - kCopyWarp) * 4 + (lane >> 3), chunk = lane & 7;
         uint32_t it = 0;
         bool ok = true;
@@ -504,12 +512,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
         // this thread's columns: 128 g .. + 127 in quarters, or 64 g .. + 63 of both parts in halves (parts in turn)
         auto column = [&](int i) { return GLU ? (i & 1) * kM + 64 * g + (i >> 1) * 32 : kM * g + 32 * i; };
         const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
-        uint32_t it = 0, turn = 0, group = 0;        // blocks, tiles, groups of scales
+        uint32_t it = 0, turn = 0, group = 0, record = 0;   // blocks, tiles, groups of scales, tiles' records
         bool ok = true;
         for (int t = t0; t < tiles && ok; t += t_step) {
-            const TileAt w = tile_at(t);
-            int to = row < w.n ? w.row + row : -1;
-            if (!GLU && a.pairs && to >= 0) to = out_row_of(a, to);
             uint64_t acc[4][16];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -585,6 +590,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
                     }
                 break;
             }
+            const int *tile = reinterpret_cast<const int *>(smem + oRecord + record * kRecordBytes);
+            const int to = tile[row], m0 = tile[kRows];
+            record = record + 1 == kRecords ? 0 : record + 1;
             if (GLU) {
                 uint32_t *amax = reinterpret_cast<uint32_t *>(smem + oMax) + (turn & 1) * 2 * kRows + row;
                 float big = 0.f;
@@ -608,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
                 const float inv = byte == 255u ? 0.f : inv_scale(byte);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int at = w.m0 + 64 * g + 32 * i;
+                    const int at = m0 + 64 * g + 32 * i;
                     if (to < 0 || at >= a.N) continue;
                     uint32_t c[8];
 #pragma unroll
@@ -627,14 +635,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
                     }
                 }
                 if (g == 0 && to >= 0) {
-                    const int64_t i = (int64_t)to * p.NB + w.m0 / kM;
+                    const int64_t i = (int64_t)to * p.NB + m0 / kM;
                     if (a.out_type == ENGRAM_FMT_FP8_E8M0)
                         static_cast<uint8_t *>(a.out_scales)[i] = (uint8_t)byte;
                     else
                         static_cast<float *>(a.out_scales)[i] = e8m0_to_f32(byte);
                 }
             } else if (to >= 0) {
-                const int at = w.m0 + kM * g, left = a.N - at;
+                const int at = m0 + kM * g, left = a.N - at;
                 const int64_t o = (int64_t)to * a.out_stride + at;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
