@@ -453,20 +453,17 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 template <bool GLU>
 cudaError_t launch_tile(Params &p, cudaStream_t s) {
     const ProductArgs &a = p.a;
-    static Fit fit[64] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!fit[dev].ready) {
-        const cudaError_t e = make_fit(&fit[dev], product_kernel<GLU>, kThreads, smem_bytes(kMaxExperts));
-        if (e != cudaSuccess) return e;
-    }
+    static Fit fits[64] = {};
+    Fit fit;
+    const cudaError_t e = fit_of(fits, product_kernel<GLU>, kThreads, smem_bytes(kMaxExperts), &fit);
+    if (e != cudaSuccess) return e;
     const uint64_t xd[2] = {(uint64_t)a.K, (uint64_t)a.rows}, xst[1] = {(uint64_t)a.x_stride};
     const uint32_t box[2] = {128, NT}, box16[2] = {128, 16};
     if (!make_map_u8(&p.mx, a.x, 2, xd, xst, box) || !make_map_u8(&p.mx16, a.x, 2, xd, xst, box16)) return cudaErrorInvalidValue;
     p.m_tiles = (a.N + (GLU ? kM : 2 * kM) - 1) / (GLU ? kM : 2 * kM);
     const int64_t tiles = (int64_t)product_row_tiles(a, NT) * p.m_tiles;
     if (tiles > 0x3FFFFFFF) return cudaErrorInvalidConfiguration;
-    p.split = fitting_split(fit[dev], tiles, p.KB / 2, false);
+    p.split = fitting_split(fit, tiles, p.KB / 2, false);
     // row tiles of a dense product side by side whose rows stay in L2
     const int64_t rows_l2 = (int64_t(48) << 20) / a.K / NT;
     p.group = (int)(rows_l2 < 8 ? 8 : rows_l2 > 0x3FFFFFFF ? 0x3FFFFFFF : rows_l2);

@@ -6,6 +6,8 @@
 #include "experts.cuh"
 #include "tcgen05.cuh"
 
+#include <mutex>
+
 namespace engram {
 
 namespace product {
@@ -278,7 +280,7 @@ __device__ __forceinline__ int out_row_of(const ProductArgs &a, int row) {
     set_err(a.err, ENGRAM_E_ROW);
     return -1;
 }
-// g / (1 + e^-g) u of the clamped g and u; NaN stays.  (The quotient is off by 2 ulp; a denominator over 2^126 gives 0.)
+// g / (1 + e^-g) u of the clamped g and u; NaN stays.  (The quotient is off by 2 ulp; a denominator over 2^126, g under -87, gives 0.)
 __device__ __forceinline__ float gated(float g, float u, float limit) {
     if (limit > 0.f) {
         g = g > limit ? limit : g;
@@ -298,8 +300,15 @@ struct Fit {
     bool ready;
     int clusters[9];
 };
-// smem: what the most experts need.
-inline cudaError_t make_fit(Fit *fit, Kernel kernel, int threads, size_t smem) {
+// The current device's of fits[64] (a kernel's, made at its first call), copied to *out.  smem: what the most experts need.
+inline cudaError_t fit_of(Fit *fits, Kernel kernel, int threads, size_t smem, Fit *out) {
+    static std::mutex mutex;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mutex);
+    Fit *fit = fits + dev;
+    *out = *fit;
+    if (fit->ready) return cudaSuccess;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     for (int s = 2; s <= 8 && e == cudaSuccess; ++s) {
         cudaLaunchConfig_t cfg = {};
@@ -315,6 +324,7 @@ inline cudaError_t make_fit(Fit *fit, Kernel kernel, int threads, size_t smem) {
         e = cudaOccupancyMaxActiveClusters(&fit->clusters[s], kernel, &cfg);
     }
     fit->ready = e == cudaSuccess;
+    *out = *fit;
     return e;
 }
 // How many CTAs share a tile (at most `most`): the most of 2..8 (powers of two) for which all clusters run at once, or 1.

@@ -566,7 +566,7 @@ int engram_project_fp8(const uint8_t *d_x, int64_t x_stride, const void *d_x_sca
 
 /* The gated product: g and u are the rows' products (as above, in f32) with the two
  * parts of a gated weight; limit > 0: g = min(g, limit), u = max(-limit, min(u, limit));
- *   a = g / (1 + exp(-g)) * u,
+ *   a = g / (1 + exp(-g)) * u  (0 for g under -87),
  * written as e4m3 codes d_out [.., n] (dense, 16-byte aligned, n % 16 == 0) with a power-of-two
  * scale for each block of 128 of a row (8-bit blocks, above), d_out_scales [..,
  * ceil(n / 128)], out_fmt ENGRAM_FMT_FP8 (f32) or ENGRAM_FMT_FP8_E8M0 (bytes).

@@ -117,6 +117,58 @@ def test_graphs_see_new_inputs_and_give_the_same_bits(E):
     _check(s, codes, scales, T)
 
 
+def test_captured_behind_copies_and_other_streams(E):
+    """A capture in which copies, and a kernel of another stream, come before the calls and behind them."""
+    s = _sublayer(seed=7)
+    T = 50
+    source = [_rows(E, T, s.dim, i) for i in (1, 2)]
+    codes, scales = (torch.empty_like(x) for x in source[0])
+    kept = torch.empty((T, s.dim), dtype=torch.bfloat16, device="cuda")
+    want = []
+    for c, sc in source:
+        want.append(s.forward(c, sc, T).clone())
+    torch.cuda.synchronize()
+    staged = [x.clone() for x in source[0]]
+    main, other = torch.cuda.Stream(), torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        codes.copy_(staged[0])
+        other.wait_stream(main)
+        with torch.cuda.stream(other):
+            scales.copy_(staged[1])
+        main.wait_stream(other)
+        y = s.forward(codes, scales, T)
+        kept.copy_(y)
+    for (c, sc), w in zip(source, want):
+        staged[0].copy_(c)
+        staged[1].copy_(sc)
+        kept.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert E.engram_check() == 0 and torch.equal(kept, w)
+
+
+def test_results_do_not_change_with_what_runs_before(E):
+    """The calls start beside the end of the kernel before them: one that writes their input late, and one that reads their output."""
+    g = rng(8)
+    rows, K, N = 96, 2048, 512
+    w = E.Fp8Weight(torch.full((1, N, K), 0x38, dtype=torch.uint8, device="cuda"),
+                    torch.full((1, N // 128, K // 128), 127, dtype=torch.uint8, device="cuda"), E.ENGRAM_FMT_FP8_E8M0, 1, N, K)
+    x = torch.zeros((rows, K), dtype=torch.uint8, device="cuda")
+    sc = torch.full((rows, K // 128), 127, dtype=torch.uint8, device="cuda")
+    y = torch.zeros((rows, N), device="cuda")
+    pick = torch.tensor([0x38, 0x40], dtype=torch.uint8, device="cuda")     # 1 and 2
+    for turn in range(30):
+        big = torch.randn((2048, 2048), generator=g, device="cuda")
+        late = (big @ big).abs().argmax() * 0 + turn % 2                    # a value that takes a while to be there
+        x.copy_(pick[late].expand(rows, K))
+        E.engram_project_fp8(x, 0, sc, E.ENGRAM_FMT_FP8_E8M0, rows, w, None, E.ENGRAM_T_F32, y, 0)
+        got = y.clone()
+        E.engram_project_fp8(x, 0, sc, E.ENGRAM_FMT_FP8_E8M0, 1, w, None, E.ENGRAM_T_F32, y, 0)
+        assert (got == K * (1 + turn % 2)).all() and torch.equal(got, y)
+    assert E.engram_check() == 0
+
+
 def test_two_streams_at_once(E):
     """Calls of unlike sizes that overlap: each with its buffers, both as alone."""
     subs = [_sublayer(seed=5), _sublayer(seed=6)]

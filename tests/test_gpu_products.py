@@ -121,7 +121,7 @@ def test_project_experts(E, i, shape):
 
 FORMATS = [("e8m0", "e8m0"), ("e8m0", "fp8"), ("fp8", "e8m0"), ("fp8", "fp8")]
 # enough rows for tiles of 128 rows and 256 weight rows: K of 1 to 33 blocks, whole and cut off, N with tails of both halves
-MANY = [(65, 4096, 300, "f32"), (100, 1568, 1000, "bf16"), (777, 640, 515, "f16"), (128, 8192, 256, "bf16"), (300, 2064, 2100, "f32"), (1300, 1040, 2000, "bf16"), (700, 128, 7000, "f32"), (2500, 528, 1100, "f16"), (1153, 4112, 2177, "f32"), (9000, 16, 300, "bf16"),
+MANY = [(2600, 1552, 2049, "bf16"), (65, 4096, 300, "f32"), (100, 1568, 1000, "bf16"), (777, 640, 515, "f16"), (128, 8192, 256, "bf16"), (300, 2064, 2100, "f32"), (1300, 1040, 2000, "bf16"), (700, 128, 7000, "f32"), (2500, 528, 1100, "f16"), (1153, 4112, 2177, "f32"), (9000, 16, 300, "bf16"),
         (640, 1664, 4097, "f16")]
 
 
@@ -238,7 +238,7 @@ def test_glu_experts(E, i, shape):
 
 @pytest.mark.parametrize("formats", FORMATS)
 @pytest.mark.parametrize("i,shape", [(0, (1500, 272, 1200)), (1, (2600, 1296, 640)), (2, (700, 128, 2064)),
-                                     (3, (70, 4096, 80)), (4, (333, 1088, 272)), (5, (128, 2048, 1040))])
+                                     (3, (70, 4096, 80)), (4, (333, 1088, 272)), (5, (128, 2048, 1040)), (6, (2600, 1040, 1040))])
 def test_glu_many_rows(E, i, shape, formats):
     rows, K, N = shape
     g, out, limit = rng(600 + i), ("e8m0", "fp8")[i % 2], (0.0, 0.75)[i % 2]
