@@ -7,14 +7,14 @@
 // MMA of M 128, N 256, K 32 reads 12 KB for 128 clocks, and a row's largest output is
 // found by the threads that hold it.
 //
-// Roles (16 warps):
+// Roles (16 warps, or 12):
 //   warp 0       TMA: a block's 256 weight rows and, unless they are gathered, its 128 rows of x;
 //   warp 1       issues the MMAs, two 256-column buffers in tensor memory;
 //   warps 2, 3   scales of a block's rows and weights, to shared memory (a load of theirs takes the better part of
 //                two blocks beside the copies);
-//   warps 4..7   rows of x that the lists gather, by 16-byte asynchronous copies (a block of 128 rows
+//   warps 4..7   (where there are any) rows of x that the lists gather, by 16-byte asynchronous copies (a block of 128 rows
 //                takes four warps 290 clocks, one warp 690; as tile::gather4 2200 to 2900);
-//   warps 8..15  take a block's sums into their f32 accumulators (thread: a row, 128 columns,
+//   the last 8   take a block's sums into their f32 accumulators (thread: a row, 128 columns,
 //                for glu 64 of each part; 128 KB of them in about 300 clocks); at the end of a tile they write it.
 // Where both scales are powers of two (e8m0 bytes) the tensor cores apply them: tcgen05.mma kind::mxf8f6f4 with a
 // block's bytes in tensor memory (four blocks to a 32-bit column; an MMA names its byte).  Sums then stay in tensor memory over
@@ -32,7 +32,10 @@ namespace {
 using namespace product;
 
 constexpr int kRows = 128, kCols = 256;
-constexpr int kScaleWarp = 2, kCopyWarp = 4, kCopyWarps = 4, kEpiWarp = 8, kEpiWarps = 8, kThreads = 32 * (kEpiWarp + kEpiWarps);
+constexpr int kScaleWarp = 2, kCopyWarp = 4, kCopyWarps = 4, kEpiWarps = 8;
+// Without gathered rows there are no copying warps (but where the tensor cores apply scales, which needs no more registers: 134 us for 140).
+constexpr int epi_warp(bool mx, bool gather) { return mx || gather ? kCopyWarp + kCopyWarps : kCopyWarp; }
+constexpr int threads_of(bool mx, bool gather) { return 32 * (epi_warp(mx, gather) + kEpiWarps); }
 constexpr uint32_t kStage = 3 * kTileA;              // x, then the weights
 constexpr int kStages = 4;
 // Scales of four blocks at a time (the last of a tile: what is left), [4][128] of rows and [4][2] of weights.
@@ -228,9 +231,10 @@ __device__ __forceinline__ void share_of_tile(const Params &p, const TileAt &w, 
     }
 }
 
-template <bool GLU, bool MX>
-__global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_constant__ Params p) {
-    constexpr int ST = kStages;
+// GATHER: rows of x come by the lists (glu).
+template <bool GLU, bool MX, bool GATHER>
+__global__ void __launch_bounds__(threads_of(MX, GATHER), 1) product_rows_kernel(const __grid_constant__ Params p) {
+    constexpr int ST = kStages, kEpiWarp = epi_warp(MX, GATHER), kThreads = threads_of(MX, GATHER);
     extern __shared__ uint8_t smem_raw[];
     const ProductArgs &a = p.a;
     const uint32_t raw = smem_u32(smem_raw);
@@ -249,10 +253,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
     int *first = reinterpret_cast<int *>(smem + oLists), *count = first + a.E, *before = count + a.E;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool gather = GLU && a.pairs;
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
-            mbar_init(full(s), gather ? 1 + kCopyWarps : 1);
+            mbar_init(full(s), GATHER ? 1 + kCopyWarps : 1);
             mbar_init(done(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -291,8 +294,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
     auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, warp_wait(bar, parity & 1, abort_flag, a.err)) != 0; };
     auto lane_wait = [&](uint32_t bar, uint32_t parity) { return warp_wait(bar, parity & 1, abort_flag, a.err); };
 
-    // 512 threads launch with 128 registers each: 256 x 80 + 256 x 176 are as many
-    if (warp < kEpiWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    // 512 threads launch with 128 registers each, and 256 x 64 + 256 x 192 are as many; 384 with 168: 128 x 88 + 256 x 208.  (What
+    // the last warps keep in local memory costs a block's step: 184 for 208 took 4096 rows' way back 186 us for 170.)
+    if (warp < kEpiWarp) {
+        if (kThreads == 512)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    }
     if (warp == 0) {
         // ---- weights, and rows that stand together ----
         uint32_t it = 0;
@@ -304,9 +313,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
                 if (!(ok = wait(done(s), it / ST ^ 1))) break;
                 if (elect()) {
                     const uint32_t at = base + s * kStage, bar = full(s);
-                    mbar_expect_tx(bar, gather ? 2 * kTileA : 3 * kTileA);
+                    mbar_expect_tx(bar, GATHER ? 2 * kTileA : 3 * kTileA);
                     tma_weights(at + kTileA, &p.mw, kb * 128, w.m0, 0, w.e, bar);
-                    if (!gather) tma_rows(at, &p.mx, kb * 128, w.row, bar);
+                    if (!GATHER) tma_rows(at, &p.mx, kb * 128, w.row, bar);
                 }
                 __syncwarp();
             }
@@ -398,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
                 const int c = c0 + v * 32;
-                xi[v] = c < w.n ? gather ? token_of(a, w.row + c) : w.row + c : -1;
+                xi[v] = c < w.n ? GATHER ? token_of(a, w.row + c) : w.row + c : -1;
                 to[c] = c >= w.n ? -1 : GLU || !a.pairs ? w.row + c : out_row_of(a, w.row + c);
             }
             if (warp == kScaleWarp && lane == 0) to[kRows] = w.m0;
@@ -409,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int c = i * 32 + lane;
-                    r4[i] = warp == kScaleWarp && c < w.n ? gather ? token_of(a, w.row + c) : w.row + c : -1;
+                    r4[i] = warp == kScaleWarp && c < w.n ? GATHER ? token_of(a, w.row + c) : w.row + c : -1;
                 }
                 for (int kb4 = kb0; kb4 < kb1; kb4 += 4, ++it) {
                     const int left = KB - kb4, slot = it % kSlots;
@@ -438,7 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
                 }
                 continue;
             }
-            // the next four blocks' scales are on their way while these are written
+            // where there are registers for it, the next four blocks' scales are on their way while these are written
+            constexpr bool kAhead = !GATHER;
             uint4 next_x[2], next_w[2];
             auto fetch = [&](int kb4) {
                 const int left = KB - kb4;
@@ -448,10 +458,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
                 next_w[0] = load_scales(a.w_scales, a.w_fmt, vec_w, w0 + kb4, left);
                 if (both) next_w[1] = load_scales(a.w_scales, a.w_fmt, vec_w, w1 + kb4, left);
             };
-            fetch(kb0);
+            if (kAhead) fetch(kb0);
             for (int kb4 = kb0; kb4 < kb1; kb4 += 4, ++it) {
+                if (!kAhead) fetch(kb4);
                 const uint4 x[2] = {next_x[0], next_x[1]}, s0 = next_w[0], s1 = both ? next_w[1] : s0;
-                if (kb4 + 4 < kb1) fetch(kb4 + 4);
+                if (kAhead && kb4 + 4 < kb1) fetch(kb4 + 4);
                 const int slot = it % kSlots;
                 float *f = reinterpret_cast<float *>(smem + oScale + slot * kSlotBytes);
                 if (!(ok = wait(sempty(slot), it / kSlots ^ 1))) break;
@@ -477,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
             __syncwarp();
             if (lane == 0) mbar_arrive(full(done % ST));
         };
-        for (int t = t0; t < tiles && ok && gather; t += t_step) {
+        for (int t = t0; GATHER && t < tiles && ok; t += t_step) {
             const TileAt w = tile_at(t);
             uint32_t from[NR];                       // where the rows begin, in 16 bytes
 #pragma unroll
@@ -503,11 +514,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
             }
         }
         cp_wait<0>();
-        for (uint32_t done = it > LAG ? it - LAG : 0; ok && gather && done < it; ++done) landed(done);
+        for (uint32_t done = it > LAG ? it - LAG : 0; GATHER && ok && done < it; ++done) landed(done);
         __syncwarp();
     } else {
         // ---- sums and output ----
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        if (kThreads == 512)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        else
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int g = (warp - kEpiWarp) >> 2, q = warp & 3, row = 32 * q + lane;
         // this thread's columns: 128 g .. + 127 in quarters, or 64 g .. + 63 of both parts in halves (parts in turn)
         auto column = [&](int i) { return GLU ? (i & 1) * kM + 64 * g + (i >> 1) * 32 : kM * g + 32 * i; };
@@ -688,12 +702,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_rows_kernel(const __grid_
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-template <bool GLU, bool MX>
+template <bool GLU, bool MX, bool GATHER>
 cudaError_t launch(Params &p, cudaStream_t s) {
     const ProductArgs &a = p.a;
     static Fit fits[64] = {};
     Fit fit;
-    const cudaError_t e = fit_of(fits, product_rows_kernel<GLU, MX>, kThreads, smem_bytes(kMaxExperts), &fit);
+    const cudaError_t e = fit_of(fits, product_rows_kernel<GLU, MX, GATHER>, threads_of(MX, GATHER), smem_bytes(kMaxExperts), &fit);
     if (e != cudaSuccess) return e;
     const uint64_t xd[2] = {(uint64_t)a.K, (uint64_t)a.rows}, xst[1] = {(uint64_t)a.x_stride};
     const uint32_t box[2] = {128, kRows};
@@ -705,15 +719,16 @@ cudaError_t launch(Params &p, cudaStream_t s) {
     // row tiles side by side whose rows stay in L2
     const int64_t rows_l2 = (int64_t(48) << 20) / a.K / kRows;
     p.group = (int)(rows_l2 < 8 ? 8 : rows_l2 > 0x3FFFFFFF ? 0x3FFFFFFF : rows_l2);
-    return launch_split(product_rows_kernel<GLU, MX>, p, tiles, kThreads, smem_bytes(a.E), s);
+    return launch_split(product_rows_kernel<GLU, MX, GATHER>, p, tiles, threads_of(MX, GATHER), smem_bytes(a.E), s);
 }
 
 }  // namespace
 
 cudaError_t launch_product_rows(product::Params &p, cudaStream_t s) {
     const bool mx = p.a.x_fmt == ENGRAM_FMT_FP8_E8M0 && p.a.w_fmt == ENGRAM_FMT_FP8_E8M0;
-    if (p.a.glu) return mx ? launch<true, true>(p, s) : launch<true, false>(p, s);
-    return mx ? launch<false, true>(p, s) : launch<false, false>(p, s);
+    if (!p.a.glu) return mx ? launch<false, true, false>(p, s) : launch<false, false, false>(p, s);
+    if (!p.a.pairs) return mx ? launch<true, true, false>(p, s) : launch<true, false, false>(p, s);
+    return mx ? launch<true, true, true>(p, s) : launch<true, false, true>(p, s);
 }
 
 }  // namespace engram
