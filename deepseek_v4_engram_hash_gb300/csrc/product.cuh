@@ -31,21 +31,22 @@ struct TileAt {
     int e, row, n, m0;                               // expert, first row, rows, first weight row
 };
 
-// Bounded wait as common.cuh's mbar_wait, for a whole warp; the timer, whose reading takes longer than most waits here, is looked at
-// every 64 tests only.  (One lane that waits for its warp is slow: 1245 clocks for a hand-over that takes all lanes 513.)
+constexpr long long kWaitClocks = 2 * (long long)kWaitNs;
+// Bounded wait as common.cuh's mbar_wait, for a whole warp, by the SM's clock (about 2 s; reading the timer takes longer than most waits
+// here).  (One lane that waits for its warp is slow: 1245 clocks for a hand-over that takes all lanes 513.)
 // Once the flag is up a wait ends after 64 tests, so that loops may vote on the outcome at their end alone.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *err) {
     bool ok = true;
-    uint64_t began = 0;
+    long long began = 0;
     for (uint32_t i = 1; !mbar_try(bar, parity); ++i) {
         if (i & 63) continue;
         if (*abort_flag) {
             ok = false;
             break;
         }
-        const uint64_t now = now_ns();
+        const long long now = clock64();
         if (!began) began = now;
-        if (now - began > kWaitNs) {
+        if (now - began > kWaitClocks) {
             *abort_flag = 1;
             set_err(err, ENGRAM_E_TIMEOUT);
             ok = false;
