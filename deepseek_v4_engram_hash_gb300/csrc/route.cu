@@ -3,7 +3,8 @@
 //
 // A warp takes a token; lane l holds c = ceil(n_experts / 32) consecutive experts from l c on.  A
 // lane sorts its experts (up to eight) by their keys, a float's bits ordered as integers; a choice is the largest first key by one
-// warp-wide maximum of integers, the lowest lane that has it by a vote, and a step of that lane's list.  Groups that are a power of two
+// warp-wide maximum of integers, the lowest lane that has it by a vote, and a step of that lane's list.  The sort is of 32-bit words that hold
+// a key's upper 29 bits and its place, wherever that tells all that a choice needs.  Groups that are a power of two
 // of lanes (8 groups of 256 experts: four) find their two largest all at once by exchanges.  Scores are formed in 32 bits;
 // where two that a choice depends on lie closer than their error (kTol, about one row in a thousand of 256
 // sigmoid scores), those in question are formed again in 64 bits, one a lane (all of a row's took its warp 15 us).
@@ -16,6 +17,8 @@
 // Bound by latency and instructions: one token is a chain of load, exponential and top_k + 1 maxima.
 #include "experts.cuh"
 
+#include <mutex>
+
 namespace engram {
 
 namespace {
@@ -23,11 +26,12 @@ namespace {
 constexpr int kOneBlock = 32;                        // tokens up to which one block does all
 constexpr int kBlocks = 152;                         // blocks at most of the others
 constexpr unsigned kAll = 0xFFFFFFFFu;
-// A 32-bit score that orders experts is within 4e-7 max(1, |c|) of the 64-bit one.  e = __expf(-l) is off by 2^-22 + 2^-23 |l| of itself, which moves
-// s = 1 / (1 + e) by s (1 - s) of that, under 2^-23; 1 + e and the reciprocal (1 ulp) by 2^-24 + 2^-23 of s; the sum with the
+// A 32-bit score that orders experts is within 4e-7 max(1, |c|) of the 64-bit one.  e = 2^(-l log2 e) is off by 2^-22 + 2^-23 |l| of itself, which
+// moves s = 1 / (1 + e) by s (1 - s) of that, under 2^-23; 1 + e and the reciprocal (1 ulp) by 2^-24 + 2^-23 of s; the sum with the
 // bias by 2^-24 |c|.  Softmax: e^(l - max) by 2^-22 + 2^-22 |l - max| of itself, under 2^-22 after all, and as much for the divisor.
-// Two of them, and sums of two, differ by twice that.
-constexpr float kTol = 1e-6f;
+// Two of them differ by twice that, 8e-7, and where keys lose their last three bits, all to the same side, by 7 2^-23 |c| = 8.4e-7 more: 1.7e-6.
+// Sums of two by twice as much.
+constexpr float kTol = 2e-6f;
 
 // Warps a block: 32 with 64 registers; rows of many experts take 16 with 128.
 int route_warps(int n_experts) { return n_experts <= 256 ? 32 : 16; }
@@ -280,9 +284,14 @@ __device__ __forceinline__ float reciprocal(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+__device__ __forceinline__ float exp_of(float x) {   // 2^(x log2 e); 0 below 2^-126
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.44269504f));
+    return r;
+}
 // The same, of few instructions, to order by (see kTol); of sum its reciprocal.
 __device__ __forceinline__ float quick_score(bool soft, float x, float top, float per_sum) {
-    return soft ? __expf(x - top) * per_sum : reciprocal(1.f + __expf(-x));
+    return soft ? exp_of(x - top) * per_sum : reciprocal(1.f + exp_of(-x));
 }
 // The value that orders groups, of a key.
 __device__ __forceinline__ uint32_t group_key32(const RouteArgs &a, bool soft, uint32_t key, float top, float per_sum) {
@@ -455,8 +464,27 @@ __device__ __forceinline__ void sort_falling(uint64_t (&s)[NV]) {
                     }
 }
 
-// Token `row` with the logits l: its ids and weights, one choice a lane.
+__device__ __forceinline__ void sort_falling(uint32_t (&s)[1]) {}
 template <int NV>
+__device__ __forceinline__ void sort_falling(uint32_t (&s)[NV]) {
+#pragma unroll
+    for (int p = 1; p < NV; p <<= 1)
+#pragma unroll
+        for (int k = p; k > 0; k >>= 1)
+#pragma unroll
+            for (int j = k % p; j + k < NV; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < NV && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const uint32_t x = s[i + j], y = s[i + j + k];
+                        s[i + j] = max(x, y);
+                        s[i + j + k] = min(x, y);
+                    }
+}
+
+// Token `row` with the logits l: its ids and weights, one choice a lane.  PACKED: a key's last bits give way to its place in the lane (scores with a
+// bias, for which kTol allows; logits of 16 bits, which leave them alone), so that a lane sorts words of 32 bits: half the instructions.
+template <int NV, bool PACKED>
 __device__ __forceinline__ int route_row(const RouteArgs &a, const Shape &sh, const float (&bias)[NV], float (&l)[NV], int64_t row,
                                          int lane) {
     const engram_router &r = a.r;
@@ -495,7 +523,34 @@ __device__ __forceinline__ int route_row(const RouteArgs &a, const Shape &sh, co
     }
     int id;
     bool chosen;
-    if (NV <= 8) {
+    if (PACKED) {
+        constexpr uint32_t kPlace = NV <= 8 ? NV - 1 : 0;
+        uint32_t s[NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) s[v] = key[v] ? (key[v] & ~kPlace) | (kPlace - v) : 0u;
+        sort_falling(s);
+        if (grouped && sh.lanes) {
+            // (a 16-bit logit's key has its last bits all 0, or all 1 if it is negative)
+            auto value = [&](uint32_t k) { return exact && k && (int)k >= 0 ? k | kPlace : k & ~kPlace; };
+            uint32_t first = group_key32(a, soft, value(s[0]), top, per_sum);
+            uint32_t second = NV > 1 ? group_key32(a, soft, value(s[NV > 1]), top, per_sum) : 0u;
+            two_best_of_lanes(first, second, sh.lanes);
+            const uint32_t mine = __shfl_sync(kAll, sum_of(r.group_best, first, second), lane * sh.lanes & 31);
+            settle_groups(lane < r.n_groups ? mine : 0u);
+            const bool out = !(kept >> min(31, lane / sh.lanes) & 1);
+#pragma unroll
+            for (int v = 0; v < NV; ++v) s[v] = out ? 0u : s[v];
+        }
+        uint32_t m = s[0] & ~kPlace;                 // equal ones: the lowest lane's, and in a lane the lowest place's
+        int at = kPlace - (s[0] & kPlace);
+        auto next = [&](bool mine) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) s[v] = mine ? v + 1 < NV ? s[(v + 1) % NV] : 0u : s[v];
+            m = s[0] & ~kPlace;
+            at = kPlace - (s[0] & kPlace);
+        };
+        chosen = choose<true>(a, sh, row, m, at, next, exact, lane, id, least);
+    } else if (NV <= 8) {
         uint64_t s[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) s[v] = (uint64_t)key[v] << 32 | (uint32_t)(NV - 1 - v);
@@ -624,7 +679,7 @@ __device__ __forceinline__ void place_pairs(const RouteArgs &a, int *counts, con
 }
 
 // One block: everything.  Several: ids, weights and the block's counts (ws).
-template <int NV>
+template <int NV, bool PACKED>
 __global__ void __launch_bounds__(NV <= 8 ? 1024 : 512) route_kernel(const __grid_constant__ RouteArgs a) {
     extern __shared__ int smem[];
     __shared__ int part[32];
@@ -647,7 +702,7 @@ __global__ void __launch_bounds__(NV <= 8 ? 1024 : 512) route_kernel(const __gri
 #pragma unroll
         for (int v = 0; v < NV; ++v) l[v] = next[v];
         if (t + 1 < hi) load_row<NV>(a, sh.c, wide, t + 1, lane, next);
-        const int id = route_row<NV>(a, sh, bias, l, t, lane);
+        const int id = route_row<NV, PACKED>(a, sh, bias, l, t, lane);
         if (a.offsets) count_row(a, mine, id, lane);
     }
     if (!a.offsets) return;
@@ -717,8 +772,10 @@ size_t smem_bytes(int E, int warps) { return ((size_t)(warps + 2) * E + 2) * siz
 
 // Once a device: dynamic shared memory for the most experts.
 cudaError_t allow_smem(void (*kernel)(const RouteArgs), bool (&done)[64]) {
+    static std::mutex mutex;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mutex);
     if (done[dev]) return cudaSuccess;
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(kMaxExperts, 32));
@@ -726,13 +783,18 @@ cudaError_t allow_smem(void (*kernel)(const RouteArgs), bool (&done)[64]) {
     return e;
 }
 
+template <int NV, bool PACKED>
+cudaError_t launch_kernel(const RouteArgs &a, int blocks, int warps, cudaStream_t s) {
+    static bool wide[64] = {};
+    const cudaError_t e = allow_smem(route_kernel<NV, PACKED>, wide);
+    if (e != cudaSuccess) return e;
+    route_kernel<NV, PACKED><<<blocks, 32 * warps, a.offsets ? smem_bytes(a.r.n_experts, warps) : 0, s>>>(a);
+    return cudaGetLastError();
+}
 template <int NV>
 cudaError_t launch_rows(const RouteArgs &a, int blocks, int warps, cudaStream_t s) {
-    static bool wide[64] = {};
-    const cudaError_t e = allow_smem(route_kernel<NV>, wide);
-    if (e != cudaSuccess) return e;
-    route_kernel<NV><<<blocks, 32 * warps, a.offsets ? smem_bytes(a.r.n_experts, warps) : 0, s>>>(a);
-    return cudaGetLastError();
+    if (NV <= 8 && (a.bias || a.type != ENGRAM_T_F32)) return launch_kernel<NV, NV <= 8>(a, blocks, warps, s);
+    return launch_kernel<NV, false>(a, blocks, warps, s);
 }
 
 }  // namespace
