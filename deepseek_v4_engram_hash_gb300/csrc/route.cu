@@ -108,40 +108,46 @@ __device__ __forceinline__ void two_best_of_lanes(Key &first, Key &second, int l
         two_best(first, second, x, y);
     }
 }
-// Groups that are no whole lanes: lane g gets group g's sum.
+// The larger of the two numbers' sizes: it bounds the error of their sum, which may be smaller.
+template <class Key>
+__device__ __forceinline__ float part_of(int best, Key first, Key second) {
+    const float x = first ? fabsf((float)of_key(first)) : 0.f;
+    return best == 2 && second ? fmaxf(x, fabsf((float)of_key(second))) : x;
+}
+// Groups that are no whole lanes: lane g gets group g's sum, and its larger part.
 template <class Key, int NV>
-__device__ __forceinline__ Key group_sums(const RouteArgs &a, const Shape &sh, const Key (&group)[NV], int lane) {
+__device__ __forceinline__ Key group_sums(const RouteArgs &a, const Shape &sh, const Key (&group)[NV], int lane, float &part) {
     Key mine = 0;
+    part = 0.f;
     for (int g = 0; g < a.r.n_groups; ++g) {
         const int lo = g * sh.size - lane * sh.c, hi = lo + sh.size;   // of this lane's experts
         Key first = 0, second = 0;
 #pragma unroll
         for (int v = 0; v < NV; ++v) two_best(first, second, v >= lo && v < hi ? group[v] : Key(0), Key(0));
         two_best_of_lanes(first, second, 32);
-        if (lane == g) mine = sum_of(a.r.group_best, first, second);
+        if (lane == g) mine = sum_of(a.r.group_best, first, second), part = part_of(a.r.group_best, first, second);
     }
     return mine;
 }
-// The top_groups of the groups' sums `mine` (lane g: group g's).  CHECK: false in `sure` where 32 bits leave a doubt.
-template <bool CHECK, class Key>
-__device__ __forceinline__ unsigned keep_groups(const RouteArgs &a, Key mine, bool exact, int lane, bool &sure) {
-    using T = typename Real<Key>::type;
+// The top_groups of the groups' sums `mine` (lane g: group g's).
+template <class Key>
+__device__ __forceinline__ unsigned keep_groups(const RouteArgs &a, Key mine, int lane) {
     unsigned kept = 0;
-    T last = 0;
-    for (int i = 0; i <= a.r.top_groups; ++i) {
+    for (int i = 0; i < a.r.top_groups; ++i) {
         const Key top = warp_max(mine);
         if (!top) break;                             // masked groups alone are left
-        if (i == a.r.top_groups) {
-            // logits alone are ordered exactly
-            if (CHECK && !(exact && a.r.group_best == 1) && last - of_key(top) <= (T)(2 * kTol) * fmax((T)1, fabs(last))) sure = false;
-            break;
-        }
         const int g = __ffs(__ballot_sync(kAll, mine == top)) - 1;
-        last = of_key(top);
         kept |= 1u << g;
         mine = lane == g ? Key(0) : mine;
     }
     return kept;
+}
+// Whether 32 bits tell that the groups `kept` are those: the least that any of them can be is above the most that any other can.
+__device__ __forceinline__ bool sure_of_groups(uint32_t mine, float part, unsigned kept, int lane) {
+    const float x = of_key(mine), err = 2 * kTol * fmaxf(1.f, part);
+    const bool in = kept >> lane & 1;
+    const uint32_t most = __reduce_max_sync(kAll, mine && !in ? key_of(x + err) : 0u);
+    return !most || __reduce_min_sync(kAll, mine && in ? key_of(x - err) : 0xFFFFFFFFu) > most;
 }
 template <class Key, int NV>
 __device__ __forceinline__ void mask_groups(const Shape &sh, unsigned kept, int lane, Key (&key)[NV]) {
@@ -360,10 +366,10 @@ __device__ __noinline__ int choose_all(const RouteArgs &a, int64_t row, int lane
         key[v] = masked ? 0 : key_of(a.bias ? p + (double)a.bias[lane * sh.c + v] : s[v]);
         group[v] = masked ? 0 : a.bias || a.r.group_best == 1 ? key[v] : key_of(p);
     }
-    bool sure = true;
+    float part;
     int id;
     if (a.r.top_groups < a.r.n_groups)
-        mask_groups(sh, keep_groups<false>(a, group_sums(a, sh, group, lane), true, lane, sure), lane, key);
+        mask_groups(sh, keep_groups(a, group_sums(a, sh, group, lane, part), lane), lane, key);
     choose_of<false>(a, sh, row, key, true, lane, id, least);
     return id;
 }
@@ -415,8 +421,7 @@ __device__ __noinline__ unsigned groups_again(const RouteArgs &a, int64_t row, i
         const uint64_t second = warp_max(x);
         if (lane == g) sums = sum_of(r.group_best, first, second);
     }
-    bool sure = true;
-    return keep_groups<false>(a, sums, true, lane, sure);
+    return keep_groups(a, sums, lane);
 }
 // The choices among the groups `kept`, by 64-bit scores of the experts that may be among them: from `least`, the 32-bit key behind the
 // last choice, on.  -2: too many.
@@ -426,7 +431,7 @@ __device__ __noinline__ int experts_again(const RouteArgs &a, int64_t row, int l
     uint32_t key[NV];
     keys_again(a, sh, row, lane, top, per_sum, key);
     if (a.r.top_groups < a.r.n_groups) mask_groups(sh, kept, lane, key);
-    const float x = of_key(least), from = x - kTol * fmaxf(1.f, fabsf(x));
+    const float x = of_key(least), from = least ? x - kTol * fmaxf(1.f, fabsf(x)) : -INFINITY;   // 0: none is left behind them
     unsigned want = 0;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
@@ -508,17 +513,20 @@ __device__ __forceinline__ int route_row(const RouteArgs &a, const Shape &sh, co
     uint32_t key[NV], least = 0;
     keys_of(a, soft, l, bias, top, per_sum, key);
     // a softmax beside a bias needs its divisor in 64 bits, too: all scores
-    bool all = false, sure = true;
+    bool all = false;
     unsigned kept = 0xFFFFFFFFu;
-    auto settle_groups = [&](uint32_t mine) {
-        kept = keep_groups<true>(a, mine, exact, lane, sure);
-        if (!sure) all = (soft && a.bias) || !(kept = groups_again<NV>(a, row, lane, top, per_sum));
+    auto settle_groups = [&](uint32_t mine, float part) {
+        kept = keep_groups(a, mine, lane);
+        // (logits alone are ordered exactly)
+        if (!(exact && r.group_best == 1) && !sure_of_groups(mine, part, kept, lane)) all = (soft && a.bias) || !(kept = groups_again<NV>(a, row, lane, top, per_sum));
     };
     if (grouped && (!sh.lanes || NV > 8)) {
         uint32_t group[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) group[v] = group_key32(a, soft, key[v], top, per_sum);
-        settle_groups(group_sums(a, sh, group, lane));
+        float part;
+        const uint32_t mine = group_sums(a, sh, group, lane, part);
+        settle_groups(mine, part);
         mask_groups(sh, kept, lane, key);
     }
     int id;
@@ -536,7 +544,8 @@ __device__ __forceinline__ int route_row(const RouteArgs &a, const Shape &sh, co
             uint32_t second = NV > 1 ? group_key32(a, soft, value(s[NV > 1]), top, per_sum) : 0u;
             two_best_of_lanes(first, second, sh.lanes);
             const uint32_t mine = __shfl_sync(kAll, sum_of(r.group_best, first, second), lane * sh.lanes & 31);
-            settle_groups(lane < r.n_groups ? mine : 0u);
+            const float part = __shfl_sync(kAll, part_of(r.group_best, first, second), lane * sh.lanes & 31);
+            settle_groups(lane < r.n_groups ? mine : 0u, part);
             const bool out = !(kept >> min(31, lane / sh.lanes) & 1);
 #pragma unroll
             for (int v = 0; v < NV; ++v) s[v] = out ? 0u : s[v];
@@ -560,7 +569,8 @@ __device__ __forceinline__ int route_row(const RouteArgs &a, const Shape &sh, co
             uint32_t second = NV > 1 ? group_key32(a, soft, (uint32_t)(s[NV > 1] >> 32), top, per_sum) : 0u;
             two_best_of_lanes(first, second, sh.lanes);
             const uint32_t mine = __shfl_sync(kAll, sum_of(r.group_best, first, second), lane * sh.lanes & 31);
-            settle_groups(lane < r.n_groups ? mine : 0u);
+            const float part = __shfl_sync(kAll, part_of(r.group_best, first, second), lane * sh.lanes & 31);
+            settle_groups(lane < r.n_groups ? mine : 0u, part);
             const bool out = !(kept >> min(31, lane / sh.lanes) & 1);
 #pragma unroll
             for (int v = 0; v < NV; ++v) s[v] = out ? (uint32_t)s[v] : s[v];
@@ -606,6 +616,170 @@ __device__ __forceinline__ int route_row(const RouteArgs &a, const Shape &sh, co
     return id;
 }
 
+// ---- four tokens a warp ----
+// Eight lanes a token, C consecutive experts a lane: what takes all lanes' attention above (maxima, votes) is paid once for four tokens.
+// A key gives five bits to its place, so more rows than above are in doubt; those are formed again as above.
+// Two scores of which x is the larger are told apart by this: 8e-7 max(1, |x|) (see kTol), and C units of its last place.  Half of it
+// bounds the error of a value in the middle of those that its key may stand for.
+template <int C>
+__device__ __forceinline__ float quad_tol(float x) {
+    return fmaf(__uint_as_float(__float_as_uint(x) & 0x7F800000u), C * 0x1p-23f, 1e-6f * fmaxf(1.f, fabsf(x)));
+}
+template <int NV>
+__device__ __noinline__ int row_again(const RouteArgs &a, int64_t row, int lane) {
+    const Shape sh = shape_of(a.r);
+    float l[NV], bias[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) bias[v] = a.bias ? __ldg(a.bias + lane * NV + v) : 0.f;
+    load_row<NV>(a, NV, wide_rows<NV>(a), row, lane, l);
+    return route_row<NV, true>(a, sh, bias, l, row, lane);
+}
+// Whether `a` has such rows, and enough of them, four a warp (16384 tokens, 256 experts: 23.7 us for 30.2, without lists; 4096: 20.4 for 16.1): 8 C experts, whole lanes a group, up to 8 choices, keys that may lose bits, aligned rows.
+inline bool quads_fit(const RouteArgs &a, int blocks, int C) {
+    const int size = a.type == ENGRAM_T_F32 ? 4 : 2;
+    return a.tokens >= 64 * blocks && blocks > 1 && a.r.n_experts == 8 * C && a.r.n_groups <= 8 && 8 % a.r.n_groups == 0 && a.r.top_k <= 8 && a.r.score == ENGRAM_SCORE_SIGMOID &&
+           (a.bias || a.type != ENGRAM_T_F32) && a.stride * size % 16 == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0;
+}
+// Tokens t .. t + 3 (before hi); bias: [C / 4][8 lanes][4] in shared memory.  A lane's choice: lane j of a token's eight, choice j.
+template <int C>
+__device__ __forceinline__ int route_quad(const RouteArgs &a, const float4 *bias, int64_t t, int64_t hi, int lane) {
+    constexpr uint32_t kPlace = C - 1;
+    const engram_router &r = a.r;
+    const int sub = lane & 7, seg = lane >> 3, k = r.top_k;
+    const int64_t row = t + seg < hi ? t + seg : hi - 1;
+    const bool exact = !a.bias;
+    uint32_t key[C];
+    bool nan = false;
+    {
+        const int64_t at = row * a.stride + sub * C;
+#pragma unroll
+        for (int v = 0; v < C; v += 8) {
+            float l[8];
+            if (a.type == ENGRAM_T_F32) {
+                const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.logits) + at + v);
+                const float4 x = __ldg(p), y = __ldg(p + 1);
+                l[0] = x.x, l[1] = x.y, l[2] = x.z, l[3] = x.w, l[4] = y.x, l[5] = y.y, l[6] = y.z, l[7] = y.w;
+            } else {
+                const uint4 raw = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.logits) + at + v));
+                if (a.type == ENGRAM_T_BF16)
+                    load8<ENGRAM_T_BF16>(&raw, 0, l);
+                else
+                    load8<ENGRAM_T_F16>(&raw, 0, l);
+            }
+            float b[8] = {};
+            if (a.bias) {
+                const float4 x = bias[v / 4 * 8 + sub], y = bias[(v / 4 + 1) * 8 + sub];
+                b[0] = x.x, b[1] = x.y, b[2] = x.z, b[3] = x.w, b[4] = y.x, b[5] = y.y, b[6] = y.z, b[7] = y.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                nan |= l[i] != l[i];
+                const uint32_t u = key_of(a.bias ? quick_score(false, l[i], 0.f, 0.f) + b[i] : l[i]);
+                key[v + i] = l[i] > -INFINITY ? (u & ~kPlace) | (kPlace - (v + i)) : 0u;
+            }
+        }
+    }
+    nan = (__ballot_sync(kAll, nan) >> (8 * seg) & 0xFF) != 0;
+    uint32_t m = 0, second = 0;                      // the lane's largest two
+#pragma unroll
+    for (int v = 0; v < C; ++v) {
+        second = max(second, min(m, key[v]));
+        m = max(m, key[v]);
+    }
+    bool doubt = false, doubt_group = false;
+    unsigned groups = 0xFF;                          // this token's lanes that stay
+    if (r.top_groups < r.n_groups) {
+        const int lanes = 8 / r.n_groups;
+        // (a 16-bit logit's key has its last bits all 0, or all 1 if it is negative)
+        auto value = [&](uint32_t x) { return !x ? 0u : !exact ? (x & ~kPlace) | C / 2 : (int)x >= 0 ? x | kPlace : x & ~kPlace; };
+        uint32_t x1 = group_key32(a, false, value(m), 0.f, 0.f), x2 = group_key32(a, false, value(second), 0.f, 0.f);
+        two_best_of_lanes(x1, x2, lanes);
+        const uint32_t mine = sum_of(r.group_best, x1, x2);
+        // of equal sums the lower group; a lane asks for those of the token's other lanes
+        int before = 0;
+#pragma unroll
+        for (int o = 1; o < 8; ++o) {
+            const uint32_t other = __shfl_xor_sync(kAll, mine, o);
+            if ((sub ^ o) / lanes != sub / lanes) before += other > mine || (other == mine && (sub ^ o) < sub);
+        }
+        const bool kept = before < r.top_groups * lanes;
+        if (!(exact && r.group_best == 1)) {         // logits alone are ordered exactly
+            const bool both = r.group_best == 2 && x2;
+            const float s = of_key(mine), err = mine ? 0.5f * (quad_tol<C>(of_key(x1)) + (both ? quad_tol<C>(of_key(x2)) : 0.f)) : 0.f;
+            float least = mine && kept ? s - err : INFINITY, most = mine && !kept ? s + err : -INFINITY;
+#pragma unroll
+            for (int o = 4; o; o >>= 1) {
+                least = fminf(least, __shfl_xor_sync(kAll, least, o));
+                most = fmaxf(most, __shfl_xor_sync(kAll, most, o));
+            }
+            doubt_group = least <= most;
+        }
+        m = kept ? m : 0u;
+        groups = __ballot_sync(kAll, kept) >> (8 * seg) & 0xFF;
+    }
+    int id = -1, behind = -1;
+    uint32_t mine = 0, after = 0, least = 0;
+#pragma unroll 1
+    for (int j = 0; j <= k; ++j) {
+        const uint32_t x = m & ~kPlace;
+        uint32_t top = x;
+#pragma unroll
+        for (int o = 4; o; o >>= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
+        const int first = __ffs(__ballot_sync(kAll, x == top) >> (8 * seg) & 0xFF) - 1;   // lower lanes hold lower experts
+        const int e = __shfl_sync(kAll, sub * C + (int)(kPlace - (m & kPlace)), 8 * seg + first);
+        if (j == k) {
+            behind = e, after = least = top;
+        } else if (sub == j && top) {
+            id = e, mine = top;
+        }
+        uint32_t next = 0;
+#pragma unroll
+        for (int v = 0; v < C; ++v) next = max(next, key[v] < m ? key[v] : 0u);
+        m = sub == first && top ? next : m;
+    }
+    if (!exact) {
+        const uint32_t down = __shfl_down_sync(kAll, mine, 1);
+        const int other = __shfl_down_sync(kAll, id, 1);
+        if (sub != k - 1) after = down, behind = other;
+        if (sub < k && mine && after) {
+            const float x = of_key(mine), y = of_key(after);
+            if (x - y <= quad_tol<C>(x))
+                doubt |= !(load_logit(a, row * a.stride + id) == load_logit(a, row * a.stride + behind) && a.bias[id] == a.bias[behind]);
+        }
+    }
+    const bool real = t + seg < hi;
+    unsigned doubts = __ballot_sync(kAll, (doubt || doubt_group) && real);
+#pragma unroll 1
+    while (doubts) {
+        const int at = (__ffs(doubts) - 1) >> 3;
+        doubts &= ~(0xFFu << (8 * at));
+        // the token's groups as the others have them, a bit a group
+        const unsigned lanes_in = __shfl_sync(kAll, groups, 8 * at);
+        unsigned kept = 0;
+        for (int g = 0; g < r.n_groups; ++g) kept |= (lanes_in >> (g * 8 / r.n_groups) & 1) << g;
+        const uint32_t from = __shfl_sync(kAll, least, 8 * at);
+        const bool same = !__shfl_sync(kAll, (int)doubt_group, 8 * at) || groups_again<C / 4>(a, t + at, lane, 0.f, 0.f) == kept;
+        if (same && !__any_sync(kAll, doubt && seg == at)) continue;
+        int again = same ? experts_again<C / 4>(a, t + at, lane, 0.f, 0.f, kept, from) : -2;
+        if (__any_sync(kAll, again == -2)) again = row_again<C / 4>(a, t + at, lane);
+        __syncwarp();
+        again = __shfl_sync(kAll, again, sub);
+        if (seg == at) id = sub < k ? again : -1;
+    }
+    float s = id >= 0 ? score32(false, load_logit(a, row * a.stride + id), 0.f, 0.f) : 0.f;
+    if (r.renormalise) {
+        float u = s;
+#pragma unroll
+        for (int o = 4; o; o >>= 1) u += __shfl_xor_sync(kAll, u, o);
+        s = s / (u + 1e-20f);
+    }
+    if (real && sub < k) {
+        a.ids[row * k + sub] = id;
+        a.weights[row * k + sub] = nan ? __int_as_float(0x7FFFFFFF) : id < 0 ? 0.f : s * r.scale;
+    }
+    return real ? id : -1;
+}
+
 // Tokens of warp `w` of block b.
 __device__ __forceinline__ void warp_tokens(const RouteArgs &a, int b, int blocks, int w, int64_t &lo, int64_t &hi) {
     const int warps = blockDim.x >> 5;
@@ -628,13 +802,15 @@ __device__ __forceinline__ void block_scan(int *v, int n, int *part) {
         }
         if (lane == 31) part[warp] = s;
         __syncthreads();
-        int before = carry, total = carry;
-        for (int w = 0; w < warps; ++w) {
-            if (w < warp) before += part[w];
-            total += part[w];
+        int of = lane < warps ? part[lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kAll, of, o);
+            if (lane >= o) of += y;
         }
+        const int before = carry + (warp ? __shfl_sync(kAll, of, warp - 1) : 0);
         if (i < n) v[i] = before + s - x;
-        carry = total;
+        carry += __shfl_sync(kAll, of, 31);
         __syncthreads();
     }
     if (tid == 0) v[n] = carry;
@@ -659,10 +835,15 @@ __device__ __forceinline__ void place_pairs(const RouteArgs &a, int *counts, con
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, E = a.r.n_experts, k = a.r.top_k;
     for (int e = tid; e < E; e += blockDim.x) {
         int at = first[e];
-        for (int w = 0; w < warps; ++w) {
-            const int n = counts[w * E + e];
-            counts[w * E + e] = at;
-            at += n;
+        for (int w = 0; w < warps; w += 8) {
+            int n[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) n[i] = w + i < warps ? counts[(w + i) * E + e] : 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (w + i < warps) counts[(w + i) * E + e] = at;
+                at += n[i];
+            }
         }
     }
     __syncthreads();
@@ -710,6 +891,7 @@ __global__ void __launch_bounds__(NV <= 8 ? 1024 : 512) route_kernel(const __gri
     if (gridDim.x > 1) {
         for (int e = tid; e < E; e += blockDim.x) {
             int n = 0;
+#pragma unroll 8
             for (int w = 0; w < warps; ++w) n += counts[w * E + e];
             a.ws[(int64_t)blockIdx.x * E + e] = n;
         }
@@ -717,6 +899,7 @@ __global__ void __launch_bounds__(NV <= 8 ? 1024 : 512) route_kernel(const __gri
     }
     for (int e = tid; e < E; e += blockDim.x) {
         int n = 0;
+#pragma unroll 8
         for (int w = 0; w < warps; ++w) n += counts[w * E + e];
         first[e] = n;
     }
@@ -724,6 +907,37 @@ __global__ void __launch_bounds__(NV <= 8 ? 1024 : 512) route_kernel(const __gri
     block_scan(first, E, part);
     for (int e = tid; e <= E; e += blockDim.x) a.offsets[e] = first[e];
     place_pairs(a, counts, first, lo, hi);
+}
+
+// Several blocks, four tokens a warp: as route_kernel.
+template <int C>
+__global__ void __launch_bounds__(512) route_quads_kernel(const __grid_constant__ RouteArgs a) {
+    extern __shared__ int smem[];
+    __shared__ float4 bias[2 * C];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, E = 8 * C;
+    int *counts = smem, *mine = counts + warp * E;
+    int64_t lo, hi;
+    warp_tokens(a, blockIdx.x, gridDim.x, warp, lo, hi);
+    if (a.offsets)
+        for (int e = lane; e < E; e += 32) mine[e] = 0;
+    if (a.bias)
+        for (int e = tid; e < E; e += blockDim.x)
+            reinterpret_cast<float *>(bias)[((e % C) / 4 * 8 + e / C) * 4 + e % 4] = __ldg(a.bias + e);
+    __syncthreads();
+    for (int64_t t = lo; t < hi; t += 4) {
+        const int id = route_quad<C>(a, bias, t, hi, lane);
+        if (!a.offsets) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) count_row(a, mine, lane >> 3 == i ? id : -1, lane);
+    }
+    if (!a.offsets) return;
+    __syncthreads();
+    for (int e = tid; e < E; e += blockDim.x) {
+        int n = 0;
+#pragma unroll 8
+        for (int w = 0; w < warps; ++w) n += counts[w * E + e];
+        a.ws[(int64_t)blockIdx.x * E + e] = n;
+    }
 }
 
 __global__ void __launch_bounds__(1024) route_lists_kernel(const RouteArgs a) {
@@ -791,8 +1005,17 @@ cudaError_t launch_kernel(const RouteArgs &a, int blocks, int warps, cudaStream_
     route_kernel<NV, PACKED><<<blocks, 32 * warps, a.offsets ? smem_bytes(a.r.n_experts, warps) : 0, s>>>(a);
     return cudaGetLastError();
 }
+template <int C>
+cudaError_t launch_quads(const RouteArgs &a, int blocks, cudaStream_t s) {
+    static bool wide[64] = {};
+    const cudaError_t e = allow_smem(route_quads_kernel<C>, wide);
+    if (e != cudaSuccess) return e;
+    route_quads_kernel<C><<<blocks, 512, a.offsets ? smem_bytes(a.r.n_experts, 16) : 0, s>>>(a);
+    return cudaGetLastError();
+}
 template <int NV>
 cudaError_t launch_rows(const RouteArgs &a, int blocks, int warps, cudaStream_t s) {
+    if (NV >= 2 && NV <= 8 && quads_fit(a, blocks, 4 * NV)) return launch_quads<(NV >= 2 && NV <= 8 ? 4 * NV : 8)>(a, blocks, s);
     if (NV <= 8 && (a.bias || a.type != ENGRAM_T_F32)) return launch_kernel<NV, NV <= 8>(a, blocks, warps, s);
     return launch_kernel<NV, false>(a, blocks, warps, s);
 }

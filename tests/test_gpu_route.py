@@ -30,9 +30,9 @@ def _route(E, logits, bias, k, score="sigmoid", groups=1, top_groups=1, best=2, 
     return ids, w, offsets, pairs
 
 
-def _check(E, logits, bias, k, lists=True, **spec):
-    ids, w, offsets, pairs = _route(E, logits, bias, k, lists=lists, **spec)
-    want_ids, want_w = X.route(logits, bias, k, **spec)
+def _check(E, logits, bias, k, lists=True, times=1, **spec):
+    ids, w, offsets, pairs = _route(E, logits.repeat(times, 1) if times > 1 else logits, bias, k, lists=lists, **spec)
+    want_ids, want_w = (x.repeat(times, 1) for x in X.route(logits, bias, k, **spec))
     assert torch.equal(ids.cpu(), want_ids)
     got = w.double().cpu()
     assert torch.equal(torch.isnan(got), torch.isnan(want_w))
@@ -91,6 +91,55 @@ def test_scores_nearer_than_32_bits_tell(E, score):
         _check(E, logits, bias, 8, score=score, groups=8, top_groups=3)
     _check(E, logits, None, 8, score=score, groups=8, top_groups=3)
     _check(E, logits, None, 8, score=score)
+
+
+def _near(T, n, seed):
+    g = rng(seed)
+    base = torch.rand((T, 1), generator=g, device="cuda") * 4 + 2
+    return (base.view(torch.int32) + torch.randint(0, 40, (T, n), generator=g, device="cuda").int()).view(torch.float32)
+
+
+@pytest.mark.parametrize("T,n,k", [(9, 8, 8), (70, 8, 8), (50, 40, 9), (90, 64, 6), (90, 256, 8)])
+def test_near_scores_with_none_behind_the_last(E, T, n, k):
+    """As many experts as choices, or that many that are not masked: no score bounds the last choice from below."""
+    logits = _near(T, n, n)
+    if n > k:
+        keep = torch.rand((T, n), generator=rng(n + 1), device="cuda").argsort(1)[:, :k]
+        logits = torch.full_like(logits, -math.inf).scatter(1, keep, logits.gather(1, keep))
+    for score in ("sigmoid", "softmax"):
+        _check(E, logits, torch.full((n,), 0.25, device="cuda"), k, score=score)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n,groups", [(64, 1), (64, 8), (128, 4), (256, 1), (256, 2), (256, 8)])
+def test_four_tokens_a_warp(E, n, groups, dt):
+    """8, 16 and 32 experts a lane: random rows, near and equal scores, masked and non-finite ones, an odd number of
+    tokens, 62 times."""
+    T, g = 159, rng(n + groups)
+    logits = 2 * torch.randn((T, n), generator=g, device="cuda")
+    logits[40:80] = _near(40, n, 5)
+    logits[80:100] = torch.randint(-1, 2, (20, n), generator=g, device="cuda").float() * 0.5
+    logits[100:120][torch.rand((20, n), generator=g, device="cuda") < 0.9] = -math.inf
+    logits[120] = -math.inf
+    logits[121, 5], logits[122, 9], logits[123, 3] = math.nan, math.inf, -3e4
+    logits[124, : n // 2] = -math.inf
+    logits = logits.to(TYPES[dt][0])
+    biases = [0.2 * torch.randn(n, generator=g, device="cuda"), torch.randint(0, 2, (n,), generator=g, device="cuda") * 0.25]
+    for k, b in ((8, biases[0]), (3, biases[1]), (8, torch.zeros(n, device="cuda")), (6, None)):
+        for best in (1, 2):
+            _check(E, logits, b, k, times=62, groups=groups, top_groups=max(1, groups // 2), best=best, renorm=k != 3)
+
+
+@pytest.mark.parametrize("n", [48, 256])
+def test_group_sums_whose_parts_are_larger(E, n):
+    """Biases of +-1000: a group's two largest nearly cancel, and the sums' 32-bit errors are those of the parts."""
+    g = rng(n)
+    logits = 2 * torch.randn((90, n), generator=g, device="cuda")
+    size = n // 8
+    bias = torch.full((n,), -1000.0, device="cuda")
+    bias[::size] = 1000.0
+    for T, times in ((20, 1), (89, 1), (89, 111)):
+        _check(E, logits[:T], bias, 2, times=times, groups=8, top_groups=3)
 
 
 def test_masked_experts_and_rows(E):
