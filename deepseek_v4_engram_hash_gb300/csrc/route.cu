@@ -6,7 +6,7 @@
 // warp-wide maximum of integers, the lowest lane that has it by a vote, and a step of that lane's list.  The sort is of 32-bit words that hold
 // a key's upper 29 bits and its place, wherever that tells all that a choice needs.  Groups that are a power of two
 // of lanes (8 groups of 256 experts: four) find their two largest all at once by exchanges.  Scores are formed in 32 bits;
-// where two that a choice depends on lie closer than their error (kTol, about one row in a thousand of 256
+// where two that a choice depends on lie closer than their error (kTol, about one row in some hundreds of 256
 // sigmoid scores), those in question are formed again in 64 bits, one a lane (all of a row's took its warp 15 us).
 //
 // Lists: counts of a block's experts, then positions from the counts of the blocks
@@ -14,7 +14,8 @@
 // and a token's choices are different experts, so a counter an expert and warp needs no atomics and the lists
 // are in rising order.
 //
-// Bound by latency and instructions: one token is a chain of load, exponential and top_k + 1 maxima.
+// Bound by latency and instructions: one token is a chain of load, exponential and top_k + 1 maxima, 6.2 us; 16384 tokens of 256 experts in 8
+// groups, 8 choices, 34 us, of which the lists' kernel is 10 and the rare rows in 64 bits, whose warps are the last, about 5.
 #include "experts.cuh"
 
 #include <mutex>
@@ -518,7 +519,8 @@ __device__ __forceinline__ int route_row(const RouteArgs &a, const Shape &sh, co
     auto settle_groups = [&](uint32_t mine, float part) {
         kept = keep_groups(a, mine, lane);
         // (logits alone are ordered exactly)
-        if (!(exact && r.group_best == 1) && !sure_of_groups(mine, part, kept, lane)) all = (soft && a.bias) || !(kept = groups_again<NV>(a, row, lane, top, per_sum));
+        if ((exact && r.group_best == 1) || sure_of_groups(mine, part, kept, lane)) return;
+        all = (soft && a.bias) || !(kept = groups_again<NV>(a, row, lane, top, per_sum));
     };
     if (grouped && (!sh.lanes || NV > 8)) {
         uint32_t group[NV];
@@ -634,11 +636,12 @@ __device__ __noinline__ int row_again(const RouteArgs &a, int64_t row, int lane)
     load_row<NV>(a, NV, wide_rows<NV>(a), row, lane, l);
     return route_row<NV, true>(a, sh, bias, l, row, lane);
 }
-// Whether `a` has such rows, and enough of them, four a warp (16384 tokens, 256 experts: 23.7 us for 30.2, without lists; 4096: 20.4 for 16.1): 8 C experts, whole lanes a group, up to 8 choices, keys that may lose bits, aligned rows.
+// Whether `a` has such rows (8 C experts, whole lanes a group, up to 8 choices, keys that may lose bits, aligned) and enough of them, four
+// a warp: 16384 tokens of 256 experts, without lists, 23.7 us for 30.2; 4096 tokens 20.4 for 16.0.
 inline bool quads_fit(const RouteArgs &a, int blocks, int C) {
     const int size = a.type == ENGRAM_T_F32 ? 4 : 2;
-    return a.tokens >= 64 * blocks && blocks > 1 && a.r.n_experts == 8 * C && a.r.n_groups <= 8 && 8 % a.r.n_groups == 0 && a.r.top_k <= 8 && a.r.score == ENGRAM_SCORE_SIGMOID &&
-           (a.bias || a.type != ENGRAM_T_F32) && a.stride * size % 16 == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0;
+    return a.tokens >= 64 * blocks && blocks > 1 && a.r.n_experts == 8 * C && a.r.n_groups <= 8 && 8 % a.r.n_groups == 0 &&
+           a.r.top_k <= 8 && a.r.score == ENGRAM_SCORE_SIGMOID && (a.bias || a.type != ENGRAM_T_F32) && a.stride * size % 16 == 0 && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0;
 }
 // Tokens t .. t + 3 (before hi); bias: [C / 4][8 lanes][4] in shared memory.  A lane's choice: lane j of a token's eight, choice j.
 template <int C>
@@ -802,15 +805,13 @@ __device__ __forceinline__ void block_scan(int *v, int n, int *part) {
         }
         if (lane == 31) part[warp] = s;
         __syncthreads();
-        int of = lane < warps ? part[lane] : 0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(kAll, of, o);
-            if (lane >= o) of += y;
+        int before = carry, total = carry;
+        for (int w = 0; w < warps; ++w) {
+            if (w < warp) before += part[w];
+            total += part[w];
         }
-        const int before = carry + (warp ? __shfl_sync(kAll, of, warp - 1) : 0);
         if (i < n) v[i] = before + s - x;
-        carry += __shfl_sync(kAll, of, 31);
+        carry = total;
         __syncthreads();
     }
     if (tid == 0) v[n] = carry;
@@ -835,15 +836,10 @@ __device__ __forceinline__ void place_pairs(const RouteArgs &a, int *counts, con
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, E = a.r.n_experts, k = a.r.top_k;
     for (int e = tid; e < E; e += blockDim.x) {
         int at = first[e];
-        for (int w = 0; w < warps; w += 8) {
-            int n[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) n[i] = w + i < warps ? counts[(w + i) * E + e] : 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (w + i < warps) counts[(w + i) * E + e] = at;
-                at += n[i];
-            }
+        for (int w = 0; w < warps; ++w) {
+            const int n = counts[w * E + e];
+            counts[w * E + e] = at;
+            at += n;
         }
     }
     __syncthreads();
@@ -891,7 +887,6 @@ __global__ void __launch_bounds__(NV <= 8 ? 1024 : 512) route_kernel(const __gri
     if (gridDim.x > 1) {
         for (int e = tid; e < E; e += blockDim.x) {
             int n = 0;
-#pragma unroll 8
             for (int w = 0; w < warps; ++w) n += counts[w * E + e];
             a.ws[(int64_t)blockIdx.x * E + e] = n;
         }
@@ -899,7 +894,6 @@ __global__ void __launch_bounds__(NV <= 8 ? 1024 : 512) route_kernel(const __gri
     }
     for (int e = tid; e < E; e += blockDim.x) {
         int n = 0;
-#pragma unroll 8
         for (int w = 0; w < warps; ++w) n += counts[w * E + e];
         first[e] = n;
     }
@@ -934,7 +928,6 @@ __global__ void __launch_bounds__(512) route_quads_kernel(const __grid_constant_
     __syncthreads();
     for (int e = tid; e < E; e += blockDim.x) {
         int n = 0;
-#pragma unroll 8
         for (int w = 0; w < warps; ++w) n += counts[w * E + e];
         a.ws[(int64_t)blockIdx.x * E + e] = n;
     }
