@@ -22,7 +22,7 @@
 // Where there are fewer tiles than SMs a cluster shares a tile as in product.cu, K cut at groups of four blocks.
 // Waits are bounded as in product.cu.
 //
-// Bounds, measured: powers of two, 8192 rows, 4096 -> 6144: 134 us, 3.1 PFLOP/s; a block's 48 KB come from L2 at 64 bytes a clock and SM in
+// Bounds, measured: powers of two, 8192 rows, 4096 -> 6144: 132 us, 3.1 PFLOP/s; a block's 48 KB come from L2 at 64 bytes a clock and SM in
 // 750 clocks, its MMAs take 514, and in long runs power holds the clock at 1.7 GHz.  Other scales: about 1000 clocks a block, which the
 // last warps need for their eight loads of 64 clocks in turn and the hand-over: the same product 180 us; 4096 tokens, 8 of 64 experts, 4096 -> 2 x 1024
 // 325 us, and back 173.
