@@ -15,7 +15,7 @@
 // are in rising order.
 //
 // Bound by latency and instructions: one token is a chain of load, exponential and top_k + 1 maxima, 6.2 us; 16384 tokens of 256 experts in 8
-// groups, 8 choices, 34 us, of which the lists' kernel is 10 and the rare rows in 64 bits, whose warps are the last, about 5.
+// groups, 8 choices, 32 us, of which the lists' kernel is 10 and the rare rows in 64 bits, whose warps are the last, about 5.
 #include "experts.cuh"
 
 #include <mutex>
@@ -637,7 +637,7 @@ __device__ __noinline__ int row_again(const RouteArgs &a, int64_t row, int lane)
     return route_row<NV, true>(a, sh, bias, l, row, lane);
 }
 // Whether `a` has such rows (8 C experts, whole lanes a group, up to 8 choices, keys that may lose bits, aligned) and enough of them, four
-// a warp: 16384 tokens of 256 experts, without lists, 23.7 us for 30.2; 4096 tokens 20.4 for 16.0.
+// a warp: 16384 tokens of 256 experts, without lists, 21.2 us for 30.2; 4096 tokens some 4 more.
 inline bool quads_fit(const RouteArgs &a, int blocks, int C) {
     const int size = a.type == ENGRAM_T_F32 ? 4 : 2;
     return a.tokens >= 64 * blocks && blocks > 1 && a.r.n_experts == 8 * C && a.r.n_groups <= 8 && 8 % a.r.n_groups == 0 &&
@@ -735,10 +735,12 @@ __device__ __forceinline__ int route_quad(const RouteArgs &a, const float4 *bias
         } else if (sub == j && top) {
             id = e, mine = top;
         }
-        uint32_t next = 0;
+        if (j == k) break;
+        // the largest key below m: of the differences from m modulo 2^32 the largest, for they are larger for those below m (0 is one) than for others
+        uint32_t next = 0u - m;
 #pragma unroll
-        for (int v = 0; v < C; ++v) next = max(next, key[v] < m ? key[v] : 0u);
-        m = sub == first && top ? next : m;
+        for (int v = 0; v < C; v += 2) next = __vimax3_u32(next, key[v] - m, key[v + 1] - m);
+        m = sub == first && top ? m + next : m;
     }
     if (!exact) {
         const uint32_t down = __shfl_down_sync(kAll, mine, 1);
