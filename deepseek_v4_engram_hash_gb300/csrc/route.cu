@@ -621,8 +621,9 @@ __device__ __forceinline__ int route_row(const RouteArgs &a, const Shape &sh, co
 // ---- four tokens a warp ----
 // Eight lanes a token, C consecutive experts a lane: what takes all lanes' attention above (maxima, votes) is paid once for four tokens.
 // A key gives five bits to its place, so more rows than above are in doubt; those are formed again as above.
-// Two scores of which x is the larger are told apart by this: 8e-7 max(1, |x|) (see kTol), and C units of its last place.  Half of it
-// bounds the error of a value in the middle of those that its key may stand for.
+// Two scores, x the one of the larger size, are told apart by this: 8e-7 max(1, |x|) (see kTol), and C units of its last place (keys lose their
+// last bits towards minus infinity, so of two negative ones the smaller's unit counts, which may be twice the other's).  Half of it bounds the
+// error of a value in the middle of those that its key may stand for.
 template <int C>
 __device__ __forceinline__ float quad_tol(float x) {
     return fmaf(__uint_as_float(__float_as_uint(x) & 0x7F800000u), C * 0x1p-23f, 1e-6f * fmaxf(1.f, fabsf(x)));
@@ -748,7 +749,7 @@ __device__ __forceinline__ int route_quad(const RouteArgs &a, const float4 *bias
         if (sub != k - 1) after = down, behind = other;
         if (sub < k && mine && after) {
             const float x = of_key(mine), y = of_key(after);
-            if (x - y <= quad_tol<C>(x))
+            if (x - y <= quad_tol<C>(fmaxf(fabsf(x), fabsf(y))))
                 doubt |= !(load_logit(a, row * a.stride + id) == load_logit(a, row * a.stride + behind) && a.bias[id] == a.bias[behind]);
         }
     }
