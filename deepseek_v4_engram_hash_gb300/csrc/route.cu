@@ -157,43 +157,53 @@ __device__ __forceinline__ void mask_groups(const Shape &sh, unsigned kept, int 
         if (!(kept >> min(31, (lane * sh.c + v) / sh.size) & 1)) key[v] = 0;
 }
 
+// Whether two experts' scores are formed of the same numbers.
+__device__ __forceinline__ bool same_numbers(const RouteArgs &a, int64_t row, int e, int f) {
+    return load_logit(a, row * a.stride + e) == load_logit(a, row * a.stride + f) && a.bias[e] == a.bias[f];
+}
+
 // The top_k of the keys of which a lane's largest that is left is `m`, of its expert `at`; next(): the lane takes it out.  Lane j gets
-// id j (-1: none).  CHECK: false where 32 bits leave a doubt about the order of two choices, or of the last and `least`, the key
-// behind it -- not where two are equal for being formed of the same numbers.
+// id j (-1: none).  CHECK: false where 32 bits leave a doubt about the order of two choices, or of the last and any that is left (`least`: the
+// largest of those) -- not where two are equal for being formed of the same numbers.
 template <bool CHECK, class Key, class Next>
 __device__ __forceinline__ bool choose(const RouteArgs &a, const Shape &sh, int64_t row, Key &m, int &at, Next next, bool exact,
                                        int lane, int &id, Key &least) {
     const int k = a.r.top_k;
     id = -1;
-    Key mine = 0;
-    int behind = -1;
+    Key mine = 0, last = 0;
+    int last_id = 0;
     least = 0;
     for (int j = 0;; ++j) {
         const Key top = warp_max(m);
         if (!top) break;
+        if (j == k) {
+            least = top;
+            break;
+        }
         const bool from = m == top;
         const unsigned who = __ballot_sync(kAll, from);
         const int first = __ffs(who) - 1;                // lower lanes hold lower experts
-        const int e = __shfl_sync(kAll, lane * sh.c + at, first);
-        if (j == k) {
-            least = top;
-            behind = e;
-            break;
-        }
-        id = lane == j ? e : id;
+        last = top;
+        last_id = __shfl_sync(kAll, lane * sh.c + at, first);
+        id = lane == j ? last_id : id;
         mine = lane == j ? top : mine;
         next(lane == first);
     }
     if (!CHECK || exact) return true;
-    Key after = __shfl_down_sync(kAll, mine, 1);
-    int other = __shfl_down_sync(kAll, id, 1);
-    after = lane == k - 1 ? least : after;
-    other = lane == k - 1 ? behind : other;
+    const Key after = __shfl_down_sync(kAll, mine, 1);
+    const int other = __shfl_down_sync(kAll, id, 1);
     bool doubt = false;
-    if (lane < k && mine && after) {
+    if (lane < k - 1 && mine && after) {
         const float x = (float)of_key(mine), y = (float)of_key(after);
-        doubt = x - y <= kTol * fmaxf(1.f, fabsf(x));
-        if (doubt) doubt = !(load_logit(a, row * a.stride + id) == load_logit(a, row * a.stride + other) && a.bias[id] == a.bias[other]);
+        doubt = x - y <= kTol * fmaxf(1.f, fabsf(x)) && !same_numbers(a, row, id, other);
+    }
+    // Behind the last choice the key that stands first may be of the same numbers, and another behind that of larger ones.
+    const float x = (float)of_key(last);
+    const Key from = key_of(x - kTol * fmaxf(1.f, fabsf(x)));
+    while (__any_sync(kAll, m >= from)) {
+        const bool near = m >= from;
+        if (near) doubt |= !same_numbers(a, row, last_id, lane * sh.c + at);
+        next(near);
     }
     return !__any_sync(kAll, doubt);
 }
@@ -721,8 +731,16 @@ __device__ __forceinline__ int route_quad(const RouteArgs &a, const float4 *bias
         m = kept ? m : 0u;
         groups = __ballot_sync(kAll, kept) >> (8 * seg) & 0xFF;
     }
-    int id = -1, behind = -1;
-    uint32_t mine = 0, after = 0, least = 0;
+    // from m to the largest key below it: of the differences from m modulo 2^32 the largest, for they are larger for those below m (0 is one)
+    // than for others
+    auto next_key = [&](uint32_t m) {
+        uint32_t next = 0u - m;
+#pragma unroll
+        for (int v = 0; v < C; v += 2) next = __vimax3_u32(next, key[v] - m, key[v + 1] - m);
+        return next;
+    };
+    int id = -1;
+    uint32_t mine = 0, least = 0;
 #pragma unroll 1
     for (int j = 0; j <= k; ++j) {
         const uint32_t x = m & ~kPlace;
@@ -732,25 +750,30 @@ __device__ __forceinline__ int route_quad(const RouteArgs &a, const float4 *bias
         const int first = __ffs(__ballot_sync(kAll, x == top) >> (8 * seg) & 0xFF) - 1;   // lower lanes hold lower experts
         const int e = __shfl_sync(kAll, sub * C + (int)(kPlace - (m & kPlace)), 8 * seg + first);
         if (j == k) {
-            behind = e, after = least = top;
+            least = top;
         } else if (sub == j && top) {
             id = e, mine = top;
         }
         if (j == k) break;
-        // the largest key below m: of the differences from m modulo 2^32 the largest, for they are larger for those below m (0 is one) than for others
-        uint32_t next = 0u - m;
-#pragma unroll
-        for (int v = 0; v < C; v += 2) next = __vimax3_u32(next, key[v] - m, key[v + 1] - m);
+        const uint32_t next = next_key(m);
         m = sub == first && top ? m + next : m;
     }
-    if (!exact) {
-        const uint32_t down = __shfl_down_sync(kAll, mine, 1);
+    if (!exact) {                                    // as in choose()
+        const uint32_t after = __shfl_down_sync(kAll, mine, 1);
         const int other = __shfl_down_sync(kAll, id, 1);
-        if (sub != k - 1) after = down, behind = other;
-        if (sub < k && mine && after) {
+        if (sub < k - 1 && mine && after) {
             const float x = of_key(mine), y = of_key(after);
-            if (x - y <= quad_tol<C>(fmaxf(fabsf(x), fabsf(y))))
-                doubt |= !(load_logit(a, row * a.stride + id) == load_logit(a, row * a.stride + behind) && a.bias[id] == a.bias[behind]);
+            doubt = x - y <= quad_tol<C>(fmaxf(fabsf(x), fabsf(y))) && !same_numbers(a, row, id, other);
+        }
+        const uint32_t last = __shfl_sync(kAll, mine, 8 * seg + k - 1);
+        const float x = of_key(last);                // (of those that are near enough none is of a larger size than the inner sum)
+        const uint32_t from = last ? key_of(x - quad_tol<C>(fabsf(x) + quad_tol<C>(x))) : 0xFFFFFFFFu;
+        while (__any_sync(kAll, m >= from)) {
+            const int last_id = __shfl_sync(kAll, id, 8 * seg + k - 1);
+            if (m >= from) {
+                doubt |= !same_numbers(a, row, last_id, sub * C + (int)(kPlace - (m & kPlace)));
+                m += next_key(m);
+            }
         }
     }
     const bool real = t + seg < hi;
