@@ -29,10 +29,18 @@ constexpr int kBlocks = 152;                         // blocks at most of the ot
 constexpr unsigned kAll = 0xFFFFFFFFu;
 // A 32-bit score that orders experts is within 4e-7 max(1, |c|) of the 64-bit one.  e = 2^(-l log2 e) is off by 2^-22 + 2^-23 |l| of itself, which
 // moves s = 1 / (1 + e) by s (1 - s) of that, under 2^-23; 1 + e and the reciprocal (1 ulp) by 2^-24 + 2^-23 of s; the sum with the
-// bias by 2^-24 |c|.  Softmax: e^(l - max) by 2^-22 + 2^-22 |l - max| of itself, under 2^-22 after all, and as much for the divisor.
-// Two of them differ by twice that, 8e-7, and where keys lose their last three bits, all to the same side, by 7 2^-23 |c| = 8.4e-7 more: 1.7e-6.
-// Sums of two by twice as much.
+// bias by 2^-24 |c|.  Two of them differ by twice that, 8e-7, and where keys lose their last three bits, all to the same side, by 7 2^-23 |c| =
+// 8.4e-7 more: 1.7e-6.  Sums of two by twice as much.
 constexpr float kTol = 2e-6f;
+// The same for rows of NV experts a lane.  Softmax beside a bias, in units of u = 2^-24: of two p = e^(l - max) / sum, which are together at most 1, the
+// exponentials, the differences' rounding and the products are off by 6 u in all; of the divisor, by which the two move apart by at most its own
+// error, the terms by 4 u and by |l - max| u each, under 5 u of 1024 terms together, the sum by NV - 1 additions in a lane and 5
+// exchanges, u each, and the reciprocal by u; the sums with the biases by u max(1, |c|) each: NV + 22 in all, and 14 for the keys' lost bits where
+// NV is at most 8.  kTol is 33 of them.  (Without a bias the divisor is common to all that is compared.)
+template <int NV>
+__device__ __forceinline__ float tol_of(const RouteArgs &a) {
+    return a.bias && a.r.score == ENGRAM_SCORE_SOFTMAX ? kTol + (NV + 4) * 0x1p-24f : kTol;
+}
 
 // Warps a block: 32 with 64 registers; rows of many experts take 16 with 128.
 int route_warps(int n_experts) { return n_experts <= 256 ? 32 : 16; }
@@ -144,8 +152,8 @@ __device__ __forceinline__ unsigned keep_groups(const RouteArgs &a, Key mine, in
     return kept;
 }
 // Whether 32 bits tell that the groups `kept` are those: the least that any of them can be is above the most that any other can.
-__device__ __forceinline__ bool sure_of_groups(uint32_t mine, float part, unsigned kept, int lane) {
-    const float x = of_key(mine), err = 2 * kTol * fmaxf(1.f, part);
+__device__ __forceinline__ bool sure_of_groups(uint32_t mine, float part, unsigned kept, float tol, int lane) {
+    const float x = of_key(mine), err = 2 * tol * fmaxf(1.f, part);
     const bool in = kept >> lane & 1;
     const uint32_t most = __reduce_max_sync(kAll, mine && !in ? key_of(x + err) : 0u);
     return !most || __reduce_min_sync(kAll, mine && in ? key_of(x - err) : 0xFFFFFFFFu) > most;
@@ -167,7 +175,7 @@ __device__ __forceinline__ bool same_numbers(const RouteArgs &a, int64_t row, in
 // largest of those) -- not where two are equal for being formed of the same numbers.
 template <bool CHECK, class Key, class Next>
 __device__ __forceinline__ bool choose(const RouteArgs &a, const Shape &sh, int64_t row, Key &m, int &at, Next next, bool exact,
-                                       int lane, int &id, Key &least) {
+                                       float tol, int lane, int &id, Key &least) {
     const int k = a.r.top_k;
     id = -1;
     Key mine = 0, last = 0;
@@ -195,11 +203,11 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const Shape &sh, int6
     bool doubt = false;
     if (lane < k - 1 && mine && after) {
         const float x = (float)of_key(mine), y = (float)of_key(after);
-        doubt = x - y <= kTol * fmaxf(1.f, fabsf(x)) && !same_numbers(a, row, id, other);
+        doubt = x - y <= tol * fmaxf(1.f, fabsf(x)) && !same_numbers(a, row, id, other);
     }
     // Behind the last choice the key that stands first may be of the same numbers, and another behind that of larger ones.
     const float x = (float)of_key(last);
-    const Key from = key_of(x - kTol * fmaxf(1.f, fabsf(x)));
+    const Key from = key_of(x - tol * fmaxf(1.f, fabsf(x)));
     while (__any_sync(kAll, m >= from)) {
         const bool near = m >= from;
         if (near) doubt |= !same_numbers(a, row, last_id, lane * sh.c + at);
@@ -227,7 +235,7 @@ __device__ __forceinline__ bool choose_of(const RouteArgs &a, const Shape &sh, i
 #pragma unroll
     for (int v = 0; v < NV; ++v)
         if (key[v] > m) m = key[v], at = v;
-    return choose<CHECK>(a, sh, row, m, at, next, exact, lane, id, least);
+    return choose<CHECK>(a, sh, row, m, at, next, exact, tol_of<NV>(a), lane, id, least);
 }
 
 // Up to 32 experts, marked in `want` bit by bit of a lane, to one a lane in rising order; -1 behind the last.  False: more.
@@ -529,7 +537,7 @@ __device__ __forceinline__ int route_row(const RouteArgs &a, const Shape &sh, co
     auto settle_groups = [&](uint32_t mine, float part) {
         kept = keep_groups(a, mine, lane);
         // (logits alone are ordered exactly)
-        if ((exact && r.group_best == 1) || sure_of_groups(mine, part, kept, lane)) return;
+        if ((exact && r.group_best == 1) || sure_of_groups(mine, part, kept, tol_of<NV>(a), lane)) return;
         all = (soft && a.bias) || !(kept = groups_again<NV>(a, row, lane, top, per_sum));
     };
     if (grouped && (!sh.lanes || NV > 8)) {
@@ -570,7 +578,7 @@ __device__ __forceinline__ int route_row(const RouteArgs &a, const Shape &sh, co
             m = s[0] & ~kPlace;
             at = kPlace - (s[0] & kPlace);
         };
-        chosen = choose<true>(a, sh, row, m, at, next, exact, lane, id, least);
+        chosen = choose<true>(a, sh, row, m, at, next, exact, tol_of<NV>(a), lane, id, least);
     } else if (NV <= 8) {
         uint64_t s[NV];
 #pragma unroll
@@ -603,7 +611,7 @@ __device__ __forceinline__ int route_row(const RouteArgs &a, const Shape &sh, co
             m = key[0];
             at = order & 15;
         };
-        chosen = choose<true>(a, sh, row, m, at, next, exact, lane, id, least);
+        chosen = choose<true>(a, sh, row, m, at, next, exact, tol_of<NV>(a), lane, id, least);
     } else {
         chosen = choose_of<true>(a, sh, row, key, exact, lane, id, least);
     }

@@ -81,3 +81,23 @@ def test_equal_numbers_alone(E):
         for dt in ("f32", "bf16"):
             _check(E, logits.to(TYPES[dt][0]), torch.full((256,), 0.5, device="cuda"), 8, times=times)
             _check(E, logits.to(TYPES[dt][0]), torch.full((256,), 0.5, device="cuda"), 4, times=times, groups=8, top_groups=4)
+
+
+@pytest.mark.parametrize("T", [1, 100])
+def test_a_softmax_whose_sum_loses_its_small_terms(E, T):
+    """1024 experts, one of e^0 and the others each too small for the sum where they come to it (36 x 2^-24 in all): the 32-bit score of the
+    first is 2.1e-6 too large, and a rival by its bias lies between."""
+    t = 2.0 ** -24 * 0.999
+    logits = torch.empty((32, 32), dtype=torch.float64)
+    logits[0] = math.log(t)
+    lane = torch.arange(32)
+    for mine in (lane == 16, lane % 16 == 8, lane % 8 == 4, lane % 4 == 2, lane % 2 == 1):
+        logits[mine] = math.log(t / 32 / int(mine.sum()))
+    logits[0, 0] = 0
+    rows = logits.flatten().float().cuda().expand(T, 1024).contiguous()
+    for rival in (5, 700):
+        for step in range(12):
+            bias = torch.full((1024,), -1.0, device="cuda")
+            bias[0] = -0.5
+            bias[rival] = torch.tensor(0.49999775).view(torch.int32).add(step).view(torch.float32)
+            _check(E, rows, bias, 2, score="softmax")
