@@ -206,7 +206,10 @@ __device__ __forceinline__ float scale_at(const uint4 &r, int fmt, bool vec, int
 
 
 // The experts' rows (global memory: after griddep_wait) and how many tiles of up to `rows` rows come before each: shared memory, by all threads.
+// An expert counts only if its offsets rise from where those before it that count have ended: their rows are at most n_pairs in all, and
+// their tiles at most product_row_tiles(), for which the grid of clusters is made.
 __device__ __forceinline__ void set_lists(const ProductArgs &a, int *first, int *count, int *before, int rows, int threads) {
+    int bad = 0;
     for (int e = threadIdx.x; e < a.E; e += threads) {
         int lo = 0, n = a.n_pairs;
         if (a.offsets) {
@@ -216,12 +219,28 @@ __device__ __forceinline__ void set_lists(const ProductArgs &a, int *first, int 
             if (lo < 0 || hi < lo || hi > a.n_pairs) {
                 set_err(a.err, ENGRAM_E_LENGTH);
                 lo = n = 0;
+                bad = 1;
             }
         }
         first[e] = lo;
         count[e] = n;
     }
-    __syncthreads();
+    // offsets that rise everywhere need no more than that
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0) {
+            int end = 0;
+            for (int e = 0; e < a.E; ++e) {
+                if (!count[e]) continue;
+                if (first[e] < end) {
+                    set_err(a.err, ENGRAM_E_LENGTH);
+                    first[e] = count[e] = 0;
+                } else {
+                    end = first[e] + count[e];
+                }
+            }
+        }
+        __syncthreads();
+    }
     if (threadIdx.x >= 32) return;
     const int lane = threadIdx.x;
     int carry = 0;

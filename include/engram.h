@@ -501,8 +501,8 @@ typedef struct {
  * pairs[offsets[e + 1] - 1], in rising order.  offsets [n_experts + 1], pairs
  * [tokens * top_k] (those behind offsets[n_experts] have no meaning).  Device
  * arrays, 4-byte aligned; the products read them when their kernels run.  An
- * expert whose offsets fall or leave 0 .. tokens * top_k raises ENGRAM_E_LENGTH and
- * counts as one without pairs; a pair outside 0 .. tokens * top_k - 1 raises
+ * expert whose offsets fall, leave 0 .. tokens * top_k or begin before the end of an earlier
+ * one that counts raises ENGRAM_E_LENGTH and counts as one without pairs; a pair outside 0 .. tokens * top_k - 1 raises
  * ENGRAM_E_ROW. */
 typedef struct {
     int32_t *offsets, *pairs;
