@@ -594,7 +594,8 @@ __global__ void __launch_bounds__(threads_of(MX, GATHER), 1) product_rows_kernel
             }
             }
             ++turn;
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            ok = __all_sync(0xFFFFFFFFu, ok) != 0;   // a warp's lanes leave together: what follows meets at barriers
+            if (!ok) break;
             if (p.split > 1) {
                 // this part's sums as [column][row]; the ring they overwrite is drained: a cluster has one tile
                 float *part = reinterpret_cast<float *>(smem) + row;
