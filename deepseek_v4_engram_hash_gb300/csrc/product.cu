@@ -11,7 +11,7 @@
 //
 // Bound by the weights on their way from DRAM (five stages of 32 KB a CTA): 64 tokens, 8 of 256 experts, 4096 -> 2 x 2048:
 // 403 us for 2.87 GB; the second product 212 us for 1.44 GB: the measured copy rate.  One token's eight experts, 134 MB, take 28 us (0.70 of it:
-// 128 tiles on 152 SMs, 4 us of start and end); 4096 -> 6144 for one token, 25 MB, 9.5 us: 4.3 us is what one block of a
+// 4 us are start and end; what holds the rest under the copy rate is not known); 4096 -> 6144 for one token, 25 MB, 9.5 us: 4.3 us is what one block of a
 // single CTA takes, 2.2 more the exchange in a cluster.
 //
 // Roles (12 warps):

@@ -6,16 +6,18 @@
 // warp-wide maximum of integers, the lowest lane that has it by a vote, and a step of that lane's list.  The sort is of 32-bit words that hold
 // a key's upper 29 bits and its place, wherever that tells all that a choice needs.  Groups that are a power of two
 // of lanes (8 groups of 256 experts: four) find their two largest all at once by exchanges.  Scores are formed in 32 bits;
-// where two that a choice depends on lie closer than their error (kTol, about one row in some hundreds of 256
-// sigmoid scores), those in question are formed again in 64 bits, one a lane (all of a row's took its warp 15 us).
+// where two that a choice depends on lie closer than their error (tol_of, about one row in some hundreds of 256
+// sigmoid scores), those in question are formed again in 64 bits, one a lane (all of a row's took its warp 15 us: so for softmax beside a bias).
 //
 // Lists: counts of a block's experts, then positions from the counts of the blocks
 // before it (two kernels; one where a block takes all tokens).  A warp's tokens are consecutive and walked in order,
 // and a token's choices are different experts, so a counter an expert and warp needs no atomics and the lists
-// are in rising order.
+// are in rising order.  Each block of the second kernel reads all blocks' counts (155 KB of 152 x 256, 24 MB from L2 in all) and counts its own
+// tokens again before it places them: a third of a long prompt's time.
 //
-// Bound by latency and instructions: one token is a chain of load, exponential and top_k + 1 maxima, 6.2 us; 16384 tokens of 256 experts in 8
-// groups, 8 choices, 32 us, of which the lists' kernel is 10 and the rare rows in 64 bits, whose warps are the last, about 5.
+// Bound by latency and instructions: one token is a chain of load, exponential and top_k + 1 maxima, 6.0 us; 4096 tokens of 256 experts in 8
+// groups, 8 choices, 24 us; 16384 of them 32 us, of which the lists' kernel is 10 and the rare rows in 64 bits, whose warps are the last, about 5 (up to
+// 39 us with inputs of which more rows are in doubt).
 #include "experts.cuh"
 
 #include <mutex>
@@ -77,10 +79,6 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t k) {
     const uint32_t lo = __reduce_max_sync(kAll, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
     return (uint64_t)hi << 32 | lo;
 }
-
-template <class Key> struct Real;
-template <> struct Real<uint32_t> { using type = float; };
-template <> struct Real<uint64_t> { using type = double; };
 
 // How lanes hold a row's experts, and groups their lanes.
 struct Shape {
@@ -655,8 +653,8 @@ __device__ __noinline__ int row_again(const RouteArgs &a, int64_t row, int lane)
     load_row<NV>(a, NV, wide_rows<NV>(a), row, lane, l);
     return route_row<NV, true>(a, sh, bias, l, row, lane);
 }
-// Whether `a` has such rows (8 C experts, whole lanes a group, up to 8 choices, keys that may lose bits, aligned) and enough of them, four
-// a warp: 16384 tokens of 256 experts, without lists, 21.2 us for 30.2; 4096 tokens some 4 more.
+// Whether `a` has such rows (64, 128 or 256 experts, sigmoid, groups of whole lanes, up to 8 choices, keys that may lose bits, aligned) and enough of
+// them, four a warp in all blocks: 16384 tokens of 256 experts, without lists, 21.2 us for 30.2; 4096 tokens some 4 more.
 inline bool quads_fit(const RouteArgs &a, int blocks, int C) {
     const int size = a.type == ENGRAM_T_F32 ? 4 : 2;
     return a.tokens >= 64 * blocks && blocks > 1 && a.r.n_experts == 8 * C && a.r.n_groups <= 8 && 8 % a.r.n_groups == 0 &&

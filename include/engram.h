@@ -517,7 +517,7 @@ typedef struct {
  *     bias is NULL) have the largest sums;
  *   the choices are the top_k experts of those groups with the largest c, in
  *     falling order; of equal ones (experts or groups) the lower index;
- *   weight_j = scale * s_j, divided by sum_j s_j + 1e-20 if renormalise.
+ *   weight_j = scale * s_j, divided by sum_j s_j + 1e-20 if renormalise (in f32; an s under 2^-126 may count as 0 there).
  * Choices are those of 64-bit scores: where 32-bit ones are too near to tell, the
  * row's are formed again in 64 bits.  An expert whose logit is -inf is masked: it
  * is never chosen and adds nothing to a softmax or a group (a group of masked experts
@@ -551,7 +551,9 @@ typedef struct {
 
 /* out = x W^T of e4m3 rows: row r is
  *   out[r, n] = sum_b (sx[r, b] sw[n / 128, b]) sum_{128 b <= k < 128 (b + 1)} x[r, k] W[n, k],
- * products of codes exact, sums and scales in f32, rounded once to out_type.
+ * products of codes exact, sums and scales in f32, rounded once to out_type.  (Sums on the tensor cores cut off what lies under an
+ * accumulator's last bit: over 128 values at a time, or, where both scales are e8m0 and there are more than 24 rows (an expert, on
+ * average), over all of k, which grows with k if the products have one sign: 65536 of them are off by up to 9e-6 of their sum, 4096 by 1e-7.)
  *   d_x [rows, k] codes, rows x_stride bytes apart (0 = k; a multiple of 16), 16-byte
  *   aligned; d_x_scales [rows, ceil(k / 128)] dense, x_fmt ENGRAM_FMT_FP8 (f32) or
  *   ENGRAM_FMT_FP8_E8M0: what engram_residual_norm and engram_glu_fp8 write with blocks of 128;
@@ -571,8 +573,8 @@ int engram_project_fp8(const uint8_t *d_x, int64_t x_stride, const void *d_x_sca
  * scale for each block of 128 of a row (8-bit blocks, above), d_out_scales [..,
  * ceil(n / 128)], out_fmt ENGRAM_FMT_FP8 (f32) or ENGRAM_FMT_FP8_E8M0 (bytes).
  * lists NULL: output row r from x row r.  Otherwise rows == lists->tokens, and
- * output row p is that of pair pairs[p]: x row pairs[p] / top_k, expert p's matrices; rows behind
- * offsets[n_experts] are not written.  x: as above (gathered: under 2^36 bytes, else
+ * output row p is that of pair pairs[p]: x row pairs[p] / top_k, the matrices of the expert whose
+ * list p lies in; rows behind offsets[n_experts] are not written.  x: as above (gathered: under 2^36 bytes, else
  * ENGRAM_E_UNSUPPORTED).  limit: 0 (none) or finite and > 0. */
 int engram_glu_fp8(const uint8_t *d_x, int64_t x_stride, const void *d_x_scales, int32_t x_fmt, int32_t rows,
                    const engram_fp8_weight *w, const engram_expert_lists *lists, float limit, int32_t out_fmt,
